@@ -371,6 +371,65 @@ int spec_verify_adapt(const spec_verify_adapt_args* args, void* hip_stream);
 /* sizeof(spec_verify_adapt_args) as compiled into the library. */
 int64_t spec_verify_adapt_args_size(void);
 
+/* ---- log probabilities of given tokens -------------------------------------
+ * For each of `rows` rows of logits (a verify call's target rows, for
+ * instance: its emitted_tokens has one entry per target row, so the two go
+ * together as they are) and one token per row:
+ *   logprob  log softmax(x / T)[token], natural logarithm
+ *   entropy  -sum p log p of softmax(x / T), in nats
+ *   rank     1 + the number of logits strictly above the token's
+ *   top_*    the `top` largest logits' tokens, best first (the lower index
+ *            first on ties), and their log probabilities
+ * A row whose token is negative (the -1 behind a round's emitted tokens) is
+ * not read: logprob 0, entropy 0, rank 0, top tokens -1 with -inf.  With
+ * tokens == NULL every row is read, for entropy and top alone.
+ * All pointers are device pointers owned by the caller.
+ *   logits         [rows][ld], SV_F32 or SV_BF16, ld >= vocab, aligned to
+ *                  the element size; columns >= vocab are never read
+ *   tokens         [rows] int32 or NULL (then logprob and rank are NULL too)
+ *   temperature    [rows] float or NULL (= 1.0)
+ *   top            0 .. SV_LOGPROBS_MAX_TOP, at most vocab
+ *   logprob, entropy, rank, top_logprobs, status   each may be NULL
+ *   top_tokens     [rows * top] int32, required for top > 0
+ *   status         SV_ST_BAD_TOKEN (token >= vocab), SV_ST_BAD_TEMPERATURE
+ *                  (as for a verify call) or SV_ST_NONFINITE (the row holds
+ *                  NaN or +inf, or is entirely -inf): the row's values are
+ *                  then NaN, its rank 0 and its top tokens -1
+ *   workspace      16-byte aligned, at least
+ *                  spec_verify_logprobs_workspace(...) bytes; its contents
+ *                  need not survive the call, and calls that may overlap
+ *                  each need their own
+ * Sums are float32 in a fixed order: repeated calls are bitwise identical.
+ * Enqueues two kernels on `hip_stream`, which belongs to the calling
+ * thread's current device; allocates nothing, does not synchronise.
+ * SV_ERR_INVALID: nothing was enqueued.  rows == 0 is a no-op. */
+#define SV_LOGPROBS_MAX_TOP 64
+typedef struct spec_verify_logprobs_args {
+  int64_t rows;
+  int64_t vocab;               /* 1 .. 2097152 */
+  int32_t dtype;
+  int32_t top;
+  const void* logits;
+  int64_t ld;
+  const int32_t* tokens;
+  const float* temperature;
+  float* logprob;
+  float* entropy;
+  int32_t* rank;
+  int32_t* top_tokens;
+  float* top_logprobs;
+  int32_t* status;
+  void* workspace;
+  int64_t workspace_bytes;
+} spec_verify_logprobs_args;
+int spec_verify_token_logprobs(const spec_verify_logprobs_args* args, void* hip_stream);
+
+/* Bytes of workspace for these sizes, or SV_ERR_INVALID. */
+int64_t spec_verify_logprobs_workspace(int64_t rows, int64_t vocab, int32_t dtype, int32_t top);
+
+/* sizeof(spec_verify_logprobs_args) as compiled into the library. */
+int64_t spec_verify_logprobs_args_size(void);
+
 /* Library version string. */
 const char* spec_verify_version(void);
 

@@ -27,7 +27,7 @@ from ._lib import (  # noqa: F401
 )
 
 __all__ = ["Verifier", "VerifyError", "verify", "propose_ngram", "NgramProposer", "AcceptanceStats",
-           "DraftLengthController", "LibraryMissing", "KERNEL_NAMES"]
+           "DraftLengthController", "token_logprobs", "LibraryMissing", "KERNEL_NAMES"]
 
 
 class VerifyError(RuntimeError):
@@ -388,6 +388,69 @@ class DraftLengthController:
         st = stream if stream is not None else torch.cuda.current_stream()
         _check(self._lib.spec_verify_adapt(ctypes.byref(self._args), ctypes.c_void_p(st.cuda_stream)))
         return self.next_k
+
+
+def _on_stream(dev, stream):
+    """The stream a call queues on, as a context in which it is torch's
+    current one (so that what the call allocates belongs to it) and its
+    device the current device."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab: Optional[int] = None,
+                   want_entropy: bool = True, want_rank: bool = True, want_status: bool = True, stream=None) -> dict:
+    """Log probabilities of one given token per row of ``logits`` ([rows, >=
+    vocab], float32 or bfloat16, unit column stride), with entropy, rank and
+    the ``top`` best alternatives (spec_verify_token_logprobs).
+
+    ``tokens`` is int32 [rows]; a negative token leaves its row out, so a
+    verify call's ``emitted`` goes with its ``target`` as they are.  Without
+    ``tokens`` every row is read, for entropy and alternatives alone.
+    ``temperature`` is float32 [rows].  Returns ``logprob``, ``entropy``
+    (float32 [rows]), ``rank`` (int32 [rows], 1 for the largest logit),
+    ``top_tokens`` (int32 [rows, top]), ``top_logprobs`` (float32 [rows,
+    top]) and ``status`` (int32 [rows]); what was not asked for is None,
+    except the empty [rows, 0] alternatives of ``top`` = 0."""
+    import torch
+    lib = _lib.load()
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-D with unit column stride")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    dev = logits.device
+    R, V = int(logits.shape[0]), int(logits.shape[1]) if vocab is None else int(vocab)
+    if V < 1 or V > logits.shape[1]:
+        raise ValueError(f"vocab {V} outside 1..{logits.shape[1]} columns")
+    dtype = _logits_dtype(logits, torch)
+    _need(tokens, "tokens", (torch.int32,), torch, R, dev)
+    _need(temperature, "temperature", (torch.float32,), torch, R, dev)
+    top = int(top)
+    nbytes = lib.spec_verify_logprobs_workspace(R, V, dtype, top)
+    if nbytes < 0:
+        _check(int(nbytes))
+    with _on_stream(dev, stream):
+        f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
+        out = {
+            "logprob": torch.empty(R, **f32) if tokens is not None else None,
+            "entropy": torch.empty(R, **f32) if want_entropy else None,
+            "rank": torch.empty(R, **i32) if want_rank and tokens is not None else None,
+            "top_tokens": torch.empty((R, top), **i32),
+            "top_logprobs": torch.empty((R, top), **f32),
+            "status": torch.empty(R, **i32) if want_status else None,
+        }
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        a = _lib.SpecVerifyLogprobsArgs(
+            R, V, dtype, top, logits.data_ptr(), logits.stride(0) if R > 1 else logits.shape[1], _ptr(tokens),
+            _ptr(temperature), _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out["rank"]),
+            out["top_tokens"].data_ptr() if top else None, out["top_logprobs"].data_ptr() if top else None,
+            _ptr(out["status"]), ws.data_ptr(), nbytes)
+        _check(lib.spec_verify_token_logprobs(ctypes.byref(a), torch.cuda.current_stream(dev).cuda_stream))
+    return out
 
 
 def library_loaded_path() -> str:

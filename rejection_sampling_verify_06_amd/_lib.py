@@ -48,7 +48,9 @@ EXPORTED = (
     "spec_verify_args_size", "spec_verify_ngram_propose", "spec_verify_ngram_args_size",
     "spec_verify_stats_accumulate", "spec_verify_stats_summary", "spec_verify_adapt_reset", "spec_verify_adapt",
     "spec_verify_adapt_args_size", "spec_verify_run_noalloc",
+    "spec_verify_token_logprobs", "spec_verify_logprobs_workspace", "spec_verify_logprobs_args_size",
 )
+SV_LOGPROBS_MAX_TOP = 64
 SV_NOALLOC_SCRATCH_BYTES = 67108864
 
 
@@ -112,6 +114,27 @@ class SpecVerifyAdaptArgs(ctypes.Structure):
     ]
 
 
+class SpecVerifyLogprobsArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("top", ctypes.c_int32),
+        ("logits", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p),
+        ("logprob", ctypes.c_void_p),
+        ("entropy", ctypes.c_void_p),
+        ("rank", ctypes.c_void_p),
+        ("top_tokens", ctypes.c_void_p),
+        ("top_logprobs", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _LIB = None
 
 
@@ -164,12 +187,20 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_adapt.restype = ctypes.c_int
     lib.spec_verify_adapt_args_size.argtypes = []
     lib.spec_verify_adapt_args_size.restype = ctypes.c_int64
+    lib.spec_verify_token_logprobs.argtypes = [ctypes.POINTER(SpecVerifyLogprobsArgs), P]
+    lib.spec_verify_token_logprobs.restype = ctypes.c_int
+    lib.spec_verify_logprobs_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+    lib.spec_verify_logprobs_workspace.restype = ctypes.c_int64
+    lib.spec_verify_logprobs_args_size.argtypes = []
+    lib.spec_verify_logprobs_args_size.restype = ctypes.c_int64
     if lib.spec_verify_args_size() != ctypes.sizeof(SpecVerifyArgs):
         raise RuntimeError("spec_verify_args layout differs between the library and the binding")
     if lib.spec_verify_ngram_args_size() != ctypes.sizeof(SpecVerifyNgramArgs):
         raise RuntimeError("spec_verify_ngram_args layout differs between the library and the binding")
     if lib.spec_verify_adapt_args_size() != ctypes.sizeof(SpecVerifyAdaptArgs):
         raise RuntimeError("spec_verify_adapt_args layout differs between the library and the binding")
+    if lib.spec_verify_logprobs_args_size() != ctypes.sizeof(SpecVerifyLogprobsArgs):
+        raise RuntimeError("spec_verify_logprobs_args layout differs between the library and the binding")
     _LIB = lib
     return lib
 

@@ -1,0 +1,693 @@
+// Attention of a round's new tokens over a paged key-value cache, for gfx950.
+//
+// Sequence b brings n = num_draft[b] + 1 query rows (packed like a verify
+// call's target rows; n = 1 is plain decoding) and holds L = seq_len[b]
+// tokens in its pages, the new ones among them.  Row i sees positions
+// j <= L - n + i, with a window only the last `window` of them:
+//   o_i = sum_j softmax_j(scale q_i . k_j) v_j
+// in one pass over the cache, with a running maximum m, sum l and
+// unnormalised O:  O += 2^(s_j - m) v_j,  l += 2^(s_j - m),  s in log2 units.
+//
+// Bound by the cache's bytes.  The rows of all query heads that share a key
+// head form one tile (16 MT rows), so that each key and value is read once:
+//   S^T = K Q^T   (keys x rows)     O^T += V^T P^T   (head dim x rows)
+// with 16x16x32 MFMAs.  In this orientation a lane holds the scores of one
+// row (column lane & 15) for keys 4g..4g+3 of two 16-key tiles (g = lane >>
+// 4), and that is the layout of P^T as the second product's right operand if
+// the reduction's slots are numbered so: slot (g, e) is key 4g + e of the
+// first tile for e < 4, key 4g + e - 4 of the second above.  V^T is taken
+// under the same numbering: a lane loads D/16 adjacent elements of the 8 rows
+// of its slots and pairs them with byte permutes.  Neither scores nor values
+// pass through shared memory; K and V come straight from the pages into
+// registers, K of the next 32 keys while the softmax runs, V of them while
+// the next scores are formed.
+//
+// P is split into two halves of the 16-bit type, p = hi + lo, each its own
+// product: rounding p once would put an error of the output's own rounding
+// on top of it, and the second product hides behind the cache's reads.
+//
+// Work is cut into units of 128 keys of one (sequence, row tile, key head)
+// and dealt out in equal contiguous ranges, one per block, so that neither a
+// few long sequences nor a ragged batch leaves blocks idle.  The lengths are
+// only known on the device: every block forms the prefix of the units for
+// itself.  A range may end inside a tile; such parts (at most two per block)
+// go to the workspace as (O, m, l), and k_attention_join adds them up in
+// order.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "sv_internal.h"
+#include "sv_wave.h"
+
+namespace sv {
+
+namespace {
+
+using namespace wave;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kAtThreads = 256;
+constexpr int kAtWaves = kAtThreads / kWave;
+constexpr int kTileKeys = 32;                    // keys a wave takes at a time
+constexpr int kUnitKeys = kTileKeys * kAtWaves;  // keys of a unit of work
+static_assert(kUnitKeys == kAttnUnitKeys, "unit of work");
+constexpr float kLn2 = 0.693147180559945309417f;
+
+__device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <bool BF>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// two floats rounded to the 16-bit type (to nearest even), a in the low half
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (BF) {
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    const h2 v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+}
+template <bool BF>
+__device__ __forceinline__ float lo16(uint32_t w) {
+  if constexpr (BF) return __uint_as_float(w << 16);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+}
+template <bool BF>
+__device__ __forceinline__ float hi16(uint32_t w) {
+  if constexpr (BF) return __uint_as_float(w & 0xFFFF0000u);
+  else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+}
+
+// maximum over the four lanes that share a column (lanes l, l ^ 16, l ^ 32, l ^ 48)
+__device__ __forceinline__ float column_max(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The round's layout as every block works it out for itself: for sequence b
+// its first packed row and its first unit of work.  Returns false where the
+// rows do not add up.  Both arrays have B + 1 entries in shared memory.
+struct Extent {
+  int slot;       // row of page_table and seq_len; -1: refused
+  int len;        // cached tokens (0 for a refused sequence)
+  int blk0;       // first 128-key block any row sees
+  int nblk;       // blocks, at least 1 (an empty sequence still writes its rows)
+};
+
+__device__ __forceinline__ Extent seq_extent(const AttnParams& P, int b, int n) {
+  Extent x;
+  x.slot = P.seqs ? P.seqs[b] : b;
+  if ((unsigned)x.slot >= (unsigned)P.slots) x.slot = -1;
+  x.len = x.slot < 0 ? 0 : P.seq_len[x.slot];
+  if (x.len < 0 || x.len > P.max_len) {
+    x.slot = -1;
+    x.len = 0;
+  }
+  const int first = P.window > 0 ? max(0, x.len - n + 1 - P.window) : 0;
+  x.blk0 = first / kUnitKeys;
+  x.nblk = max(1, (x.len + kUnitKeys - 1) / kUnitKeys - x.blk0);
+  return x;
+}
+
+__device__ __forceinline__ uint32_t wave_incl_scan_u32(uint32_t v) {
+  v += (uint32_t)dpp_i<kDppRowShr1>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr2>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr4>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr8>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowBcast15, 0xA>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowBcast31, 0xC>(0, (int)v);
+  return v;
+}
+
+__device__ __forceinline__ bool plan(const AttnParams& P, int TM, uint32_t* rows, uint32_t* units) {
+  __shared__ uint32_t tr[kAtWaves], tu[kAtWaves];
+  __shared__ int bad;
+  const int t = threadIdx.x, lane = t & (kWave - 1), w = t / kWave;
+  if (t == 0) bad = 0;
+  __syncthreads();
+  const int per = (P.B + kAtThreads - 1) / kAtThreads;
+  const int b0 = min(t * per, P.B), b1 = min(b0 + per, P.B);
+  uint32_t r = 0, u = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int K = P.num_draft[b];
+    if (K < 0 || K >= P.total_rows) {
+      bad = 1;
+      continue;
+    }
+    const Extent x = seq_extent(P, b, K + 1);
+    r += (uint32_t)(K + 1);
+    u += (uint32_t)(((K + 1) * P.group + TM - 1) / TM * P.kv_heads) * (uint32_t)x.nblk;
+  }
+  const uint32_t ir = wave_incl_scan_u32(r), iu = wave_incl_scan_u32(u);
+  if (lane == kWave - 1) {
+    tr[w] = ir;
+    tu[w] = iu;
+  }
+  __syncthreads();
+  uint32_t ar = ir - r, au = iu - u;
+  for (int i = 0; i < w; ++i) {
+    ar += tr[i];
+    au += tu[i];
+  }
+  for (int b = b0; b < b1; ++b) {
+    rows[b] = ar;
+    units[b] = au;
+    const int K = P.num_draft[b];
+    if (K < 0 || K >= P.total_rows) continue;
+    const Extent x = seq_extent(P, b, K + 1);
+    ar += (uint32_t)(K + 1);
+    au += (uint32_t)(((K + 1) * P.group + TM - 1) / TM * P.kv_heads) * (uint32_t)x.nblk;
+  }
+  if (t == kAtThreads - 1) {
+    rows[P.B] = ar;
+    units[P.B] = au;
+    if (ar != (uint32_t)P.total_rows) bad = 1;
+  }
+  __syncthreads();
+  return bad == 0;
+}
+
+// What a block that starts inside a tile leaves for the join.
+struct Part {
+  int first_unit, end_unit;   // the tile's units; first_unit -1: the block starts at a tile's beginning
+  int row0, n;                // the sequence's packed rows
+  int head, mb;
+  int pad[2];
+};
+static_assert(sizeof(Part) == kAttnPartBytes, "part record");
+
+// block w of W takes units [w U / W, (w + 1) U / W); the block that holds unit u
+__device__ __forceinline__ uint32_t range_start(uint32_t w, uint32_t W, uint32_t U) { return (uint32_t)((uint64_t)w * U / W); }
+__device__ __forceinline__ uint32_t range_of(uint32_t u, uint32_t W, uint32_t U) {
+  return (uint32_t)((((uint64_t)u + 1) * W - 1) / U);
+}
+
+// a part in the workspace: TM rows of O, then TM maxima, then TM sums
+__device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, int TM, int D) {
+  return P.parts + ((int64_t)w * 2 + slot) * TM * (D + 2);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint16_t to16(float x) {
+  return (uint16_t)pack16<BF>(x, 0.f);
+}
+
+}  // namespace
+
+template <bool BF, int D, int MT>
+__global__ void __launch_bounds__(kAtThreads) k_attention(AttnParams P) {
+  constexpr int TM = 16 * MT;
+  constexpr int NS = D / 32;                     // 32-element slices of the head dimension (scores)
+  constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
+  constexpr int VW = NJ / 2;                     // dwords of those
+  extern __shared__ uint32_t dyn[];
+  uint32_t* rows = dyn;
+  uint32_t* units = dyn + P.B + 1;
+  __shared__ float ml[kAtWaves][2][TM];
+  __shared__ float ob[kAtWaves][16][D / 4 + 1];
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int g = lane >> 4, col = lane & 15;
+  const bool ok = plan(P, TM, rows, units);
+  Part* desc = reinterpret_cast<Part*>(P.desc);
+  const uint32_t U = units[P.B], W = min((uint32_t)gridDim.x, U);
+  const uint32_t w = blockIdx.x;
+  if (!ok) {                                     // the rows do not add up: every output is cleared
+    if (t == 0) desc[w].first_unit = -1;
+    const int64_t total = (int64_t)P.total_rows * P.heads * D;
+    for (int64_t i = (int64_t)w * kAtThreads + t; i < total; i += (int64_t)gridDim.x * kAtThreads)
+      ((uint16_t*)P.out)[i] = BF ? 0x7FC0 : 0x7E00;
+    if (P.lse)
+      for (int64_t i = (int64_t)w * kAtThreads + t; i < (int64_t)P.total_rows * P.heads; i += (int64_t)gridDim.x * kAtThreads)
+        P.lse[i] = __builtin_nanf("");
+    return;
+  }
+  if (w >= W) {
+    if (t == 0) desc[w].first_unit = -1;
+    return;
+  }
+  uint32_t u = range_start(w, W, U);
+  const uint32_t u_end = range_start(w + 1, W, U);
+  // the sequence that holds unit u
+  int b = 0;
+  for (int step = 4096; step > 0; step >>= 1)
+    if (b + step < P.B && units[b + step] <= u) b += step;
+  bool first_part = true;
+  while (u < u_end) {
+    while (units[b + 1] <= u) ++b;
+    const int row0 = (int)rows[b], n = (int)(rows[b + 1] - rows[b]);
+    const Extent x = seq_extent(P, b, n);
+    const uint32_t rel = u - units[b];
+    const int seg = (int)(rel / (uint32_t)x.nblk), b0 = (int)(rel - (uint32_t)seg * x.nblk);
+    const int b1 = (int)min((uint32_t)x.nblk, b0 + (u_end - u));
+    const int mb = seg / P.kv_heads, head = seg - mb * P.kv_heads;
+    if (first_part && t == 0) {
+      Part d;
+      d.first_unit = b0 > 0 ? (int)(u - b0) : -1;
+      d.end_unit = (int)(u - b0) + x.nblk;
+      d.row0 = row0;
+      d.n = n;
+      d.head = head;
+      d.mb = mb;
+      desc[w] = d;
+    }
+    const int nrow = min(TM, n * P.group - mb * TM);   // rows of this tile
+    // the rows of this lane's columns: their query, and the positions they see
+    u32x4 q[MT][NS];
+    int last[MT], from[MT];
+    int min_last = 0x7FFFFFFF, max_from = 0;
+    {
+      const int i0 = mb * TM / P.group, i1 = (mb * TM + nrow - 1) / P.group;
+      min_last = x.len - n + i0;
+      max_from = P.window > 0 ? max(0, x.len - n + i1 + 1 - P.window) : 0;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int r = m * 16 + col;
+      const bool in = r < nrow;
+      const int rr = mb * TM + (in ? r : 0);
+      const int i = rr / P.group, h = head * P.group + rr - i * P.group;
+      last[m] = in ? x.len - n + i : -1;
+      from[m] = P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
+      const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head + 8 * g;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) q[m][s] = *(const u32x4*)(qp + 32 * s);
+    }
+    f32x4 o[MT][NJ];
+    float mx[MT], ls[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m] = -INFINITY;
+      ls[m] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    bool bad = x.slot < 0;
+    const int32_t* table = P.table + (int64_t)max(x.slot, 0) * P.table_stride;
+    const int pmask = (1 << P.page_log2) - 1;
+    u32x4 kr[2][NS];
+    uint32_t vr[8][VW];
+    const char *kb[2], *vb[2];
+    // first key of block blk for this wave
+    auto key0 = [&](int blk) { return (x.blk0 + blk) * kUnitKeys + wv * kTileKeys; };
+    // Base addresses of the wave's two 16-key tiles.  A tile lies in one
+    // page; behind the last token the first tile's is used again (its reads
+    // stay in bounds and are masked).  A page outside the pool is replaced
+    // by page 0 and noted.
+    auto locate = [&](int pos) {
+      int id0 = table[pos >> P.page_log2];
+      int id1 = pos + 16 < x.len ? table[(pos + 16) >> P.page_log2] : id0;
+      if ((unsigned)id0 >= (unsigned)P.num_pages || (unsigned)id1 >= (unsigned)P.num_pages) {
+        bad = true;
+        id0 = (unsigned)id0 >= (unsigned)P.num_pages ? 0 : id0;
+        id1 = (unsigned)id1 >= (unsigned)P.num_pages ? 0 : id1;
+      }
+      const int off0 = pos & pmask, off1 = (pos + 16) & pmask;
+      kb[0] = (const char*)P.k + 2 * ((int64_t)id0 * P.k_page + (int64_t)head * P.k_head + (int64_t)off0 * P.k_tok);
+      kb[1] = (const char*)P.k + 2 * ((int64_t)id1 * P.k_page + (int64_t)head * P.k_head + (int64_t)off1 * P.k_tok);
+      vb[0] = (const char*)P.v + 2 * ((int64_t)id0 * P.v_page + (int64_t)head * P.v_head + (int64_t)off0 * P.v_tok);
+      vb[1] = (const char*)P.v + 2 * ((int64_t)id1 * P.v_page + (int64_t)head * P.v_head + (int64_t)off1 * P.v_tok);
+    };
+    const uint32_t ko = 2u * ((uint32_t)col * (uint32_t)P.k_tok + 8u * g);
+    auto load_k = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) kr[h][s] = *(const u32x4*)(kb[h] + ko + 64 * s);
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const char* p = vb[e >> 2] + 2u * ((uint32_t)(4 * g + (e & 3)) * (uint32_t)P.v_tok + (uint32_t)NJ * col);
+        if constexpr (VW == 2) {
+          const u32x2 a = *(const u32x2*)p;
+          vr[e][0] = a[0];
+          vr[e][1] = a[1];
+        } else {
+#pragma unroll
+          for (int c = 0; c < VW / 4; ++c) {
+            const u32x4 a = *(const u32x4*)(p + 16 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[e][4 * c + i] = a[i];
+          }
+        }
+      }
+    };
+    int pos = key0(b0);
+    const int pos_end = min(x.len, key0(b1));
+    if (pos < pos_end) {
+      locate(pos);
+      load_k();
+      load_v();
+    }
+    for (; pos < pos_end; pos += kUnitKeys) {
+      const bool more = pos + kUnitKeys < pos_end;
+      f32x4 sc[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          sc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < NS; ++s) sc[m][h] = mfma<BF>(kr[h][s], q[m][s], sc[m][h]);
+        }
+      if (more) {
+        locate(pos + kUnitKeys);
+        load_k();
+      }
+      const bool masked = pos + kTileKeys - 1 > min_last || pos < max_from;   // some row does not see some key
+      // what the mask hides of V must not be multiplied: 0 * NaN is NaN
+      bool strange = false;
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int kp = pos + 16 * (e >> 2) + 4 * g + (e & 3);
+          const bool gone = kp >= x.len;
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            vr[e][i] = gone ? 0u : vr[e][i];
+            constexpr uint32_t EX = BF ? 0x7F80u : 0x7C00u;
+            strange |= (vr[e][i] & EX) == EX || (vr[e][i] >> 16 & EX) == EX;
+          }
+        }
+        strange = __ballot(strange) != 0;
+      }
+      u32x4 ph[MT], pl[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = sc[m][e >> 2][e & 3] * P.scale_log2;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int kp = pos + 16 * (e >> 2) + 4 * g + (e & 3);
+            s[e] = kp <= last[m] && kp >= from[m] ? s[e] : -INFINITY;
+          }
+        }
+        float top = s[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+        if (__ballot(top > mx[m])) {             // a new maximum in some row: rescale
+          const float nm = fmaxf(mx[m], column_max(top));
+          const float f = mx[m] == nm ? 1.f : at_exp2(mx[m] - nm);
+          mx[m] = nm;
+          ls[m] *= f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) o[m][j] *= f;
+        }
+        const float ref = mx[m] == -INFINITY ? 0.f : mx[m];
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          p[e] = at_exp2(s[e] - ref);
+          ls[m] += p[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ph[m][i] = pack16<BF>(p[2 * i], p[2 * i + 1]);
+          pl[m][i] = pack16<BF>(p[2 * i] - lo16<BF>(ph[m][i]), p[2 * i + 1] - hi16<BF>(ph[m][i]));
+        }
+      }
+      if (!strange) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          u32x4 a;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            o[m][j] = mfma<BF>(a, ph[m], o[m][j]);
+            o[m][j] = mfma<BF>(a, pl[m], o[m][j]);
+          }
+        }
+      } else {
+        // a value that is not finite next to a key that some row does not
+        // see: one key at a time, added to the rows that see it
+        for (int kk = 0; kk < kTileKeys; ++kk) {
+          const int slot_g = (kk & 15) >> 2, slot_e = (kk >> 4) * 4 + (kk & 3);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+              const uint32_t keep = (slot_e >> 1) == i && slot_g == g ? ((slot_e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+              a[i] &= keep;
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              f32x4 d = mfma<BF>(a, ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
+              d = mfma<BF>(a, pl[m], d);
+              if (pos + kk <= last[m] && pos + kk >= from[m]) o[m][j] += d;
+            }
+          }
+        }
+      }
+      if (more) load_v();
+    }
+    // the waves' parts of the tile become one
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      ls[m] = column_sum(ls[m]);
+      if (bad) ls[m] = __builtin_nanf("");
+      if (g == 0) {
+        ml[wv][0][m * 16 + col] = mx[m];
+        ml[wv][1][m * 16 + col] = ls[m];
+      }
+    }
+    __syncthreads();
+    const bool whole = b0 == 0 && b1 == x.nblk;
+    float* part = part_at(P, (int)w, b0 > 0 ? 0 : 1, TM, D);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m * 16 >= nrow) break;
+      float M = ml[0][0][m * 16 + col];
+#pragma unroll
+      for (int i = 1; i < kAtWaves; ++i) M = fmaxf(M, ml[i][0][m * 16 + col]);
+      const float f = mx[m] == M ? 1.f : at_exp2(mx[m] - M);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) ob[wv][col][g * NJ + j] = o[m][j][r] * f;
+        __syncthreads();
+        // element c of row q: head dimension NJ (4 (c / NJ) + r) + c % NJ
+        for (int i = t; i < 16 * (D / 4); i += kAtThreads) {
+          const int qr = i / (D / 4), c = i - qr * (D / 4);
+          const int rr = m * 16 + qr;
+          if (rr < nrow) {
+            const int d = NJ * (4 * (c / NJ) + r) + c % NJ;
+            float Mq = ml[0][0][rr];
+#pragma unroll
+            for (int k = 1; k < kAtWaves; ++k) Mq = fmaxf(Mq, ml[k][0][rr]);
+            float L = 0.f, v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kAtWaves; ++k) {
+              L += ml[k][1][rr] * (ml[k][0][rr] == Mq ? 1.f : at_exp2(ml[k][0][rr] - Mq));
+              v += ob[k][qr][c];
+            }
+            if (whole) {
+              const int R = mb * TM + rr, ri = R / P.group, h = head * P.group + R - ri * P.group;
+              const int64_t at = (int64_t)(row0 + ri) * P.heads + h;
+              ((uint16_t*)P.out)[at * D + d] = to16<BF>(L == 0.f ? 0.f : v / L);
+              if (P.lse && r == 0 && c == 0) P.lse[at] = L == 0.f ? -INFINITY : (Mq + log2f(L)) * kLn2;
+            } else {
+              part[rr * D + d] = v;
+              if (r == 0 && c == 0) {
+                part[TM * D + rr] = Mq;
+                part[TM * D + TM + rr] = L;
+              }
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+    __syncthreads();                             // ml is free again
+    first_part = false;
+    u += (uint32_t)(b1 - b0);
+  }
+}
+
+// Adds up the parts of each tile that was cut: block (w, y) serves the tile
+// that block w of k_attention entered in its middle, if no earlier block did,
+// and rows 4 y .. 4 y + 3 of it, a row to a wave.  Bound by latency: a lane
+// has 8 parts of its 16 bytes in flight.  Further blocks check the sequences'
+// pages for `status`.
+template <bool BF, int D>
+__global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int TM, int W0) {
+  extern __shared__ uint32_t dyn[];
+  __shared__ float wt[kAtWaves][kWave];
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
+  if ((int)blockIdx.x >= W0) {
+    if (blockIdx.y) return;
+    // status of sequence b; block W0 checks the layout for all
+    const int b = (int)blockIdx.x - W0;
+    __shared__ int st;
+    __shared__ unsigned long long sum;
+    if (t == 0) {
+      st = 0;
+      sum = 0;
+    }
+    __syncthreads();
+    unsigned long long r = 0;
+    int f = 0;
+    for (int i = t; i < P.B; i += kAtThreads) {
+      const int K = P.num_draft[i];
+      if (K < 0 || K >= P.total_rows) f = SV_ST_BAD_LAYOUT;
+      else r += (unsigned)K + 1u;
+    }
+    if (f) atomicOr(&st, f);
+    atomicAdd(&sum, r);
+    __syncthreads();
+    if (t == 0 && sum != (unsigned long long)P.total_rows) atomicOr(&st, SV_ST_BAD_LAYOUT);
+    __syncthreads();
+    if (st == 0) {
+      const int n = P.num_draft[b] + 1;
+      const int slot = P.seqs ? P.seqs[b] : b;
+      int s = 0;
+      if ((unsigned)slot >= (unsigned)P.slots) {
+        s = SV_ST_BAD_SEQ;
+      } else {
+        const int len = P.seq_len[slot];
+        if (len < 0 || len > P.max_len) {
+          s = SV_ST_BAD_LENGTH;
+        } else {
+          const Extent x = seq_extent(P, b, n);
+          const int p0 = (x.blk0 * kUnitKeys) >> P.page_log2;
+          const int p1 = (len + (1 << P.page_log2) - 1) >> P.page_log2;
+          for (int i = p0 + t; i < p1; i += kAtThreads)
+            if ((unsigned)P.table[(int64_t)slot * P.table_stride + i] >= (unsigned)P.num_pages) s = SV_ST_BAD_PAGE;
+        }
+      }
+      __syncthreads();
+      if (s) atomicOr(&st, s);
+    }
+    __syncthreads();
+    if (t == 0) P.status[b] = st;
+    return;
+  }
+  const Part d = reinterpret_cast<const Part*>(P.desc)[blockIdx.x];
+  if (d.first_unit < 0) return;
+  const uint32_t U = (uint32_t)reinterpret_cast<const Part*>(P.desc)[W0].first_unit, W = min((uint32_t)W0, U);
+  const uint32_t w = blockIdx.x;
+  if (range_start(w - 1, W, U) > (uint32_t)d.first_unit) return;   // an earlier block joins this tile
+  const int row = (int)blockIdx.y * kAtWaves + wv;
+  const int nrow = min(TM, d.n * P.group - d.mb * TM);
+  if (row >= nrow) return;                       // whole waves; no block barrier below
+  const uint32_t w1 = range_of((uint32_t)d.end_unit - 1, W, U);
+  const int parts = (int)(w1 - w) + 2;           // part 0: slot 1 of block w - 1; part i: slot 0 of block w - 1 + i
+  auto part = [&](int i) { return (const float*)part_at(P, (int)w - 1 + i, i == 0 ? 1 : 0, TM, D); };
+  float M = -INFINITY;
+  for (int i = lane; i < parts; i += kWave) M = fmaxf(M, part(i)[TM * D + row]);
+  M = wave_max(M);
+  constexpr int Q = D / 4;                       // lanes that cover a row with 4 floats each
+  constexpr int GR = kWave / Q;                  // parts side by side: 4, 2 or 1
+  const int pg = lane / Q, dq = (lane - pg * Q) * 4;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  float L = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += kWave) {
+    float f = 0.f;
+    if (i0 + lane < parts) {
+      const float* pp = part(i0 + lane) + TM * D + row;
+      const float m = pp[0];
+      f = m == M ? 1.f : at_exp2(m - M);
+      L += pp[TM] * f;
+    }
+    wt[wv][lane] = f;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int m = min(kWave, parts - i0);
+    for (int i = pg; i < m; i += 8 * GR) {
+      f32x4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = *(const f32x4*)(part(i0 + min(i + k * GR, m - 1)) + row * D + dq);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k * GR < m) {
+          const float f2 = wt[wv][i + k * GR];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[c] = fmaf(v[k][c], f2, acc[c]);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  L = wave_sum(L);
+#pragma unroll
+  for (int off = Q; off < kWave; off <<= 1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], off);
+  const int R = d.mb * TM + row, ri = R / P.group, h = d.head * P.group + R - ri * P.group;
+  const int64_t at = (int64_t)(d.row0 + ri) * P.heads + h;
+  if (pg == 0) {
+    uint16_t* op = (uint16_t*)P.out + at * D + dq;
+    u32x2 z;
+    z[0] = L == 0.f ? 0u : pack16<BF>(acc[0] / L, acc[1] / L);
+    z[1] = L == 0.f ? 0u : pack16<BF>(acc[2] / L, acc[3] / L);
+    *(u32x2*)op = z;
+  }
+  if (P.lse && lane == 0) P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+namespace {
+
+template <bool BF, int D, int MT>
+hipError_t launch_one(const AttnParams& p, int W, hipStream_t st) {
+  const size_t lds = (size_t)(p.B + 1) * 8;
+  hipLaunchKernelGGL((k_attention<BF, D, MT>), dim3((unsigned)W), dim3(kAtThreads), lds, st, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_attention_join<BF, D>), dim3((unsigned)(W + (p.status ? p.B : 0)), 16 * MT / kAtWaves),
+                     dim3(kAtThreads), 0, st, p, 16 * MT, W);
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
+  switch (p.head_dim * 8 + mt) {
+    case 64 * 8 + 1: return launch_one<BF, 64, 1>(p, W, st);
+    case 64 * 8 + 2: return launch_one<BF, 64, 2>(p, W, st);
+    case 64 * 8 + 4: return launch_one<BF, 64, 4>(p, W, st);
+    case 128 * 8 + 1: return launch_one<BF, 128, 1>(p, W, st);
+    case 128 * 8 + 2: return launch_one<BF, 128, 2>(p, W, st);
+    case 128 * 8 + 4: return launch_one<BF, 128, 4>(p, W, st);
+    case 256 * 8 + 1: return launch_one<BF, 256, 1>(p, W, st);
+    case 256 * 8 + 2: return launch_one<BF, 256, 2>(p, W, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st) {
+  return p.bf16 ? launch_type<true>(p, row_tiles, blocks, st) : launch_type<false>(p, row_tiles, blocks, st);
+}
+
+}  // namespace sv

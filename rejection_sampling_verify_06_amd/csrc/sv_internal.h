@@ -191,6 +191,31 @@ hipError_t launch_stats_summary(const StatsParams& p, hipStream_t st);
 hipError_t launch_adapt(const AdaptParams& p, hipStream_t st);
 hipError_t launch_adapt_reset(const AdaptParams& p, hipStream_t st);
 
+// log probabilities of given tokens (sv_logprobs.hip)
+constexpr int64_t kMaxGrid = 65535;     // blocks per grid dimension
+
+struct LogprobParams {
+  int64_t rows;
+  int64_t V;
+  int64_t ld;
+  const void* logits;
+  int32_t bf16;
+  int32_t top;
+  int64_t nch;                 // 32 KB chunks per row
+  const int32_t* tokens;       // or NULL
+  const float* temperature;    // or NULL
+  float* logprob;
+  float* entropy;
+  int32_t* rank;
+  int32_t* top_tokens;
+  float* top_logprobs;
+  int32_t* status;
+  float* partials;             // [rows][nch][4]: M, S, W, count
+  float* segmax;               // [rows][nch][64] segment maxima, or NULL (top = 0)
+};
+
+hipError_t launch_logprobs(const LogprobParams& p, hipStream_t st);
+
 // ---- host side shared by the entry points (sv_api.cpp) ----------------------
 
 // Sizes a verify call may use: those of a context, or of one allocation-free call.

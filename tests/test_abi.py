@@ -159,3 +159,25 @@ def test_side_entry_points_reject_bad_arguments():
     ad.target = 0.7
     assert lib.spec_verify_adapt_reset(ctypes.byref(ad), 0, None) == _lib.SV_ERR_INVALID   # init_k
     assert lib.spec_verify_adapt(ctypes.byref(ad), None) == _lib.SV_OK                     # batch 0: nothing to do
+
+
+def test_token_logprobs_rejects_bad_arguments():
+    _lib, lib = _lib_loaded()
+    ws = lib.spec_verify_logprobs_workspace
+    assert ws(4, 1000, _lib.SV_BF16, 0) == 4 * 16 and ws(4, 1000, _lib.SV_BF16, 5) == 4 * (16 + 256)
+    assert ws(0, 1000, _lib.SV_BF16, 5) == 0
+    for rows, vocab, dtype, top in [(-1, 10, 0, 0), (4, 0, 0, 0), (4, 2097153, 0, 0), (4, 10, 2, 0), (4, 10, 0, -1),
+                                    (4, 10, 0, 11), (4, 1000, 0, 65), (1 << 31, 10, 0, 0), (1 << 62, 10, 0, 0)]:
+        assert ws(rows, vocab, dtype, top) == _lib.SV_ERR_INVALID
+    call = lib.spec_verify_token_logprobs
+    assert call(None, None) == _lib.SV_ERR_INVALID
+    a = _lib.SpecVerifyLogprobsArgs(rows=0, vocab=100, dtype=0, top=0)
+    assert call(ctypes.byref(a), None) == _lib.SV_OK                     # no rows: nothing to do
+    good = dict(rows=2, vocab=100, dtype=0, top=2, logits=0x1000, ld=100, tokens=0x1000, logprob=0x1000, top_tokens=0x1000,
+                workspace=0x1000, workspace_bytes=10000)
+    for bad in (dict(logits=None), dict(logits=0x1001), dict(ld=99), dict(ld=1 << 61), dict(tokens=None),
+                dict(top_tokens=None), dict(top=0), dict(workspace=None), dict(workspace=0x1008), dict(workspace_bytes=10),
+                dict(rows=-1), dict(dtype=3)):
+        a = _lib.SpecVerifyLogprobsArgs(**{**good, **bad})
+        assert call(ctypes.byref(a), None) == _lib.SV_ERR_INVALID, bad
+        assert b"spec_verify_token_logprobs" in lib.spec_verify_last_error(), bad
