@@ -88,8 +88,8 @@ extern "C" {
 
 typedef struct spec_verify_ctx spec_verify_ctx;
 
-/* logits element type */
-enum { SV_F32 = 0, SV_BF16 = 1 };
+/* element types: logits are SV_F32 or SV_BF16, cached keys and values SV_BF16 or SV_F16 */
+enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2 };
 
 /* per-sequence verify mode (values of args->mode[s]) */
 enum { SV_SAMPLE = 0, SV_GREEDY = 1, SV_ONEHOT = 2, SV_STRICT = 3 };
@@ -114,7 +114,11 @@ enum {
   SV_ST_NO_DRAFT_LOGITS = 16,  /* SAMPLE sequence with K_s > 0 but draft_logits == NULL */
   SV_ST_BAD_TOKEN = 32,        /* a proposed token outside [0, vocab) */
   SV_ST_NONFINITE = 64,        /* a used logit row holds NaN or +inf, or is entirely -inf */
-  SV_ST_ZERO_RESIDUAL = 128    /* the residual had no mass (rounding only); the token was drawn from p_A instead */
+  SV_ST_ZERO_RESIDUAL = 128,   /* the residual had no mass (rounding only); the token was drawn from p_A instead */
+  /* the paged cache's operators only */
+  SV_ST_BAD_SEQ = 256,         /* a sequence slot outside the cache, or named twice where it may be named once */
+  SV_ST_BAD_LENGTH = 512,      /* a length or token count that is negative or does not fit */
+  SV_ST_BAD_PAGE = 1024        /* a page outside the pool */
 };
 
 /* smallest accepted temperature for SAMPLE/ONEHOT/STRICT (float32 1e-6) */
@@ -429,6 +433,94 @@ int64_t spec_verify_logprobs_workspace(int64_t rows, int64_t vocab, int32_t dtyp
 
 /* sizeof(spec_verify_logprobs_args) as compiled into the library. */
 int64_t spec_verify_logprobs_args_size(void);
+
+/* ---- attention over a paged key-value cache ---------------------------------
+ * The attention of the target's verification pass: sequence b brings n =
+ * num_draft[b] + 1 new tokens (its last emitted one and its drafts; n = 1 is
+ * plain decoding), whose query rows are packed like a verify call's target
+ * rows.  Its keys and values lie in pages and are in the cache already:
+ * seq_len tokens, the n new ones last.  Query row i sees the positions
+ * j <= seq_len - n + i, with window > 0 only the last `window` of them:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
+ * `heads` query heads share `kv_heads` key heads in groups of neighbours
+ * (query head h reads key head h / (heads / kv_heads)).  A row that sees
+ * nothing gets out = 0 and lse = -inf.  Keys and values that a row does not
+ * see have no effect on it, whatever they hold; a row that sees one that is
+ * not finite is not finite itself (where its weight is not 0).
+ * All pointers are device pointers owned by the caller.
+ *   q              [total_rows][heads][head_dim], dtype SV_BF16 or SV_F16
+ *   k, v           [num_pages][kv_heads][page_size][head_dim] of the same
+ *                  type, in any order of the first three: strides in elements
+ *                  for page, head and token; head_dim is contiguous
+ *   page_table     [slots][page_table_stride] int32: entry j of a row holds
+ *                  tokens j * page_size ..; max_pages entries may be used
+ *   seq_len        [slots] int32
+ *   seqs           [batch] int32: sequence b is row seqs[b] of page_table and
+ *                  seq_len (a slot may be named more than once); NULL: row b
+ *   num_draft      [batch] int32, sum of (num_draft + 1) = total_rows
+ *   out            [total_rows][heads][head_dim], contiguous
+ *   lse            [total_rows][heads] float or NULL
+ *   status         [batch] int32 or NULL
+ *   workspace      16-byte aligned, at least spec_verify_attention_workspace()
+ *                  bytes; its contents need not survive the call, and calls
+ *                  that may overlap each need their own
+ * head_dim 64, 128 or 256; page_size a power of two from 16 to 1024; q, k, v
+ * and out 16-byte aligned with strides in multiples of 8 elements; batch <=
+ * 4096, total_rows <= 524288, heads / kv_heads <= 256.
+ * Scores, softmax and sums are float32, the softmax's weights enter the
+ * second product as the sum of two 16-bit values, the result is rounded once.
+ * Repeated calls are bitwise identical.
+ * What only the device can see: num_draft that does not add up sets
+ * SV_ST_BAD_LAYOUT for every sequence and every output is NaN; a sequence
+ * with SV_ST_BAD_SEQ (slot outside 0..slots-1), SV_ST_BAD_LENGTH (seq_len
+ * negative or above max_pages * page_size) or SV_ST_BAD_PAGE (a page that
+ * holds visible tokens is outside the pool) gets NaN, and no such page is read.
+ * Enqueues two kernels on `hip_stream`, which belongs to the calling
+ * thread's current device; allocates nothing, does not synchronise.
+ * SV_ERR_INVALID: nothing was enqueued.  batch == 0 is a no-op. */
+typedef struct spec_verify_attention_args {
+  int32_t batch;
+  int32_t total_rows;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int32_t page_size;
+  int32_t window;              /* 0: every earlier position */
+  int64_t num_pages;
+  int32_t slots;
+  int32_t max_pages;
+  int64_t page_table_stride;   /* >= max_pages */
+  const void* q;
+  int64_t q_row_stride;
+  int64_t q_head_stride;
+  const void* k;
+  int64_t k_page_stride;
+  int64_t k_head_stride;
+  int64_t k_token_stride;
+  const void* v;
+  int64_t v_page_stride;
+  int64_t v_head_stride;
+  int64_t v_token_stride;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* seqs;
+  const int32_t* num_draft;
+  double scale;                /* finite; head_dim^-0.5 for the usual attention */
+  void* out;
+  float* lse;
+  int32_t* status;
+  void* workspace;
+  int64_t workspace_bytes;
+} spec_verify_attention_args;
+int spec_verify_paged_attention(const spec_verify_attention_args* args, void* hip_stream);
+
+/* Bytes of workspace for a call with these sizes (the pointers, strides and
+ * tables of args are not looked at), or SV_ERR_INVALID. */
+int64_t spec_verify_attention_workspace(const spec_verify_attention_args* args);
+
+/* sizeof(spec_verify_attention_args) as compiled into the library. */
+int64_t spec_verify_attention_args_size(void);
 
 /* Library version string. */
 const char* spec_verify_version(void);

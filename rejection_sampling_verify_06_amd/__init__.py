@@ -19,15 +19,16 @@ from typing import Optional
 
 from . import _lib
 from ._lib import (  # noqa: F401
-    SV_F32, SV_BF16, SV_SAMPLE, SV_GREEDY, SV_ONEHOT, SV_STRICT,
+    SV_F32, SV_BF16, SV_F16, SV_SAMPLE, SV_GREEDY, SV_ONEHOT, SV_STRICT,
     SV_ST_BAD_LAYOUT, SV_ST_K_TOO_LARGE, SV_ST_BAD_MODE, SV_ST_BAD_TEMPERATURE,
     SV_ST_NO_DRAFT_LOGITS, SV_ST_BAD_TOKEN, SV_ST_NONFINITE, SV_ST_ZERO_RESIDUAL,
+    SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH, SV_ST_BAD_PAGE,
     KERNEL_NAMES, LibraryMissing,
     SV_ADAPT_WINDOW, SV_ADAPT_MULTIPLICATIVE, SV_ADAPT_OPTIMAL_K, SV_ADAPT_COUNT_EMITTED, SV_ADAPT_COUNT_DRAFT_ONLY,
 )
 
 __all__ = ["Verifier", "VerifyError", "verify", "propose_ngram", "NgramProposer", "AcceptanceStats",
-           "DraftLengthController", "token_logprobs", "LibraryMissing", "KERNEL_NAMES"]
+           "DraftLengthController", "token_logprobs", "paged_attention", "LibraryMissing", "KERNEL_NAMES"]
 
 
 class VerifyError(RuntimeError):
@@ -451,6 +452,82 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab
             _ptr(out["status"]), ws.data_ptr(), nbytes)
         _check(lib.spec_verify_token_logprobs(ctypes.byref(a), torch.cuda.current_stream(dev).cuda_stream))
     return out
+
+
+def _cache_dtype(t, name, torch):
+    if t.dtype == torch.bfloat16:
+        return SV_BF16
+    if t.dtype == torch.float16:
+        return SV_F16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs=None, scale: Optional[float] = None,
+                    window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None) -> dict:
+    """Attention of a round's new tokens over a paged key-value cache
+    (spec_verify_paged_attention).
+
+    ``q`` is [total_rows, heads, head_dim], bfloat16 or float16: for each
+    sequence its ``num_draft`` + 1 rows, packed like a verify call's target
+    rows (``num_draft`` 0: one new token).  ``k_pages`` / ``v_pages`` are
+    [num_pages, kv_heads, page_size, head_dim] (any strides of the first
+    three), ``page_table`` int32 [slots, max_pages], ``seq_len`` int32
+    [slots]: the cached tokens, the new ones last.  Sequence b uses slot
+    ``seqs[b]`` (int32), or b.  Row i sees positions up to seq_len -
+    num_draft - 1 + i, with ``window`` > 0 only the last ``window`` of them.
+    ``scale`` defaults to head_dim ** -0.5.  Returns ``out`` like ``q``
+    (contiguous), ``lse`` (float32 [total_rows, heads]) and ``status`` (int32
+    [batch]); what was not asked for is None."""
+    import torch
+    lib = _lib.load()
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape or page_table.dim() != 2:
+        raise ValueError("q must be 3-D, k_pages and v_pages 4-D of one shape, page_table 2-D")
+    dev = q.device
+    N, H, D = q.shape
+    pages, KV, P, Dk = k_pages.shape
+    if D != Dk:
+        raise ValueError(f"q has head_dim {D}, the pages {Dk}")
+    for t, name in ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} is {t.dtype}, q {q.dtype}")
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be a device tensor on q's device")
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+    _need(num_draft, "num_draft", (torch.int32,), torch, None, dev)
+    B = int(num_draft.numel())
+    _need(seqs, "seqs", (torch.int32,), torch, B, dev)
+    _need(seq_len, "seq_len", (torch.int32,), torch, int(page_table.shape[0]), dev)
+    if page_table.dtype != torch.int32 or page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 on q's device with unit column stride")
+    if seqs is None and B > page_table.shape[0]:
+        raise ValueError(f"{B} sequences, but page_table has {page_table.shape[0]} rows")
+    a = _lib.SpecVerifyAttentionArgs(
+        B, N, H, KV, D, _cache_dtype(q, "q", torch), P, int(window), pages, page_table.shape[0], page_table.shape[1],
+        page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1],
+        q.data_ptr(), q.stride(0) if N > 1 else 0, q.stride(1) if H > 1 else 0,
+        k_pages.data_ptr(), *_page_strides(k_pages), v_pages.data_ptr(), *_page_strides(v_pages),
+        page_table.data_ptr(), seq_len.data_ptr(), _ptr(seqs), num_draft.data_ptr(),
+        D ** -0.5 if scale is None else float(scale))
+    nbytes = lib.spec_verify_attention_workspace(ctypes.byref(a))
+    if nbytes < 0:
+        _check(int(nbytes))
+    with _on_stream(dev, stream):
+        out = {
+            "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
+            "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,
+            "status": torch.empty(B, dtype=torch.int32, device=dev) if want_status else None,
+        }
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        a.out, a.lse, a.status = out["out"].data_ptr(), _ptr(out["lse"]), _ptr(out["status"])
+        a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
+        _check(lib.spec_verify_paged_attention(ctypes.byref(a), torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def _page_strides(t):
+    """Page, head and token strides; those of a dimension of size 1 say nothing."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
 
 
 def library_loaded_path() -> str:

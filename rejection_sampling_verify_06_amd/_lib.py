@@ -7,7 +7,7 @@ import os
 from .build import library_path
 
 # values from include/spec_verify.h
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16 = 0, 1, 2
 SV_SAMPLE, SV_GREEDY, SV_ONEHOT, SV_STRICT = 0, 1, 2, 3
 SV_OK, SV_ERR_INVALID, SV_ERR_NOMEM, SV_ERR_HIP, SV_ERR_CAPACITY = 0, -1, -2, -3, -4
 SV_ST_BAD_LAYOUT = 1
@@ -18,6 +18,9 @@ SV_ST_NO_DRAFT_LOGITS = 16
 SV_ST_BAD_TOKEN = 32
 SV_ST_NONFINITE = 64
 SV_ST_ZERO_RESIDUAL = 128
+SV_ST_BAD_SEQ = 256
+SV_ST_BAD_LENGTH = 512
+SV_ST_BAD_PAGE = 1024
 SV_NUM_KERNELS = 4
 KERNEL_NAMES = ("row_stats", "filter", "final", "select")
 
@@ -49,6 +52,7 @@ EXPORTED = (
     "spec_verify_stats_accumulate", "spec_verify_stats_summary", "spec_verify_adapt_reset", "spec_verify_adapt",
     "spec_verify_adapt_args_size", "spec_verify_run_noalloc",
     "spec_verify_token_logprobs", "spec_verify_logprobs_workspace", "spec_verify_logprobs_args_size",
+    "spec_verify_paged_attention", "spec_verify_attention_workspace", "spec_verify_attention_args_size",
 )
 SV_LOGPROBS_MAX_TOP = 64
 SV_NOALLOC_SCRATCH_BYTES = 67108864
@@ -135,6 +139,44 @@ class SpecVerifyLogprobsArgs(ctypes.Structure):
     ]
 
 
+class SpecVerifyAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("total_rows", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("slots", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p),
+        ("seqs", ctypes.c_void_p),
+        ("num_draft", ctypes.c_void_p),
+        ("scale", ctypes.c_double),
+        ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _LIB = None
 
 
@@ -193,6 +235,12 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_logprobs_workspace.restype = ctypes.c_int64
     lib.spec_verify_logprobs_args_size.argtypes = []
     lib.spec_verify_logprobs_args_size.restype = ctypes.c_int64
+    lib.spec_verify_paged_attention.argtypes = [ctypes.POINTER(SpecVerifyAttentionArgs), P]
+    lib.spec_verify_paged_attention.restype = ctypes.c_int
+    lib.spec_verify_attention_workspace.argtypes = [ctypes.POINTER(SpecVerifyAttentionArgs)]
+    lib.spec_verify_attention_workspace.restype = ctypes.c_int64
+    lib.spec_verify_attention_args_size.argtypes = []
+    lib.spec_verify_attention_args_size.restype = ctypes.c_int64
     if lib.spec_verify_args_size() != ctypes.sizeof(SpecVerifyArgs):
         raise RuntimeError("spec_verify_args layout differs between the library and the binding")
     if lib.spec_verify_ngram_args_size() != ctypes.sizeof(SpecVerifyNgramArgs):
@@ -201,6 +249,8 @@ def load() -> ctypes.CDLL:
         raise RuntimeError("spec_verify_adapt_args layout differs between the library and the binding")
     if lib.spec_verify_logprobs_args_size() != ctypes.sizeof(SpecVerifyLogprobsArgs):
         raise RuntimeError("spec_verify_logprobs_args layout differs between the library and the binding")
+    if lib.spec_verify_attention_args_size() != ctypes.sizeof(SpecVerifyAttentionArgs):
+        raise RuntimeError("spec_verify_attention_args layout differs between the library and the binding")
     _LIB = lib
     return lib
 

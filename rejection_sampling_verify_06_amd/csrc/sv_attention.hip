@@ -219,7 +219,7 @@ __device__ __forceinline__ uint16_t to16(float x) {
 }  // namespace
 
 template <bool BF, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads) k_attention(AttnParams P) {
+__global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 || (D == 128 && MT == 2) ? 1 : 2) k_attention(AttnParams P) {
   constexpr int TM = 16 * MT;
   constexpr int NS = D / 32;                     // 32-element slices of the head dimension (scores)
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attention(AttnParams P) {
   Part* desc = reinterpret_cast<Part*>(P.desc);
   const uint32_t U = units[P.B], W = min((uint32_t)gridDim.x, U);
   const uint32_t w = blockIdx.x;
+  if (w == 0 && t == 0) desc[gridDim.x].first_unit = (int)U;   // the join cuts the units the same way
   if (!ok) {                                     // the rows do not add up: every output is cleared
     if (t == 0) desc[w].first_unit = -1;
     const int64_t total = (int64_t)P.total_rows * P.heads * D;
@@ -318,8 +319,8 @@ __global__ void __launch_bounds__(kAtThreads) k_attention(AttnParams P) {
     // stay in bounds and are masked).  A page outside the pool is replaced
     // by page 0 and noted.
     auto locate = [&](int pos) {
-      int id0 = table[pos >> P.page_log2];
-      int id1 = pos + 16 < x.len ? table[(pos + 16) >> P.page_log2] : id0;
+      int id0 = __builtin_amdgcn_readfirstlane(table[pos >> P.page_log2]);
+      int id1 = pos + 16 < x.len ? __builtin_amdgcn_readfirstlane(table[(pos + 16) >> P.page_log2]) : id0;
       if ((unsigned)id0 >= (unsigned)P.num_pages || (unsigned)id1 >= (unsigned)P.num_pages) {
         bad = true;
         id0 = (unsigned)id0 >= (unsigned)P.num_pages ? 0 : id0;
@@ -674,12 +675,9 @@ hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
   switch (p.head_dim * 8 + mt) {
     case 64 * 8 + 1: return launch_one<BF, 64, 1>(p, W, st);
     case 64 * 8 + 2: return launch_one<BF, 64, 2>(p, W, st);
-    case 64 * 8 + 4: return launch_one<BF, 64, 4>(p, W, st);
     case 128 * 8 + 1: return launch_one<BF, 128, 1>(p, W, st);
     case 128 * 8 + 2: return launch_one<BF, 128, 2>(p, W, st);
-    case 128 * 8 + 4: return launch_one<BF, 128, 4>(p, W, st);
     case 256 * 8 + 1: return launch_one<BF, 256, 1>(p, W, st);
-    case 256 * 8 + 2: return launch_one<BF, 256, 2>(p, W, st);
   }
   return hipErrorInvalidValue;
 }

@@ -216,6 +216,42 @@ struct LogprobParams {
 
 hipError_t launch_logprobs(const LogprobParams& p, hipStream_t st);
 
+// attention over a paged cache (sv_attention.hip)
+constexpr int kAttnUnitKeys = 128;      // keys of a unit of work
+constexpr int kAttnPartBytes = 32;      // a block's record for the join
+
+struct AttnParams {
+  int32_t B;
+  int32_t total_rows;
+  int32_t heads, kv_heads, group;   // group = heads / kv_heads
+  int32_t head_dim;
+  int32_t bf16;                     // else float16
+  int32_t window;                   // 0: none
+  int32_t page_log2;
+  int32_t slots;                    // rows of page_table and seq_len
+  int32_t max_len;                  // tokens a row of page_table can name
+  int64_t num_pages;
+  float scale_log2;                 // scale * log2(e)
+  const void* q;
+  int64_t q_row, q_head;            // strides in elements, here and below
+  const void* k;
+  int64_t k_page, k_head, k_tok;
+  const void* v;
+  int64_t v_page, v_head, v_tok;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* seq_len;
+  const int32_t* num_draft;
+  const int32_t* seqs;              // or NULL
+  void* out;
+  float* lse;                       // or NULL
+  int32_t* status;                  // or NULL
+  float* parts;                     // [blocks][2] parts of 16 row_tiles * (head_dim + 2) floats
+  void* desc;                       // [blocks + 1] records
+};
+
+hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+
 // ---- host side shared by the entry points (sv_api.cpp) ----------------------
 
 // Sizes a verify call may use: those of a context, or of one allocation-free call.

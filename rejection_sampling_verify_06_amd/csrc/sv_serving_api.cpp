@@ -1,8 +1,11 @@
 // Host side of the serving operators declared in include/spec_verify.h (token
-// log probabilities): argument validation and workspace layout.
+// log probabilities, attention over a paged cache): argument validation and workspace layout.
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "spec_verify.h"
 #include "sv_internal.h"
@@ -34,6 +37,78 @@ bool logprob_sizes_ok(const char* who, int64_t rows, int64_t vocab, int32_t dtyp
     set_err("%s: top %d outside 0..min(%d, vocab)", who, top, SV_LOGPROBS_MAX_TOP);
     return false;
   }
+  return true;
+}
+
+// How a call's work is laid out: 16-row tiles per block, and blocks.
+struct AttnShape {
+  int row_tiles;
+  int blocks;
+  int64_t part_bytes;   // of one block's two parts
+};
+
+bool is_pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
+
+bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, AttnShape* s) {
+  if (!a) {
+    set_err("%s: args is NULL", who);
+    return false;
+  }
+  if (a->dtype != SV_BF16 && a->dtype != SV_F16) {
+    set_err("%s: dtype %d is neither SV_BF16 nor SV_F16", who, a->dtype);
+    return false;
+  }
+  if (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256) {
+    set_err("%s: head_dim %d is not 64, 128 or 256", who, a->head_dim);
+    return false;
+  }
+  if (!is_pow2(a->page_size) || a->page_size < 16 || a->page_size > 1024) {
+    set_err("%s: page_size %d is not a power of two from 16 to 1024", who, a->page_size);
+    return false;
+  }
+  if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads || a->heads / a->kv_heads > 256 || a->heads > 65536) {
+    set_err("%s: heads %d must be a multiple, up to 256 times, of kv_heads %d", who, a->heads, a->kv_heads);
+    return false;
+  }
+  if (a->batch < 0 || a->batch > 4096 || a->total_rows < a->batch || a->total_rows > 524288) {
+    set_err("%s: batch %d outside 0..4096, or total_rows %d outside batch..524288", who, a->batch, a->total_rows);
+    return false;
+  }
+  if (a->window < 0 || a->num_pages < 1 || a->num_pages > INT32_MAX || a->slots < 1 || a->max_pages < 1 ||
+      (int64_t)a->max_pages * a->page_size > INT32_MAX - 4096) {
+    set_err("%s: window %d < 0, or num_pages %lld, slots %d, max_pages %d outside their range", who, a->window,
+            (long long)a->num_pages, a->slots, a->max_pages);
+    return false;
+  }
+  if (a->batch == 0) {
+    *s = AttnShape{1, 1, 0};
+    return true;
+  }
+  // The tile of a (sequence, key head) as high as the batch's average needs:
+  // a higher one would hold registers for rows that are not there, a lower
+  // one reads the keys again for every further tile.
+  const int64_t group = a->heads / a->kv_heads;
+  const int64_t rows = (a->total_rows + a->batch - 1) / a->batch * group;
+  s->row_tiles = rows <= 16 || a->head_dim == 256 ? 1 : 2;
+  const int64_t tm = 16 * s->row_tiles;
+  const int64_t keys = (int64_t)a->max_pages * a->page_size;
+  const int64_t units = (a->total_rows * group / tm + a->batch) * a->kv_heads *
+                        ((keys + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
+  if (units > INT32_MAX) {
+    set_err("%s: %lld units of work: batch, heads and max_pages are too large together", who, (long long)units);
+    return false;
+  }
+  s->blocks = (int)std::min<int64_t>(units, 512);
+  s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
+  return true;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+// strides of a tensor of 16-bit elements: multiples of 16 bytes, small enough for the kernels' offsets
+bool strides_ok(int64_t a, int64_t b, int64_t c) {
+  for (int64_t x : {a, b, c})
+    if (x < 0 || x % 8 || x > (int64_t)1 << 40) return false;
   return true;
 }
 
@@ -95,6 +170,86 @@ int spec_verify_token_logprobs(const spec_verify_logprobs_args* a, void* hip_str
   p.partials = static_cast<float*>(a->workspace);
   p.segmax = a->top > 0 ? p.partials + a->rows * p.nch * 4 : nullptr;
   hipError_t e = sv::launch_logprobs(p, (hipStream_t)hip_stream);
+  if (e != hipSuccess) return hip_fail(who, e);
+  return SV_OK;
+}
+
+int64_t spec_verify_attention_args_size(void) { return (int64_t)sizeof(spec_verify_attention_args); }
+
+int64_t spec_verify_attention_workspace(const spec_verify_attention_args* a) {
+  AttnShape s;
+  if (!attention_sizes_ok("spec_verify_attention_workspace", a, &s)) return SV_ERR_INVALID;
+  return s.blocks * s.part_bytes + (int64_t)(s.blocks + 1) * sv::kAttnPartBytes;
+}
+
+int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_stream) {
+  const char* who = "spec_verify_paged_attention";
+  AttnShape s;
+  if (!attention_sizes_ok(who, a, &s)) return SV_ERR_INVALID;
+  if (a->batch == 0) return SV_OK;
+  if (!a->q || !a->k || !a->v || !a->page_table || !a->seq_len || !a->num_draft || !a->out) {
+    set_err("%s: q, k, v, page_table, seq_len, num_draft and out are required", who);
+    return SV_ERR_INVALID;
+  }
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) ||
+      !strides_ok(a->q_row_stride, a->q_head_stride, 0) ||
+      !strides_ok(a->k_page_stride, a->k_head_stride, a->k_token_stride) ||
+      !strides_ok(a->v_page_stride, a->v_head_stride, a->v_token_stride) || a->k_token_stride > 1 << 24 ||
+      a->v_token_stride > 1 << 24) {
+    set_err("%s: q, k, v and out need 16-byte alignment, and strides that are multiples of 8 elements "
+            "(a token's at most 2^24)", who);
+    return SV_ERR_INVALID;
+  }
+  if (a->page_table_stride < a->max_pages || a->page_table_stride > INT32_MAX) {
+    set_err("%s: page_table_stride %lld < max_pages %d", who, (long long)a->page_table_stride, a->max_pages);
+    return SV_ERR_INVALID;
+  }
+  if (!isfinite(a->scale)) {
+    set_err("%s: scale is not finite", who);
+    return SV_ERR_INVALID;
+  }
+  const int64_t need = spec_verify_attention_workspace(a);
+  if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need) {
+    set_err("%s: a 16-byte aligned workspace of %lld bytes is required, got %lld", who, (long long)need,
+            (long long)a->workspace_bytes);
+    return SV_ERR_INVALID;
+  }
+  sv::AttnParams p{};
+  p.B = a->batch;
+  p.total_rows = a->total_rows;
+  p.heads = a->heads;
+  p.kv_heads = a->kv_heads;
+  p.group = a->heads / a->kv_heads;
+  p.head_dim = a->head_dim;
+  p.bf16 = a->dtype == SV_BF16;
+  p.window = std::min(a->window, 1 << 30);   // beyond every length; keeps the differences of positions in 32 bits
+  p.page_log2 = __builtin_ctz((unsigned)a->page_size);
+  p.slots = a->slots;
+  p.max_len = a->max_pages * a->page_size;
+  p.num_pages = a->num_pages;
+  p.scale_log2 = (float)(a->scale * 1.4426950408889634);
+  p.q = a->q;
+  p.q_row = a->q_row_stride;
+  p.q_head = a->q_head_stride;
+  p.k = a->k;
+  p.k_page = a->k_page_stride;
+  p.k_head = a->k_head_stride;
+  p.k_tok = a->k_token_stride;
+  p.v = a->v;
+  p.v_page = a->v_page_stride;
+  p.v_head = a->v_head_stride;
+  p.v_tok = a->v_token_stride;
+  p.table = a->page_table;
+  p.table_stride = a->page_table_stride;
+  p.seq_len = a->seq_len;
+  p.num_draft = a->num_draft;
+  p.seqs = a->seqs;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.status = a->status;
+  p.parts = static_cast<float*>(a->workspace);
+  p.desc = static_cast<char*>(a->workspace) + s.blocks * s.part_bytes;
+  hipError_t e = sv::launch_attention(p, s.row_tiles, s.blocks, (hipStream_t)hip_stream);
   if (e != hipSuccess) return hip_fail(who, e);
   return SV_OK;
 }

@@ -181,3 +181,34 @@ def test_token_logprobs_rejects_bad_arguments():
         a = _lib.SpecVerifyLogprobsArgs(**{**good, **bad})
         assert call(ctypes.byref(a), None) == _lib.SV_ERR_INVALID, bad
         assert b"spec_verify_token_logprobs" in lib.spec_verify_last_error(), bad
+
+
+def test_paged_attention_rejects_bad_arguments():
+    _lib, lib = _lib_loaded()
+    call, ws = lib.spec_verify_paged_attention, lib.spec_verify_attention_workspace
+    assert call(None, None) == ws(None) == _lib.SV_ERR_INVALID
+    good = dict(batch=2, total_rows=6, heads=8, kv_heads=2, head_dim=128, dtype=_lib.SV_BF16, page_size=16, num_pages=10, slots=2,
+                max_pages=4, page_table_stride=4, q=0x1000, q_row_stride=1024, q_head_stride=128, k=0x1000, k_page_stride=4096,
+                k_head_stride=2048, k_token_stride=128, v=0x1000, v_page_stride=4096, v_head_stride=2048, v_token_stride=128,
+                page_table=0x1000, seq_len=0x1000, num_draft=0x1000, scale=0.1, out=0x1000, workspace=0x1000,
+                workspace_bytes=1 << 30)
+    a = _lib.SpecVerifyAttentionArgs(**good)
+    assert ws(ctypes.byref(a)) > 0
+    sizes = [dict(batch=-1), dict(batch=4097, total_rows=5000), dict(total_rows=1), dict(total_rows=524289), dict(heads=7),
+             dict(kv_heads=0), dict(heads=0), dict(heads=514, kv_heads=2), dict(head_dim=96), dict(dtype=_lib.SV_F32), dict(page_size=8),
+             dict(page_size=48), dict(page_size=2048), dict(num_pages=0), dict(num_pages=1 << 31), dict(slots=0),
+             dict(max_pages=0), dict(max_pages=1 << 30), dict(window=-1),
+             dict(batch=4096, total_rows=500000, heads=256, kv_heads=256, max_pages=60000)]
+    for bad in sizes:
+        a = _lib.SpecVerifyAttentionArgs(**{**good, **bad})
+        assert ws(ctypes.byref(a)) == _lib.SV_ERR_INVALID, bad
+    for bad in sizes + [dict(q=None), dict(k=None), dict(v=None), dict(page_table=None), dict(seq_len=None),
+                        dict(num_draft=None), dict(out=None), dict(q=0x1008), dict(k=0x1002), dict(v=0x1004), dict(out=0x1008),
+                        dict(q_row_stride=1020), dict(q_head_stride=-8), dict(k_page_stride=4), dict(k_token_stride=1 << 25),
+                        dict(v_head_stride=1), dict(v_token_stride=12), dict(page_table_stride=3), dict(scale=float("nan")),
+                        dict(scale=float("inf")), dict(workspace=None), dict(workspace=0x1001), dict(workspace_bytes=100)]:
+        a = _lib.SpecVerifyAttentionArgs(**{**good, **bad})
+        assert call(ctypes.byref(a), None) == _lib.SV_ERR_INVALID, bad
+        assert b"spec_verify_" in lib.spec_verify_last_error()
+    a = _lib.SpecVerifyAttentionArgs(**{**good, "batch": 0, "total_rows": 0})
+    assert call(ctypes.byref(a), None) == _lib.SV_OK                     # no sequences: nothing to do
