@@ -118,7 +118,8 @@ enum {
   /* the paged cache's operators only */
   SV_ST_BAD_SEQ = 256,         /* a sequence slot outside the cache, or named twice where it may be named once */
   SV_ST_BAD_LENGTH = 512,      /* a length or token count that is negative or does not fit */
-  SV_ST_BAD_PAGE = 1024        /* a page outside the pool */
+  SV_ST_BAD_PAGE = 1024,       /* a page outside the pool */
+  SV_ST_CACHE_FULL = 2048      /* the pool has too few free pages */
 };
 
 /* smallest accepted temperature for SAMPLE/ONEHOT/STRICT (float32 1e-6) */
@@ -521,6 +522,100 @@ int64_t spec_verify_attention_workspace(const spec_verify_attention_args* args);
 
 /* sizeof(spec_verify_attention_args) as compiled into the library. */
 int64_t spec_verify_attention_args_size(void);
+
+/* ---- the paged cache ---------------------------------------------------------
+ * The pages that spec_verify_paged_attention reads, and what a decode loop
+ * does with them around a verify call: reserve places for the K_s + 1 new
+ * tokens of each sequence, write their keys and values (per layer), and after
+ * the verify call commit what it accepted; fork a sequence into branches that
+ * share its pages, release one, compact the pool.
+ *
+ * State, device memory owned by the caller, who starts it with page_table -1,
+ * seq_len 0 and refcount 0:
+ *   page_table  [slots][max_pages] int32: the sequence's pages in order, -1 behind them
+ *   seq_len     [slots] int32: cached tokens
+ *   refcount    [num_pages] int32, 16-byte aligned: sequences that use the page; 0: free
+ *   k, v        [layers][num_pages][kv_heads][page_size][head_dim] of a 16-bit
+ *               type, 16-byte aligned
+ *   workspace   16-byte aligned, spec_verify_cache_workspace() bytes
+ * slots <= SV_CACHE_MAX_SLOTS, max_pages <= 131072, page_size a power of two
+ * from 16 to 1024, head_dim a multiple of 8, kv_heads * head_dim <= 65536,
+ * num_pages < 2^30, layers <= 4096.
+ *
+ * Calls on one cache must be ordered on one stream (they change its state and
+ * share its workspace).  Each names its sequences with seqs, int32 [batch]
+ * (NULL: slots 0 .. batch - 1); a slot outside the cache, or named by an
+ * earlier entry of the same call, gets SV_ST_BAD_SEQ.  A refused entry
+ * changes nothing; status (int32 [batch] or NULL) says why, 0 where the entry
+ * was carried out.  What a call does depends on the state and the arguments
+ * alone: the lowest free pages are taken first, entry by entry.
+ *
+ * spec_verify_cache_reserve: entry b grows by num_new[b] >= 0 tokens, packed
+ * total_new = sum num_new <= 524288 (otherwise SV_ST_BAD_LAYOUT for every
+ * entry, nothing changes).  start[b] is its old length (-1: refused), slots
+ * (int64 [total_new]) the place of each new token, page * page_size + offset
+ * (-1: refused).  A partly filled last page that other sequences use too is
+ * first copied to a page of its own, in every layer.  SV_ST_BAD_LENGTH: the
+ * table row would be too short; SV_ST_CACHE_FULL: too few free pages (so are
+ * the entries behind it that need any).
+ * spec_verify_cache_truncate: entry b loses its last drop[b] tokens, or all
+ * of them with drop == NULL; pages that hold none of its tokens any more
+ * lose it as a user.  SV_ST_BAD_LENGTH: drop outside 0 .. length.
+ * spec_verify_cache_commit: entry b, which reserved num_draft[b] + 1 tokens,
+ * keeps accepted_len[b] + 1 of them (its last emitted token and the accepted
+ * drafts; the token the verify call drew is the next round's first), or none
+ * for accepted_len[b] = -1 (not verified).
+ * spec_verify_cache_fork: slot children[b], of length 0, gets the length and
+ * pages of slot parents[b] (which may be named more than once), as they were
+ * before the call.  SV_ST_BAD_LENGTH: the child is not empty.
+ * spec_verify_cache_compact: the pages in use move, in order, to the front of
+ * the pool: afterwards pages 0 .. live - 1 are in use and the others free;
+ * live is int32 [1] or NULL.  Places handed out before are void.
+ * spec_verify_cache_write: row r of k_new and v_new, [rows][kv_heads]
+ * [head_dim] with strides in elements (multiples of 8, 16-byte aligned), goes
+ * to slots[r] of a layer; places outside the pool (-1) are left out, and no
+ * place may be named twice.
+ *
+ * All enqueue one or two kernels on `hip_stream`, which belongs to the
+ * calling thread's current device, allocate nothing and do not synchronise;
+ * SV_ERR_INVALID (nothing enqueued) for sizes outside their range or a
+ * missing or misaligned buffer; batch 0 and rows 0 are no-ops. */
+#define SV_CACHE_MAX_SLOTS 4096
+typedef struct spec_verify_cache {
+  int32_t slots;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t layers;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t* page_table;
+  int32_t* seq_len;
+  int32_t* refcount;
+  void* k;
+  void* v;
+  void* workspace;
+  int64_t workspace_bytes;
+} spec_verify_cache;
+int spec_verify_cache_reserve(const spec_verify_cache* cache, int32_t batch, const int32_t* seqs, const int32_t* num_new,
+                              int64_t total_new, int32_t* start, int64_t* slots, int32_t* status, void* hip_stream);
+int spec_verify_cache_truncate(const spec_verify_cache* cache, int32_t batch, const int32_t* seqs, const int32_t* drop,
+                               int32_t* status, void* hip_stream);
+int spec_verify_cache_commit(const spec_verify_cache* cache, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
+                             const int32_t* accepted_len, int32_t* status, void* hip_stream);
+int spec_verify_cache_fork(const spec_verify_cache* cache, int32_t batch, const int32_t* parents, const int32_t* children,
+                           int32_t* status, void* hip_stream);
+int spec_verify_cache_compact(const spec_verify_cache* cache, int32_t* live, void* hip_stream);
+int spec_verify_cache_write(const spec_verify_cache* cache, int32_t layer, int64_t rows, const void* k_new,
+                            int64_t k_row_stride, int64_t k_head_stride, const void* v_new, int64_t v_row_stride,
+                            int64_t v_head_stride, const int64_t* slots, void* hip_stream);
+
+/* Bytes of workspace for a cache with these sizes (its pointers are not
+ * looked at), or SV_ERR_INVALID. */
+int64_t spec_verify_cache_workspace(const spec_verify_cache* cache);
+
+/* sizeof(spec_verify_cache) as compiled into the library. */
+int64_t spec_verify_cache_size(void);
 
 /* Library version string. */
 const char* spec_verify_version(void);

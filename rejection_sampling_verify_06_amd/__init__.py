@@ -22,13 +22,14 @@ from ._lib import (  # noqa: F401
     SV_F32, SV_BF16, SV_F16, SV_SAMPLE, SV_GREEDY, SV_ONEHOT, SV_STRICT,
     SV_ST_BAD_LAYOUT, SV_ST_K_TOO_LARGE, SV_ST_BAD_MODE, SV_ST_BAD_TEMPERATURE,
     SV_ST_NO_DRAFT_LOGITS, SV_ST_BAD_TOKEN, SV_ST_NONFINITE, SV_ST_ZERO_RESIDUAL,
-    SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH, SV_ST_BAD_PAGE,
+    SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH, SV_ST_BAD_PAGE, SV_ST_CACHE_FULL,
     KERNEL_NAMES, LibraryMissing,
     SV_ADAPT_WINDOW, SV_ADAPT_MULTIPLICATIVE, SV_ADAPT_OPTIMAL_K, SV_ADAPT_COUNT_EMITTED, SV_ADAPT_COUNT_DRAFT_ONLY,
 )
 
 __all__ = ["Verifier", "VerifyError", "verify", "propose_ngram", "NgramProposer", "AcceptanceStats",
-           "DraftLengthController", "token_logprobs", "paged_attention", "LibraryMissing", "KERNEL_NAMES"]
+           "DraftLengthController", "token_logprobs", "paged_attention", "PagedCache",
+           "LibraryMissing", "KERNEL_NAMES"]
 
 
 class VerifyError(RuntimeError):
@@ -528,6 +529,160 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
 def _page_strides(t):
     """Page, head and token strides; those of a dimension of size 1 say nothing."""
     return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
+
+
+class PagedCache:
+    """A paged key-value cache on the device (spec_verify_cache_*): ``k`` and
+    ``v`` [layers, num_pages, kv_heads, page_size, head_dim], ``page_table``
+    int32 [max_seqs, max_pages] (-1 behind a sequence's pages), ``seq_len``
+    int32 [max_seqs], ``refcount`` int32 [num_pages] (0: free).
+
+    A round of speculative decoding over it:
+
+        r = cache.reserve(seqs, num_draft + 1, total)      # places for the new tokens
+        cache.write(layer, k_new, v_new, r["slots"])       # every layer, before it attends
+        o = cache.attend(layer, q, num_draft, seqs)
+        ...                                                # logits, Verifier.run
+        cache.commit(seqs, num_draft, out["accepted_len"]) # the rejected tokens leave
+
+    ``seqs`` (int32 [batch], distinct slots, or None for 0 .. batch - 1) and
+    the counts are device tensors; nothing here waits for the device.  The
+    calls return a status per entry (0, or SV_ST_* bits of why it was refused
+    and changed nothing).  Calls on one cache must be ordered on one stream."""
+
+    def __init__(self, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
+                 max_pages: int, dtype=None, device=None):
+        import torch
+        self._torch, self._lib = torch, _lib.load()
+        dtype = torch.bfloat16 if dtype is None else dtype
+        dev = torch.device("cuda", 0) if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError(f"the cache lives on a GPU, not on {dev}")
+        dev = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"cached keys and values are bfloat16 or float16, got {dtype}")
+        c = _lib.SpecVerifyCache(int(max_seqs), int(max_pages), int(page_size), int(num_pages), int(layers), int(kv_heads),
+                                 int(head_dim))
+        nbytes = self._lib.spec_verify_cache_workspace(ctypes.byref(c))
+        if nbytes < 0:
+            _check(int(nbytes))
+        self.device, self.layers, self.page_size = dev, int(layers), int(page_size)
+        shape = (c.layers, c.num_pages, c.kv_heads, c.page_size, c.head_dim)
+        self.k = torch.empty(shape, dtype=dtype, device=dev)
+        self.v = torch.empty(shape, dtype=dtype, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.page_table = torch.full((c.slots, c.max_pages), -1, **i32)
+        self.seq_len = torch.zeros(c.slots, **i32)
+        self.refcount = torch.zeros(c.num_pages, **i32)
+        self._ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        c.page_table, c.seq_len, c.refcount = _ptr(self.page_table), _ptr(self.seq_len), _ptr(self.refcount)
+        c.k, c.v, c.workspace, c.workspace_bytes = _ptr(self.k), _ptr(self.v), _ptr(self._ws), nbytes
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+    def _queue(self):
+        return self._torch.cuda.current_stream(self.device).cuda_stream
+
+    def _entries(self, seqs, counts, name):
+        """The batch size, with the index arrays checked."""
+        torch = self._torch
+        _need(counts, name, (torch.int32,), torch, None, self.device)
+        B = int(counts.numel())
+        _need(seqs, "seqs", (torch.int32,), torch, B, self.device)
+        return B
+
+    def reserve(self, seqs, num_new, total_new: int, stream=None) -> dict:
+        """Grows each sequence by ``num_new`` tokens (int32 [batch], summing to
+        ``total_new``).  Returns ``start`` (int32 [batch]: the old lengths),
+        ``slots`` (int64 [total_new]: the new tokens' places, for ``write``)
+        and ``status``; -1 in the first two where an entry was refused."""
+        torch = self._torch
+        B, n = self._entries(seqs, num_new, "num_new"), int(total_new)
+        with _on_stream(self.device, stream):
+            out = {"start": torch.empty(B, dtype=torch.int32, device=self.device),
+                   "slots": torch.empty(max(n, 0), dtype=torch.int64, device=self.device),
+                   "status": torch.empty(B, dtype=torch.int32, device=self.device)}
+            _check(self._lib.spec_verify_cache_reserve(self._ref, B, _ptr(seqs), num_new.data_ptr(), n, _ptr(out["start"]),
+                                                       _ptr(out["slots"]), _ptr(out["status"]), self._queue()))
+        return out
+
+    def write(self, layer: int, k_new, v_new, slots, stream=None):
+        """Puts rows of ``k_new`` / ``v_new`` ([rows, kv_heads, head_dim], unit
+        stride in head_dim) into the places ``slots`` of ``reserve``."""
+        torch = self._torch
+        rows = int(slots.numel())
+        _need(slots, "slots", (torch.int64,), torch, None, self.device)
+        for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+            if tuple(t.shape) != (rows, self._c.kv_heads, self._c.head_dim) or t.stride(2) != 1:
+                raise ValueError(f"{name} must be [{rows}, {self._c.kv_heads}, {self._c.head_dim}] with unit stride in the last "
+                                 f"dimension, got {tuple(t.shape)}")
+            if t.dtype != self.k.dtype:
+                raise TypeError(f"{name} is {t.dtype}, the cache {self.k.dtype}")
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        one = self._c.kv_heads == 1
+        with _on_stream(self.device, stream):
+            _check(self._lib.spec_verify_cache_write(
+                self._ref, int(layer), rows, k_new.data_ptr(), k_new.stride(0) if rows > 1 else 0, 0 if one else k_new.stride(1),
+                v_new.data_ptr(), v_new.stride(0) if rows > 1 else 0, 0 if one else v_new.stride(1), slots.data_ptr(),
+                self._queue()))
+
+    def attend(self, layer: int, q, num_draft, seqs=None, **kw) -> dict:
+        """``paged_attention`` of ``q`` over a layer of this cache."""
+        if not 0 <= int(layer) < self.layers:
+            raise ValueError(f"layer {layer} outside 0..{self.layers - 1}")
+        return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, num_draft, seqs=seqs, **kw)
+
+    def commit(self, seqs, num_draft, accepted_len, stream=None):
+        """Keeps ``accepted_len`` + 1 of the ``num_draft`` + 1 tokens each
+        sequence reserved for its round (none where it is -1: not verified)."""
+        torch = self._torch
+        B = self._entries(seqs, num_draft, "num_draft")
+        _need(accepted_len, "accepted_len", (torch.int32,), torch, B, self.device)
+        with _on_stream(self.device, stream):
+            status = torch.empty(B, dtype=torch.int32, device=self.device)
+            _check(self._lib.spec_verify_cache_commit(self._ref, B, _ptr(seqs), num_draft.data_ptr(), accepted_len.data_ptr(),
+                                                      _ptr(status), self._queue()))
+        return status
+
+    def truncate(self, seqs, drop, stream=None):
+        """Takes the last ``drop`` tokens (int32 [batch]) off each sequence."""
+        torch = self._torch
+        B = self._entries(seqs, drop, "drop")
+        with _on_stream(self.device, stream):
+            status = torch.empty(B, dtype=torch.int32, device=self.device)
+            _check(self._lib.spec_verify_cache_truncate(self._ref, B, _ptr(seqs), drop.data_ptr() if B else None,
+                                                        _ptr(status), self._queue()))
+        return status
+
+    def release(self, seqs, stream=None):
+        """Empties the sequences (int32 [batch])."""
+        torch = self._torch
+        B = self._entries(None, seqs, "seqs")
+        with _on_stream(self.device, stream):
+            status = torch.empty(B, dtype=torch.int32, device=self.device)
+            _check(self._lib.spec_verify_cache_truncate(self._ref, B, seqs.data_ptr(), None, _ptr(status), self._queue()))
+        return status
+
+    def fork(self, parents, children, stream=None):
+        """The empty slots ``children`` share everything ``parents`` hold (both
+        int32 [batch]; a parent may be named more than once)."""
+        torch = self._torch
+        B = self._entries(children, parents, "parents")
+        with _on_stream(self.device, stream):
+            status = torch.empty(B, dtype=torch.int32, device=self.device)
+            _check(self._lib.spec_verify_cache_fork(self._ref, B, parents.data_ptr(), children.data_ptr(), _ptr(status),
+                                                    self._queue()))
+        return status
+
+    def compact(self, stream=None):
+        """Moves the pages in use to the front of the pool; returns their
+        number (int32 [1]).  ``slots`` handed out before are void."""
+        torch = self._torch
+        with _on_stream(self.device, stream):
+            live = torch.empty(1, dtype=torch.int32, device=self.device)
+            _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), self._queue()))
+        return live
 
 
 def library_loaded_path() -> str:

@@ -21,6 +21,7 @@ SV_ST_ZERO_RESIDUAL = 128
 SV_ST_BAD_SEQ = 256
 SV_ST_BAD_LENGTH = 512
 SV_ST_BAD_PAGE = 1024
+SV_ST_CACHE_FULL = 2048
 SV_NUM_KERNELS = 4
 KERNEL_NAMES = ("row_stats", "filter", "final", "select")
 
@@ -53,7 +54,10 @@ EXPORTED = (
     "spec_verify_adapt_args_size", "spec_verify_run_noalloc",
     "spec_verify_token_logprobs", "spec_verify_logprobs_workspace", "spec_verify_logprobs_args_size",
     "spec_verify_paged_attention", "spec_verify_attention_workspace", "spec_verify_attention_args_size",
+    "spec_verify_cache_reserve", "spec_verify_cache_truncate", "spec_verify_cache_commit", "spec_verify_cache_fork",
+    "spec_verify_cache_compact", "spec_verify_cache_write", "spec_verify_cache_workspace", "spec_verify_cache_size",
 )
+SV_CACHE_MAX_SLOTS = 4096
 SV_LOGPROBS_MAX_TOP = 64
 SV_NOALLOC_SCRATCH_BYTES = 67108864
 
@@ -177,6 +181,25 @@ class SpecVerifyAttentionArgs(ctypes.Structure):
     ]
 
 
+class SpecVerifyCache(ctypes.Structure):
+    _fields_ = [
+        ("slots", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("layers", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _LIB = None
 
 
@@ -241,6 +264,16 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_attention_workspace.restype = ctypes.c_int64
     lib.spec_verify_attention_args_size.argtypes = []
     lib.spec_verify_attention_args_size.restype = ctypes.c_int64
+    C, i32, i64 = ctypes.POINTER(SpecVerifyCache), ctypes.c_int32, ctypes.c_int64
+    for name, types in (("reserve", [C, i32, P, P, i64, P, P, P, P]), ("truncate", [C, i32, P, P, P, P]),
+                        ("commit", [C, i32, P, P, P, P, P]), ("fork", [C, i32, P, P, P, P]), ("compact", [C, P, P]),
+                        ("write", [C, i32, i64, P, i64, i64, P, i64, i64, P, P])):
+        f = getattr(lib, "spec_verify_cache_" + name)
+        f.argtypes, f.restype = types, ctypes.c_int
+    lib.spec_verify_cache_workspace.argtypes = [C]
+    lib.spec_verify_cache_workspace.restype = ctypes.c_int64
+    lib.spec_verify_cache_size.argtypes = []
+    lib.spec_verify_cache_size.restype = ctypes.c_int64
     if lib.spec_verify_args_size() != ctypes.sizeof(SpecVerifyArgs):
         raise RuntimeError("spec_verify_args layout differs between the library and the binding")
     if lib.spec_verify_ngram_args_size() != ctypes.sizeof(SpecVerifyNgramArgs):
@@ -251,6 +284,8 @@ def load() -> ctypes.CDLL:
         raise RuntimeError("spec_verify_logprobs_args layout differs between the library and the binding")
     if lib.spec_verify_attention_args_size() != ctypes.sizeof(SpecVerifyAttentionArgs):
         raise RuntimeError("spec_verify_attention_args layout differs between the library and the binding")
+    if lib.spec_verify_cache_size() != ctypes.sizeof(SpecVerifyCache):
+        raise RuntimeError("spec_verify_cache layout differs between the library and the binding")
     _LIB = lib
     return lib
 

@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_NAME = "libspec_verify.so"
 SOURCES = ["csrc/sv_kernels.hip", "csrc/sv_ngram.hip", "csrc/sv_stats.hip", "csrc/sv_filter.hip", "csrc/sv_noalloc.hip",
-           "csrc/sv_logprobs.hip", "csrc/sv_attention.hip", "csrc/sv_api.cpp", "csrc/sv_serving_api.cpp"]
+           "csrc/sv_logprobs.hip", "csrc/sv_attention.hip", "csrc/sv_cache.hip", "csrc/sv_api.cpp", "csrc/sv_serving_api.cpp"]
 ARCH = "gfx950"
 
 

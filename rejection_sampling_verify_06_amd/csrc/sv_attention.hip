@@ -133,16 +133,6 @@ __device__ __forceinline__ Extent seq_extent(const AttnParams& P, int b, int n) 
   return x;
 }
 
-__device__ __forceinline__ uint32_t wave_incl_scan_u32(uint32_t v) {
-  v += (uint32_t)dpp_i<kDppRowShr1>(0, (int)v);
-  v += (uint32_t)dpp_i<kDppRowShr2>(0, (int)v);
-  v += (uint32_t)dpp_i<kDppRowShr4>(0, (int)v);
-  v += (uint32_t)dpp_i<kDppRowShr8>(0, (int)v);
-  v += (uint32_t)dpp_i<kDppRowBcast15, 0xA>(0, (int)v);
-  v += (uint32_t)dpp_i<kDppRowBcast31, 0xC>(0, (int)v);
-  return v;
-}
-
 __device__ __forceinline__ bool plan(const AttnParams& P, int TM, uint32_t* rows, uint32_t* units) {
   __shared__ uint32_t tr[kAtWaves], tu[kAtWaves];
   __shared__ int bad;

@@ -252,6 +252,60 @@ struct AttnParams {
 
 hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 
+// the paged cache's own operations (sv_cache.hip)
+constexpr int kCacheMaxSlots = 4096;
+constexpr int kCacheMaxRows = 524288;   // new tokens of a call
+
+struct CacheParams {
+  int32_t B;
+  int32_t slots;
+  int32_t max_pages;
+  int32_t page_size, page_log2;
+  int32_t num_pages;
+  int32_t max_len;                  // max_pages * page_size
+  int32_t layers;
+  int32_t* table;                   // [slots][max_pages]
+  int32_t* seq_len;                 // [slots]
+  int32_t* refcount;                // [num_pages]
+  void* k;                          // [layers][num_pages] pages of page_bytes
+  void* v;
+  int64_t page_bytes, layer_bytes;
+  const int32_t* seqs;              // or NULL (fork: the parents)
+  const int32_t* num_new;           // reserve
+  int64_t total_new;
+  int32_t* start;
+  int64_t* new_slots;
+  const int32_t* drop;              // truncate: these, or what num_draft / accepted say, or all
+  const int32_t* num_draft;
+  const int32_t* accepted;
+  const int32_t* children;          // fork
+  int32_t* live;                    // compact, or NULL
+  int32_t* status;                  // or NULL
+  int32_t* count;                   // workspace: entries of pairs
+  int32_t* ids;                     // workspace: [num_pages]
+  int2* pairs;                      // workspace: [max(num_pages, slots)] copies (from, to)
+};
+
+struct CacheWriteParams {
+  int64_t rows;
+  int64_t places;                   // num_pages * page_size
+  int32_t kv_heads, head_dim;
+  int32_t vecs, head_vecs;          // 16-byte vectors of a row, and of a head's part of it
+  int32_t page_log2;
+  void* k;                          // one layer's pages
+  void* v;
+  const void* k_new;
+  const void* v_new;
+  int64_t k_row, k_head, v_row, v_head;   // strides in elements
+  const int64_t* new_slots;
+};
+
+hipError_t launch_cache_reserve(const CacheParams& p, hipStream_t st);
+hipError_t launch_cache_truncate(const CacheParams& p, hipStream_t st);
+hipError_t launch_cache_fork(const CacheParams& p, hipStream_t st);
+hipError_t launch_cache_compact(const CacheParams& p, hipStream_t st);
+hipError_t launch_cache_write(const CacheWriteParams& p, hipStream_t st);
+
 // ---- host side shared by the entry points (sv_api.cpp) ----------------------
 
 // Sizes a verify call may use: those of a context, or of one allocation-free call.

@@ -1,5 +1,5 @@
 // Host side of the serving operators declared in include/spec_verify.h (token
-// log probabilities, attention over a paged cache): argument validation and workspace layout.
+// log probabilities, attention over a paged cache, the cache itself): argument validation and workspace layout.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -109,6 +109,75 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool strides_ok(int64_t a, int64_t b, int64_t c) {
   for (int64_t x : {a, b, c})
     if (x < 0 || x % 8 || x > (int64_t)1 << 40) return false;
+  return true;
+}
+
+// workspace of a cache: the list's length, the ids, the list
+struct CacheLayout {
+  int64_t ids, pairs, bytes;
+};
+
+bool cache_sizes_ok(const char* who, const spec_verify_cache* c, CacheLayout* l) {
+  if (!c) {
+    set_err("%s: cache is NULL", who);
+    return false;
+  }
+  if (c->slots < 1 || c->slots > SV_CACHE_MAX_SLOTS || c->max_pages < 1 || c->max_pages > 131072 || c->num_pages < 1 ||
+      c->num_pages >= 1 << 30 || c->layers < 1 || c->layers > 4096) {
+    set_err("%s: slots %d, max_pages %d, num_pages %d or layers %d outside their range", who, c->slots, c->max_pages,
+            c->num_pages, c->layers);
+    return false;
+  }
+  if (!is_pow2(c->page_size) || c->page_size < 16 || c->page_size > 1024) {
+    set_err("%s: page_size %d is not a power of two from 16 to 1024", who, c->page_size);
+    return false;
+  }
+  if (c->kv_heads < 1 || c->head_dim < 8 || c->head_dim % 8 || (int64_t)c->kv_heads * c->head_dim > 65536) {
+    set_err("%s: head_dim %d is not a multiple of 8, or kv_heads %d * head_dim outside 1..65536", who, c->head_dim,
+            c->kv_heads);
+    return false;
+  }
+  static_assert(SV_CACHE_MAX_SLOTS == sv::kCacheMaxSlots, "slots");
+  l->ids = 256;
+  l->pairs = l->ids + (int64_t)sv::align_up((size_t)c->num_pages * 4, 256);
+  l->bytes = l->pairs + (int64_t)std::max(c->num_pages, c->slots) * 8;
+  return true;
+}
+
+// The checks every call on a cache shares, and its parameters.
+bool cache_params(const char* who, const spec_verify_cache* c, int32_t batch, sv::CacheParams* p) {
+  CacheLayout l;
+  if (!cache_sizes_ok(who, c, &l)) return false;
+  if (!c->page_table || !c->seq_len || !c->refcount || !c->k || !c->v || !c->workspace || !aligned16(c->refcount) ||
+      !aligned16(c->k) || !aligned16(c->v) || !aligned16(c->workspace) || c->workspace_bytes < l.bytes) {
+    set_err("%s: page_table, seq_len, refcount, k, v (the last three 16-byte aligned) and a workspace of %lld bytes "
+            "are required", who, (long long)l.bytes);
+    return false;
+  }
+  if (batch < 0 || batch > c->slots) {
+    set_err("%s: batch %d outside 0..%d slots", who, batch, c->slots);
+    return false;
+  }
+  *p = sv::CacheParams{};
+  p->B = batch;
+  p->slots = c->slots;
+  p->max_pages = c->max_pages;
+  p->page_size = c->page_size;
+  p->page_log2 = __builtin_ctz((unsigned)c->page_size);
+  p->num_pages = c->num_pages;
+  p->max_len = c->max_pages * c->page_size;
+  p->layers = c->layers;
+  p->table = c->page_table;
+  p->seq_len = c->seq_len;
+  p->refcount = c->refcount;
+  p->k = c->k;
+  p->v = c->v;
+  p->page_bytes = (int64_t)c->kv_heads * c->head_dim * c->page_size * 2;
+  p->layer_bytes = p->page_bytes * c->num_pages;
+  char* ws = static_cast<char*>(c->workspace);
+  p->count = reinterpret_cast<int32_t*>(ws);
+  p->ids = reinterpret_cast<int32_t*>(ws + l.ids);
+  p->pairs = reinterpret_cast<int2*>(ws + l.pairs);
   return true;
 }
 
@@ -252,6 +321,129 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
   hipError_t e = sv::launch_attention(p, s.row_tiles, s.blocks, (hipStream_t)hip_stream);
   if (e != hipSuccess) return hip_fail(who, e);
   return SV_OK;
+}
+
+int64_t spec_verify_cache_size(void) { return (int64_t)sizeof(spec_verify_cache); }
+
+int64_t spec_verify_cache_workspace(const spec_verify_cache* c) {
+  CacheLayout l;
+  return cache_sizes_ok("spec_verify_cache_workspace", c, &l) ? l.bytes : SV_ERR_INVALID;
+}
+
+int spec_verify_cache_reserve(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_new,
+                              int64_t total_new, int32_t* start, int64_t* slots, int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_reserve";
+  sv::CacheParams p;
+  if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
+  if (batch == 0) return SV_OK;
+  if (!num_new || !start || total_new < 0 || total_new > sv::kCacheMaxRows || (total_new > 0 && !slots)) {
+    set_err("%s: num_new, start and slots are required, total_new %lld in 0..%d", who, (long long)total_new,
+            sv::kCacheMaxRows);
+    return SV_ERR_INVALID;
+  }
+  p.seqs = seqs;
+  p.num_new = num_new;
+  p.total_new = total_new;
+  p.start = start;
+  p.new_slots = slots;
+  p.status = status;
+  hipError_t e = sv::launch_cache_reserve(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_truncate(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* drop,
+                               int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_truncate";
+  sv::CacheParams p;
+  if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
+  if (batch == 0) return SV_OK;
+  p.seqs = seqs;
+  p.drop = drop;
+  p.status = status;
+  hipError_t e = sv::launch_cache_truncate(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_commit(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
+                             const int32_t* accepted_len, int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_commit";
+  sv::CacheParams p;
+  if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
+  if (batch == 0) return SV_OK;
+  if (!num_draft || !accepted_len) {
+    set_err("%s: num_draft and accepted_len are required", who);
+    return SV_ERR_INVALID;
+  }
+  p.seqs = seqs;
+  p.num_draft = num_draft;
+  p.accepted = accepted_len;
+  p.status = status;
+  hipError_t e = sv::launch_cache_truncate(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_fork(const spec_verify_cache* c, int32_t batch, const int32_t* parents, const int32_t* children,
+                           int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_fork";
+  sv::CacheParams p;
+  if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
+  if (batch == 0) return SV_OK;
+  if (!parents || !children) {
+    set_err("%s: parents and children are required", who);
+    return SV_ERR_INVALID;
+  }
+  p.seqs = parents;
+  p.children = children;
+  p.status = status;
+  hipError_t e = sv::launch_cache_fork(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_compact(const spec_verify_cache* c, int32_t* live, void* hip_stream) {
+  const char* who = "spec_verify_cache_compact";
+  sv::CacheParams p;
+  if (!cache_params(who, c, 0, &p)) return SV_ERR_INVALID;
+  p.live = live;
+  hipError_t e = sv::launch_cache_compact(p, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_write(const spec_verify_cache* c, int32_t layer, int64_t rows, const void* k_new,
+                            int64_t k_row_stride, int64_t k_head_stride, const void* v_new, int64_t v_row_stride,
+                            int64_t v_head_stride, const int64_t* slots, void* hip_stream) {
+  const char* who = "spec_verify_cache_write";
+  sv::CacheParams p;
+  if (!cache_params(who, c, 0, &p)) return SV_ERR_INVALID;
+  if (layer < 0 || layer >= c->layers || rows < 0 || rows > sv::kCacheMaxRows) {
+    set_err("%s: layer %d outside 0..%d, or rows %lld outside 0..%d", who, layer, c->layers - 1, (long long)rows,
+            sv::kCacheMaxRows);
+    return SV_ERR_INVALID;
+  }
+  if (rows == 0) return SV_OK;
+  if (!k_new || !v_new || !slots || !aligned16(k_new) || !aligned16(v_new) ||
+      !strides_ok(k_row_stride, k_head_stride, 0) || !strides_ok(v_row_stride, v_head_stride, 0)) {
+    set_err("%s: k_new and v_new (16-byte aligned, strides in multiples of 8 elements) and slots are required", who);
+    return SV_ERR_INVALID;
+  }
+  sv::CacheWriteParams w{};
+  w.rows = rows;
+  w.places = (int64_t)c->num_pages * c->page_size;
+  w.kv_heads = c->kv_heads;
+  w.head_dim = c->head_dim;
+  w.head_vecs = c->head_dim / 8;
+  w.vecs = c->kv_heads * w.head_vecs;
+  w.page_log2 = p.page_log2;
+  w.k = static_cast<char*>(c->k) + layer * p.layer_bytes;
+  w.v = static_cast<char*>(c->v) + layer * p.layer_bytes;
+  w.k_new = k_new;
+  w.v_new = v_new;
+  w.k_row = k_row_stride;
+  w.k_head = k_head_stride;
+  w.v_row = v_row_stride;
+  w.v_head = v_head_stride;
+  w.new_slots = slots;
+  hipError_t e = sv::launch_cache_write(w, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
 }
 
 }  // extern "C"

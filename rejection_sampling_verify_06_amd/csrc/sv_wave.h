@@ -96,6 +96,16 @@ __device__ __forceinline__ float wave_incl_scan_f(float v) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t wave_incl_scan_u32(uint32_t v) {
+  v += (uint32_t)dpp_i<kDppRowShr1>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr2>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr4>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowShr8>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowBcast15, 0xA>(0, (int)v);
+  v += (uint32_t)dpp_i<kDppRowBcast31, 0xC>(0, (int)v);
+  return v;
+}
+
 // maximum of an int over the wave, in every lane
 __device__ __forceinline__ int wave_max_i(int v) {
   const int n = (int)0x80000000u;

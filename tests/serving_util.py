@@ -83,3 +83,117 @@ def make_pages(L, P, KV, D, dtype, seed, layout="head", extra=3):
     def up(t):
         return t.cuda() if t.is_contiguous() else t.transpose(1, 2).contiguous().cuda().transpose(1, 2)
     return up(k), up(v), table.cuda(), torch.tensor(L, dtype=torch.int32).cuda()
+
+
+class CacheModel:
+    """The paged cache with Python lists and one token's (k, v) per place:
+    sequence by sequence, page by page."""
+
+    def __init__(self, c):
+        self.P, self.W, self.NP = c.page_size, c.page_table.shape[1], c.refcount.shape[0]
+        self.len = [0] * c.seq_len.shape[0]
+        self.pages = [[] for _ in self.len]
+        self.ref = [0] * self.NP
+        self.k, self.v = c.k.cpu().clone(), c.v.cpu().clone()
+
+    def _slots(self, seqs):
+        seen = set()
+        for s in seqs:
+            yield s, 0 <= s < len(self.len) and s not in seen
+            seen.add(s)
+
+    def reserve(self, seqs, new, total):
+        if any(n < 0 for n in new) or sum(new) != total:
+            return [-1] * len(seqs), [-1] * total, [1] * len(seqs)
+        before, start, slots, status, moves = list(self.ref), [], [], [], []
+        free = [p for p in range(self.NP) if before[p] == 0]
+        asked = 0
+        for (s, ok), n in zip(self._slots(seqs), new):
+            st = 0 if ok else 256
+            if ok and self.len[s] + n > self.W * self.P:
+                st = 512
+            if not st:
+                L = self.len[s]
+                cow = n > 0 and L % self.P > 0 and before[self.pages[s][-1]] > 1
+                need = -(-(L + n) // self.P) - len(self.pages[s]) + cow
+                asked += need
+                if need and asked > len(free):
+                    st = 2048
+            if st:
+                start.append(-1)
+                slots += [-1] * n
+            else:
+                take = free[asked - need:asked]
+                if cow:
+                    old = self.pages[s][-1]
+                    self.ref[old] -= 1
+                    self.pages[s][-1] = take[0]
+                    moves.append((old, take[0]))
+                self.pages[s] += take[cow:]
+                for p in take:
+                    self.ref[p] = 1
+                self.len[s] = L + n
+                start.append(L)
+                slots += [self.pages[s][j // self.P] * self.P + j % self.P for j in range(L, L + n)]
+            status.append(st)
+        self._move(moves)
+        return start, slots, status
+
+    def _move(self, moves):
+        if moves:
+            a, b = (torch.tensor(x) for x in zip(*moves))
+            self.k[:, b], self.v[:, b] = self.k[:, a].clone(), self.v[:, a].clone()
+
+    def write(self, layer, k, v, slots):
+        for r, s in enumerate(slots):
+            if s >= 0:
+                self.k[layer, s // self.P, :, s % self.P] = k[r]
+                self.v[layer, s // self.P, :, s % self.P] = v[r]
+
+    def truncate(self, seqs, drop):
+        status = []
+        for (s, ok), d in zip(self._slots(seqs), drop):
+            st = 256 if not ok else 512 if d is None or not 0 <= d <= self.len[s] else 0
+            if not st:
+                self.len[s] -= d
+                while len(self.pages[s]) > -(-self.len[s] // self.P):
+                    self.ref[self.pages[s].pop()] -= 1
+            status.append(st)
+        return status
+
+    def commit(self, seqs, K, A):
+        return self.truncate(seqs, [k - a if k >= 0 and -1 <= a <= k else None for k, a in zip(K, A)])
+
+    def release(self, seqs):
+        return self.truncate(seqs, [self.len[s] if 0 <= s < len(self.len) else 0 for s in seqs])
+
+    def fork(self, parents, children):
+        was = list(self.len)
+        status = []
+        for p, (c, ok) in zip(parents, list(self._slots(children))):
+            st = 256 if not ok or not 0 <= p < len(was) else 512 if was[c] else 0
+            if not st and was[p]:
+                self.len[c], self.pages[c] = was[p], list(self.pages[p])
+                for q in self.pages[p]:
+                    self.ref[q] += 1
+            status.append(st)
+        return status
+
+    def compact(self):
+        used = [p for p in range(self.NP) if self.ref[p]]
+        holes = [p for p in range(len(used)) if not self.ref[p]]
+        movers = [p for p in used if p >= len(used)]
+        self._move(list(zip(movers, holes)))
+        name = dict(zip(movers, holes))
+        for p, h in name.items():
+            self.ref[h], self.ref[p] = self.ref[p], 0
+        self.pages = [[name.get(p, p) for p in row] for row in self.pages]
+        return len(used)
+
+    def check(self, c):
+        assert c.seq_len.tolist() == self.len
+        assert c.refcount.tolist() == self.ref
+        want = [row + [-1] * (self.W - len(row)) for row in self.pages]
+        assert c.page_table.tolist() == want
+        assert torch.equal(c.k.cpu().view(torch.int16), self.k.view(torch.int16))
+        assert torch.equal(c.v.cpu().view(torch.int16), self.v.view(torch.int16))

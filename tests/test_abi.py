@@ -212,3 +212,50 @@ def test_paged_attention_rejects_bad_arguments():
         assert b"spec_verify_" in lib.spec_verify_last_error()
     a = _lib.SpecVerifyAttentionArgs(**{**good, "batch": 0, "total_rows": 0})
     assert call(ctypes.byref(a), None) == _lib.SV_OK                     # no sequences: nothing to do
+
+
+def test_cache_rejects_bad_arguments():
+    _lib, lib = _lib_loaded()
+    good = dict(slots=4, max_pages=8, page_size=16, num_pages=20, layers=2, kv_heads=2, head_dim=64, page_table=0x1000,
+                seq_len=0x1000, refcount=0x1000, k=0x1000, v=0x1000, workspace=0x1000, workspace_bytes=1 << 20)
+    P = 0x1000
+
+    def every(c):
+        r = ctypes.byref(c)
+        return [lib.spec_verify_cache_reserve(r, 2, P, P, 3, P, P, P, None), lib.spec_verify_cache_truncate(r, 2, P, P, P, None),
+                lib.spec_verify_cache_commit(r, 2, P, P, P, P, None), lib.spec_verify_cache_fork(r, 2, P, P, P, None),
+                lib.spec_verify_cache_compact(r, P, None), lib.spec_verify_cache_write(r, 0, 1, P, 128, 64, P, 128, 64, P, None)]
+    sizes = [dict(slots=0), dict(slots=4097), dict(max_pages=0), dict(max_pages=131073), dict(page_size=8), dict(page_size=17),
+             dict(page_size=2048), dict(num_pages=0), dict(num_pages=1 << 30), dict(layers=0), dict(layers=4097), dict(kv_heads=0),
+             dict(head_dim=0), dict(head_dim=12), dict(kv_heads=1024, head_dim=128)]
+    for bad in sizes:
+        c = _lib.SpecVerifyCache(**{**good, **bad})
+        assert lib.spec_verify_cache_workspace(ctypes.byref(c)) == _lib.SV_ERR_INVALID, bad
+    for bad in sizes + [dict(page_table=None), dict(seq_len=None), dict(refcount=None), dict(refcount=0x1004), dict(k=None), dict(v=None),
+                        dict(k=0x1008), dict(v=0x1002), dict(workspace=None), dict(workspace=0x1008), dict(workspace_bytes=64)]:
+        assert every(_lib.SpecVerifyCache(**{**good, **bad})) == [_lib.SV_ERR_INVALID] * 6, bad
+    c = _lib.SpecVerifyCache(**good)
+    r = ctypes.byref(c)
+    assert lib.spec_verify_cache_workspace(r) > 0
+    assert lib.spec_verify_cache_workspace(None) == _lib.SV_ERR_INVALID
+    INV, OK = _lib.SV_ERR_INVALID, _lib.SV_OK
+    for batch in (-1, 5):
+        assert lib.spec_verify_cache_reserve(r, batch, P, P, 3, P, P, P, None) == INV
+        assert lib.spec_verify_cache_truncate(r, batch, P, P, P, None) == INV
+        assert lib.spec_verify_cache_commit(r, batch, P, P, P, P, None) == INV
+        assert lib.spec_verify_cache_fork(r, batch, P, P, P, None) == INV
+    for num_new, total, start, slots in ((None, 3, P, P), (P, -1, P, P), (P, 524289, P, P), (P, 3, None, P), (P, 3, P, None)):
+        assert lib.spec_verify_cache_reserve(r, 2, P, num_new, total, start, slots, P, None) == INV
+    assert lib.spec_verify_cache_commit(r, 2, P, None, P, P, None) == INV
+    assert lib.spec_verify_cache_commit(r, 2, P, P, None, P, None) == INV
+    assert lib.spec_verify_cache_fork(r, 2, None, P, P, None) == INV
+    assert lib.spec_verify_cache_fork(r, 2, P, None, P, None) == INV
+    for a in ((-1, 1, P, 128, 64, P, 128, 64, P), (2, 1, P, 128, 64, P, 128, 64, P), (0, -1, P, 128, 64, P, 128, 64, P),
+              (0, 524289, P, 128, 64, P, 128, 64, P), (0, 1, None, 128, 64, P, 128, 64, P), (0, 1, P, 128, 64, None, 128, 64, P),
+              (0, 1, P, 128, 64, P, 128, 64, None), (0, 1, 0x1008, 128, 64, P, 128, 64, P), (0, 1, P, 127, 64, P, 128, 64, P),
+              (0, 1, P, 128, 64, P, 128, -64, P)):
+        assert lib.spec_verify_cache_write(r, *a, None) == INV, a
+        assert b"spec_verify_cache_write" in lib.spec_verify_last_error()
+    assert lib.spec_verify_cache_write(r, 0, 0, None, 0, 0, None, 0, 0, None, None) == OK
+    assert lib.spec_verify_cache_reserve(r, 0, None, None, 0, None, None, None, None) == OK
+    assert lib.spec_verify_cache_fork(r, 0, None, None, None, None) == OK
