@@ -14,6 +14,7 @@ there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -392,16 +393,24 @@ class DraftLengthController:
         return self.next_k
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
 def _on_stream(dev, stream):
-    """The stream a call queues on, as a context in which it is torch's
-    current one (so that what the call allocates belongs to it) and its
-    device the current device."""
+    """A context in which a call's stream is torch's current one (so that what
+    the call allocates belongs to it) and its device the current device."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _AS_IT_IS if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _queue(dev) -> int:
+    """The handle of torch's current stream on a device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab: Optional[int] = None,
@@ -451,7 +460,7 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab
             _ptr(temperature), _ptr(out["logprob"]), _ptr(out["entropy"]), _ptr(out["rank"]),
             out["top_tokens"].data_ptr() if top else None, out["top_logprobs"].data_ptr() if top else None,
             _ptr(out["status"]), ws.data_ptr(), nbytes)
-        _check(lib.spec_verify_token_logprobs(ctypes.byref(a), torch.cuda.current_stream(dev).cuda_stream))
+        _check(lib.spec_verify_token_logprobs(ctypes.byref(a), _queue(dev)))
     return out
 
 
@@ -522,7 +531,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         a.out, a.lse, a.status = out["out"].data_ptr(), _ptr(out["lse"]), _ptr(out["status"])
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
-        _check(lib.spec_verify_paged_attention(ctypes.byref(a), torch.cuda.current_stream(dev).cuda_stream))
+        _check(lib.spec_verify_paged_attention(ctypes.byref(a), _queue(dev)))
     return out
 
 
@@ -580,9 +589,6 @@ class PagedCache:
         self._c = c
         self._ref = ctypes.byref(c)
 
-    def _queue(self):
-        return self._torch.cuda.current_stream(self.device).cuda_stream
-
     def _entries(self, seqs, counts, name):
         """The batch size, with the index arrays checked."""
         torch = self._torch
@@ -603,7 +609,7 @@ class PagedCache:
                    "slots": torch.empty(max(n, 0), dtype=torch.int64, device=self.device),
                    "status": torch.empty(B, dtype=torch.int32, device=self.device)}
             _check(self._lib.spec_verify_cache_reserve(self._ref, B, _ptr(seqs), num_new.data_ptr(), n, _ptr(out["start"]),
-                                                       _ptr(out["slots"]), _ptr(out["status"]), self._queue()))
+                                                       _ptr(out["slots"]), _ptr(out["status"]), _queue(self.device)))
         return out
 
     def write(self, layer: int, k_new, v_new, slots, stream=None):
@@ -625,7 +631,7 @@ class PagedCache:
             _check(self._lib.spec_verify_cache_write(
                 self._ref, int(layer), rows, k_new.data_ptr(), k_new.stride(0) if rows > 1 else 0, 0 if one else k_new.stride(1),
                 v_new.data_ptr(), v_new.stride(0) if rows > 1 else 0, 0 if one else v_new.stride(1), slots.data_ptr(),
-                self._queue()))
+                _queue(self.device)))
 
     def attend(self, layer: int, q, num_draft, seqs=None, **kw) -> dict:
         """``paged_attention`` of ``q`` over a layer of this cache."""
@@ -642,7 +648,7 @@ class PagedCache:
         with _on_stream(self.device, stream):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_commit(self._ref, B, _ptr(seqs), num_draft.data_ptr(), accepted_len.data_ptr(),
-                                                      _ptr(status), self._queue()))
+                                                      _ptr(status), _queue(self.device)))
         return status
 
     def truncate(self, seqs, drop, stream=None):
@@ -652,7 +658,7 @@ class PagedCache:
         with _on_stream(self.device, stream):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_truncate(self._ref, B, _ptr(seqs), drop.data_ptr() if B else None,
-                                                        _ptr(status), self._queue()))
+                                                        _ptr(status), _queue(self.device)))
         return status
 
     def release(self, seqs, stream=None):
@@ -661,7 +667,7 @@ class PagedCache:
         B = self._entries(None, seqs, "seqs")
         with _on_stream(self.device, stream):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
-            _check(self._lib.spec_verify_cache_truncate(self._ref, B, seqs.data_ptr(), None, _ptr(status), self._queue()))
+            _check(self._lib.spec_verify_cache_truncate(self._ref, B, seqs.data_ptr(), None, _ptr(status), _queue(self.device)))
         return status
 
     def fork(self, parents, children, stream=None):
@@ -672,7 +678,7 @@ class PagedCache:
         with _on_stream(self.device, stream):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_fork(self._ref, B, parents.data_ptr(), children.data_ptr(), _ptr(status),
-                                                    self._queue()))
+                                                    _queue(self.device)))
         return status
 
     def compact(self, stream=None):
@@ -681,7 +687,7 @@ class PagedCache:
         torch = self._torch
         with _on_stream(self.device, stream):
             live = torch.empty(1, dtype=torch.int32, device=self.device)
-            _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), self._queue()))
+            _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), _queue(self.device)))
         return live
 
 

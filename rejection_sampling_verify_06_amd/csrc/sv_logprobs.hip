@@ -9,11 +9,11 @@
 //   top n     = the n largest logits, the lower index first on ties
 // One read of the logits carries all of it: k_logprob_chunks reduces 32 KB of
 // a row to (M, S, W, count) and the maximum of each 512-byte segment, and
-// k_logprob_rows merges a row's chunks and finds its top n.  A token of the
-// top n lies in one of the n first segments ordered by (maximum, index): a
-// segment behind n others has n tokens in front of each of its own.  So the
-// second kernel reads n segments again, 20 of 594 for 152064 bf16 logits,
-// whatever the values.
+// k_logprob_rows merges a row's chunks and finds its top n.  It takes the
+// largest segment maximum of each lane (64 interleaved sets of segments); the
+// n-th largest of those is a floor that n tokens reach, so only the segments
+// that reach it are read again, about 24 of 594 for n = 20 and 152064 bf16
+// logits (all of them where a row ties).
 //
 // Sums are kept in 32 bits, in a fixed order; y is rounded once (fma).
 
@@ -30,6 +30,7 @@ namespace {
 
 using namespace wave;
 
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLpThreads = 256;
@@ -63,8 +64,9 @@ struct Row {
   }
   // raw element, or -inf outside [0, V)
   __device__ __forceinline__ uint32_t raw(int e, int V) const {
-    if (e < 0 || e >= V) return BF ? 0xFF80u : 0xFF800000u;
-    return BF ? (uint32_t)((const uint16_t*)base)[e] : ((const uint32_t*)base)[e];
+    const int i = min(max(e, 0), V - 1);
+    const uint32_t x = BF ? (uint32_t)((const uint16_t*)base)[i] : ((const uint32_t*)base)[i];
+    return e == i ? x : (BF ? 0xFF80u : 0xFF800000u);
   }
   // elements e .. e + VEC - 1 (e + shift is a multiple of VEC); only elements of the row are read
   __device__ __forceinline__ u32x4 vec(int e, int V) const {
@@ -117,6 +119,50 @@ __device__ __forceinline__ void rebase(float m, float M, float c, float& S, floa
   S = r > 0.f ? S * r : (S == S ? 0.f : S);
 }
 
+// Each pass over the vectors unpacks them again: held unpacked from one pass
+// to the next they would take twice the registers, and half of the waves that
+// hide the reads.
+__device__ __forceinline__ void forget_unpacked(u32x4 (&v)[kPasses][4]) {
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) asm volatile("" : "+v"(v[p][u]));
+}
+
+// S = sum 2^y and W = sum 2^y (-y) over a thread's vectors, y = f(x), and n,
+// the wave's elements above xt.  A masked token (y = -inf) adds 0 to W; NaN
+// stays NaN in S.  The sums of a vector end with it: left for later by the
+// compiler they would keep every exponential in registers.
+template <typename R, bool ENT, bool COUNT, typename F>
+__device__ __forceinline__ void chunk_sums(u32x4 (&v)[kPasses][4], F f, float xt, float& S, float& W, int& n) {
+  forget_unpacked(v);
+  S = W = 0.f;
+  float S1 = 0.f, W1 = 0.f;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x[R::VEC];
+      R::unpack(v[p][u], x);
+#pragma unroll
+      for (int q = 0; q < R::VEC; q += 2) {
+        if (COUNT) n += __popcll(__ballot(x[q] > xt)) + __popcll(__ballot(x[q + 1] > xt));
+        const float y0 = f(x[q]), y1 = f(x[q + 1]);
+        const float e0 = lp_exp2(y0), e1 = lp_exp2(y1);
+        S += e0;
+        S1 += e1;
+        if (ENT) {
+          W = fmaf(-fmaxf(y0, -1e30f), e0, W);
+          W1 = fmaf(-fmaxf(y1, -1e30f), e1, W1);
+        }
+      }
+      asm volatile("" : "+v"(S), "+v"(W), "+v"(S1), "+v"(W1));
+      if (COUNT) asm volatile("" : "+s"(n));
+    }
+  S += S1;
+  W += W1;
+}
+
 struct ChunkStats {
   float M, S, W;
   int n;
@@ -128,7 +174,7 @@ struct ChunkStats {
 // are in flight together, and the waves reduce against their own maximum, so
 // one barrier is left.
 template <bool BF, bool ENT, bool RANK>
-__global__ void __launch_bounds__(kLpThreads) k_logprob_chunks(LogprobParams P) {
+__global__ void __launch_bounds__(kLpThreads, 6) k_logprob_chunks(LogprobParams P) {
   using R = Row<BF>;
   constexpr int VEC = R::VEC;
   __shared__ ChunkStats part[kLpWaves];
@@ -161,7 +207,10 @@ __global__ void __launch_bounds__(kLpThreads) k_logprob_chunks(LogprobParams P) 
 #pragma unroll
     for (int p = 0; p < kPasses; ++p)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[p][u] = r.vec(e0 + p * (kLpThreads / 8) * R::SEG + u * 8 * VEC, V);
+      for (int u = 0; u < 4; ++u) {
+        v[p][u] = r.vec(e0 + p * (kLpThreads / 8) * R::SEG + u * 8 * VEC, V);
+        __builtin_amdgcn_sched_barrier(0);                  // the few edge chunks do not set the register count
+      }
   }
   const float xt = (RANK && tok < V) ? r.at(tok) : INFINITY;
   float m = -INFINITY;
@@ -179,30 +228,16 @@ __global__ void __launch_bounds__(kLpThreads) k_logprob_chunks(LogprobParams P) 
     if (P.segmax && (t & 7) == 0) P.segmax[lin * kSegs + p * (kLpThreads / 8) + (t >> 3)] = sm;
     m = fmaxf(m, sm);
   }
+  forget_unpacked(v);
   const float M = wave_max(m);
-  float S = 0.f, W = 0.f;
+  float S, W;
   int n = 0;
   const float K = M * c;
-  const bool safe = fabsf(K) < kSafe;                       // false for M = -inf or inf as well
-  const float Mr = M == -INFINITY ? 0.f : M;
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x[VEC];
-      R::unpack(v[p][u], x);
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) {
-        if (RANK) n += __popcll(__ballot(x[q] > xt));
-        x[q] = safe ? fmaf(x[q], c, -K) : (x[q] - Mr) * c;
-      }
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) {
-        const float e = lp_exp2(x[q]);                      // NaN stays NaN
-        S += e;
-        if (ENT) W = fmaf(-fmaxf(x[q], -1e30f), e, W);      // 0 * (-inf) is 0 here
-      }
-    }
+  if (fabsf(K) < kSafe) {
+    chunk_sums<R, ENT, RANK>(v, [&](float x) { return fmaf(x, c, -K); }, xt, S, W, n);
+  } else {                                                  // no finite maximum, or K near overflow
+    const float Mr = M == -INFINITY ? 0.f : M;
+    chunk_sums<R, ENT, RANK>(v, [&](float x) { return (x - Mr) * c; }, xt, S, W, n);
   }
   S = wave_sum(S);
   if (ENT) W = wave_sum(W);
@@ -233,58 +268,107 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-constexpr int kSegRegs = 20;                                // segment maxima a lane keeps: rows of up to 1280 segments
-
-// Calls f(r, key) for the segments r * 64 + lane of a row; keys of absent segments are 0 (below every float's).
-template <bool REG, typename F>
-__device__ __forceinline__ void each_segment(const uint32_t (&key)[kSegRegs], const float* sm, int nseg, int lane, F f) {
-  if constexpr (REG) {
-#pragma unroll
-    for (int r = 0; r < kSegRegs; ++r)
-      if (r * kWave < nseg) f(r, key[r]);
-  } else {
-    for (int r = 0; r * kWave < nseg; ++r) {
-      const int i = r * kWave + lane;
-      f(r, i < nseg ? ordered(sm[i]) : 0u);
-    }
-  }
+// The value of a key whose last 16 bits, for a bf16, were not looked at: they
+// are equal bits, all 0 above zero and all 1 below it.
+template <bool BF>
+__device__ __forceinline__ float from_ordered(uint32_t k) {
+  if (BF && !(k & 0x80000000u)) k |= 0xFFFFu;
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// The n first segments by (maximum, index), n < nseg, into list[]: the n-th
-// largest maximum is found bit by bit with ballots over all maxima (a wave
-// holds them in registers up to 1280 segments), then the segments above it
-// and, in index order, as many that equal it as are missing.
-template <bool REG, bool BF>
-__device__ __forceinline__ void first_segments(const float* sm, int nseg, int n, int lane, int* list) {
-  uint32_t key[kSegRegs];
-  if constexpr (REG) {
-#pragma unroll
-    for (int r = 0; r < kSegRegs; ++r) {
-      const int i = r * kWave + lane;
-      key[r] = i < nseg ? ordered(sm[i]) : 0u;
-    }
+// shared memory between the lanes of one wave
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A token of the top list: larger values first, then lower indices; 0 is below every token.
+__device__ __forceinline__ uint64_t top_key(float x, int id) { return (uint64_t)ordered(x) << 32 | (uint32_t)~id; }
+__device__ __forceinline__ float key_value(uint64_t k) {
+  return k ? from_ordered<false>((uint32_t)(k >> 32)) : -INFINITY;
+}
+__device__ __forceinline__ uint64_t lane_key(uint64_t k, int l) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), l) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, l);
+}
+
+// the value of lane (lane ^ MASK): row moves inside 16 lanes where there is
+// one, the row swaps of this ISA family across them
+template <int MASK>
+__device__ __forceinline__ uint32_t from_xor(uint32_t v, int lane) {
+  if constexpr (MASK == 1) {
+    return (uint32_t)dpp_i<kDppQuadXor1>(0, (int)v);
+  } else if constexpr (MASK == 2) {
+    return (uint32_t)dpp_i<kDppQuadXor2>(0, (int)v);
+  } else if constexpr (MASK == 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return lane & 16 ? s[0] : s[1];
+  } else if constexpr (MASK == 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return lane & 32 ? s[0] : s[1];
+  } else {
+    return (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x1F | MASK << 10);   // xor inside 32 lanes
   }
-  // bf16 keys end in 16 equal bits: all 0 above zero, all 1 below it
+}
+// one step of a bitonic network: the larger key to the lanes where `larger`
+template <int MASK>
+__device__ __forceinline__ void exchange(uint64_t& k, bool larger, int lane) {
+  const uint64_t o = (uint64_t)from_xor<MASK>((uint32_t)(k >> 32), lane) << 32 | from_xor<MASK>((uint32_t)k, lane);
+  k = (k > o) == larger ? k : o;
+}
+// The steps MASK, MASK / 2, .. 1 of a network whose lanes with `up` false sort the other way round.
+template <int MASK>
+__device__ __forceinline__ void bitonic(uint64_t& k, bool up, int lane) {
+  exchange<MASK>(k, ((lane & MASK) == 0) == up, lane);
+  if constexpr (MASK > 1) bitonic<MASK / 2>(k, up, lane);
+}
+// the wave's keys, largest first
+__device__ __forceinline__ void sort_keys(uint64_t& k, int lane) {
+  bitonic<1>(k, (lane & 2) == 0, lane);
+  bitonic<2>(k, (lane & 4) == 0, lane);
+  bitonic<4>(k, (lane & 8) == 0, lane);
+  bitonic<8>(k, (lane & 16) == 0, lane);
+  bitonic<16>(k, (lane & 32) == 0, lane);
+  bitonic<32>(k, true, lane);
+}
+// the 64 largest of two sorted lists of 64, sorted: one list against the other's reverse, then one merge
+__device__ __forceinline__ void merge_keys(uint64_t& a, uint64_t b, int lane) {
+  const int back = (kWave - 1 - lane) * 4;
+  const uint64_t r = (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)(b >> 32)) << 32 |
+                     (uint32_t)__builtin_amdgcn_ds_bpermute(back, (int)(uint32_t)b);
+  a = a > r ? a : r;
+  bitonic<32>(a, true, lane);
+}
+
+constexpr int kHeldMore = 512;                              // gathered tokens that may wait for more
+constexpr int kListed = 16 * kWave;                         // segments listed before they are read
+constexpr int kStage = 32;                                  // of those, read together
+
+// The n-th largest of the wave's values (n <= 64), found bit by bit.
+template <bool BF>
+__device__ __forceinline__ float nth_of_wave(float x, int n) {
+  const uint32_t key = ordered(x);
+  uint32_t thr = 0;
+  for (int bit = 31; bit >= (BF ? 16 : 0); --bit) {
+    const uint32_t cand = thr | (1u << bit);
+    if (__popcll(__ballot(key >= cand)) >= n) thr = cand;
+  }
+  return from_ordered<BF>(thr);
+}
+
+// The same over N values of every lane (NaN: none).
+template <bool BF, int N>
+__device__ __forceinline__ float nth_of_all(const float (&x)[N], int n) {
   uint32_t thr = 0;
   for (int bit = 31; bit >= (BF ? 16 : 0); --bit) {
     const uint32_t cand = thr | (1u << bit);
     int cnt = 0;
-    each_segment<REG>(key, sm, nseg, lane, [&](int, uint32_t k) { cnt += __popcll(__ballot(k >= cand)); });
+#pragma unroll
+    for (int j = 0; j < N; ++j) cnt += __popcll(__ballot(x[j] == x[j] && ordered(x[j]) >= cand));
     if (cnt >= n) thr = cand;
   }
-  const uint32_t last = BF ? thr | 0xFFFFu : thr;           // keys in [thr, last] are the n-th maximum's
-  int above = 0;
-  each_segment<REG>(key, sm, nseg, lane, [&](int, uint32_t k) { above += __popcll(__ballot(k > last)); });
-  int want = n - above, at = 0;
-  const uint64_t lower = (1ull << lane) - 1;
-  each_segment<REG>(key, sm, nseg, lane, [&](int r, uint32_t k) {
-    const uint64_t eq = __ballot(k >= thr && k <= last);
-    const bool take = k > last || (k >= thr && __popcll(eq & lower) < want);
-    const uint64_t all = __ballot(take);
-    if (take) list[at + __popcll(all & lower)] = r * kWave + lane;
-    want -= min(want, (int)__popcll(eq));
-    at += __popcll(all);
-  });
+  return from_ordered<BF>(thr);
 }
 
 }  // namespace
@@ -295,7 +379,10 @@ __device__ __forceinline__ void first_segments(const float* sm, int nseg, int n,
 template <bool BF>
 __global__ void __launch_bounds__(kWave) k_logprob_rows(LogprobParams P) {
   using R = Row<BF>;
-  __shared__ int list[SV_LOGPROBS_MAX_TOP];
+  static_assert(R::SEG % kWave == 0, "a lane's share of a segment");
+  __shared__ int list[kListed];
+  __shared__ uint64_t cand[4 * R::SEG + kHeldMore];         // at least the two partial segments, or four whole ones more
+  __shared__ u32x2 stage[kStage][kWave];
   const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= P.rows) return;
   const int lane = threadIdx.x;
@@ -344,62 +431,126 @@ __global__ void __launch_bounds__(kWave) k_logprob_rows(LogprobParams P) {
     if (P.status) P.status[row] = st;
   }
   if (top == 0) return;
-  float bv = -INFINITY;                                     // the top list: lane i holds the i-th, best first
-  int bi = 0x7FFFFFFF;
+  uint64_t best = 0;                                        // the top list: lane i holds the i-th, best first
   if (!skip && !bad) {
     const int nseg = (V + r.shift + R::SEG - 1) / R::SEG;
-    const int ns = min(top, nseg);
-    if (nseg > top) {
-      const float* sm = P.segmax + row * P.nch * kSegs;
-      if (nseg <= kSegRegs * kWave) first_segments<true, BF>(sm, nseg, top, lane, list);
-      else first_segments<false, BF>(sm, nseg, top, lane, list);
-    } else if (lane < ns) {
-      list[lane] = lane;
+    constexpr int PER = R::SEG / kWave;                     // a lane's tokens of a segment: 4 bf16 or 2 floats
+    constexpr int NM = 16;                                  // maxima of a lane in flight: 1024 segments at a time
+    const float* sm = P.segmax + row * P.nch * kSegs;
+    const uint64_t lower = (1ull << lane) - 1;
+    // `floor`: at least `top` segments (as many lanes' maxima), hence tokens, reach it
+    float x[NM], lm = -INFINITY;
+    auto load_maxima = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < NM; ++j) x[j] = sm[min(i0 + j * kWave + lane, nseg - 1)];
+#pragma unroll
+      for (int j = 0; j < NM; ++j) x[j] = i0 + j * kWave + lane < nseg ? x[j] : __builtin_nanf("");
+    };
+    for (int i0 = 0; i0 < nseg; i0 += NM * kWave) {
+      load_maxima(i0);
+#pragma unroll
+      for (int j = 0; j < NM; ++j) lm = fmaxf(lm, x[j]);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    constexpr int PER = R::SEG / kWave;                     // a lane's elements of a segment: 4 bf16 or 2 floats
-    constexpr int NB = 8;                                   // segments in flight
-    for (int s0 = 0; s0 < ns; s0 += NB) {
-      uint32_t raw[NB][PER];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const int e = (s0 + j < ns ? list[s0 + j] : list[0]) * R::SEG - r.shift + lane * PER;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) raw[j][q] = r.raw(e + q, V);
-      }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        if (s0 + j >= ns) break;
-        const int e = list[s0 + j] * R::SEG - r.shift + lane * PER;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const float x = __uint_as_float(BF ? raw[j][q] << 16 : raw[j][q]);
-          const int id = e + q;
-          const float wv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bv), top - 1));
-          const int wi = __builtin_amdgcn_readlane(bi, top - 1);
-          uint64_t better = __ballot(id >= 0 && id < V && (x > wv || (x == wv && id < wi)));
-          while (better) {
-            const int src = __builtin_ctzll(better);
-            better &= better - 1;
-            const float nv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), src));
-            const int ni = __builtin_amdgcn_readlane(id, src);
-            // the entries in front of the new one stay, the others move one lane up
-            const int pos = __popcll(__ballot(bv > nv || (bv == nv && bi < ni)));
-            const float pv = __shfl_up(bv, 1);
-            const int pi = __shfl_up(bi, 1);
-            bv = lane < pos ? bv : (lane == pos ? nv : pv);
-            bi = lane < pos ? bi : (lane == pos ? ni : pi);
-          }
+    float floor = nth_of_wave<BF>(lm, top);
+    // Near 64 the n-th of 64 lane maxima is loose (64 of 594 segments are
+    // wanted and about 300 reach it), and the n-th of all maxima pays: top 64
+    // of 256 rows 35 us against 134; up to 32 both list about as many.
+    if (top > 32 && nseg > top && nseg <= NM * kWave) floor = fmaxf(floor, nth_of_all<BF, NM>(x, top));
+    int held = 0;
+    auto merge_held = [&]() {
+      wave_sync();
+      for (int k0 = 0; k0 < held; k0 += kWave) {
+        uint64_t k = k0 + lane < held ? cand[k0 + lane] : 0;
+        if (__ballot(k > lane_key(best, top - 1))) {
+          sort_keys(k, lane);
+          merge_keys(best, k, lane);
         }
       }
+      held = 0;
+      floor = fmaxf(floor, key_value(lane_key(best, top - 1)));
+      wave_sync();
+    };
+    // tokens of a segment that reach `floor`, gathered to be sorted 64 at a time and merged into the top list
+    auto gather = [&](const uint32_t (&raw)[PER], int e) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const float v = __uint_as_float(BF ? raw[q] << 16 : raw[q]);
+        const bool in = (unsigned)(e + q) < (unsigned)V && v >= floor;
+        const uint64_t mask = __ballot(in);
+        if (mask) {
+          if (in) cand[held + __popcll(mask & lower)] = top_key(v, e + q);
+          held += __popcll(mask);
+        }
+      }
+    };
+    // the segments that lie only partly inside the row (the first and the last may), token by token
+    const int inner0 = r.shift ? 1 : 0, inner1 = (V + r.shift) / R::SEG;   // whole segments: inner0 .. inner1 - 1
+    for (int k = 0; k < 2; ++k) {
+      const int sg = k ? nseg - 1 : 0;
+      if ((sg >= inner0 && sg < inner1) || (k && nseg == 1)) continue;
+      const int e = sg * R::SEG - r.shift + lane * PER;
+      uint32_t raw[PER];
+#pragma unroll
+      for (int q = 0; q < PER; ++q) raw[q] = r.raw(e + q, V);
+      gather(raw, e);
     }
+    for (int r0 = 0; r0 < nseg; r0 += NM * kWave) {
+      if (nseg > NM * kWave) load_maxima(r0);
+      int listed = 0;
+#pragma unroll
+      for (int j = 0; j < NM; ++j) {
+        const int i = r0 + j * kWave + lane;
+        const bool reach = x[j] >= floor && i >= inner0 && i < inner1;
+        const uint64_t all = __ballot(reach);
+        if (all) {
+          if (reach) list[listed + __popcll(all & lower)] = i;
+          listed += __popcll(all);
+        }
+      }
+      wave_sync();
+      for (int s0 = 0; s0 < listed; s0 += kStage) {
+        // 8 bytes a lane, all in flight: a batch costs one latency of the logits
+        u32x2 w[kStage];
+#pragma unroll
+        for (int j = 0; j < kStage; ++j)
+          w[j] = *(const u32x2*)(r.base + (int64_t)(list[min(s0 + j, listed - 1)] * R::SEG - r.shift + lane * PER) * R::ES);
+        float m = -INFINITY;                                // the lanes' largest tokens may raise the floor
+#pragma unroll
+        for (int j = 0; j < kStage; ++j) {
+          stage[j][lane] = w[j];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (s0 + j < listed) m = fmaxf(m, __uint_as_float(BF ? w[j][q] & 0xFFFF0000u : w[j][q]));
+            if (BF && s0 + j < listed) m = fmaxf(m, __uint_as_float(w[j][q] << 16));
+          }
+        }
+        floor = fmaxf(floor, nth_of_wave<BF>(m, top));
+        wave_sync();
+        const int names = list[min(s0 + lane, listed - 1)], n_here = min(kStage, listed - s0);
+        for (int j0 = 0; j0 < n_here; j0 += 4) {
+          u32x2 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = stage[j0 + j][lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j0 + j >= n_here) break;
+            uint32_t raw[PER];
+#pragma unroll
+            for (int q = 0; q < PER; ++q) raw[q] = BF ? (v[j][q / 2] >> (q & 1) * 16) & 0xFFFFu : v[j][q & 1];
+            gather(raw, __builtin_amdgcn_readlane(names, j0 + j) * R::SEG - r.shift + lane * PER);
+          }
+          if (held > kHeldMore) merge_held();
+        }
+        wave_sync();
+      }
+      wave_sync();                                          // the list is written again
+    }
+    merge_held();
   }
   if (lane < top) {
     float out = skip ? -INFINITY : __builtin_nanf("");
-    if (!skip && !bad) out = lp_value(P, row, bv, M, c, log2f(S));
-    P.top_tokens[row * top + lane] = (skip || bad) ? -1 : bi;
+    if (!skip && !bad) out = lp_value(P, row, key_value(best), M, c, log2f(S));
+    P.top_tokens[row * top + lane] = (skip || bad) ? -1 : (int)~(uint32_t)best;
     if (P.top_logprobs) P.top_logprobs[row * top + lane] = out;
   }
 }
