@@ -60,6 +60,9 @@ constexpr int kUnitKeys = kTileKeys * kAtWaves;  // keys of a unit of work
 static_assert(kUnitKeys == kAttnUnitKeys, "unit of work");
 constexpr float kLn2 = 0.693147180559945309417f;
 
+// a value every lane holds, as a scalar
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 template <bool BF>
@@ -93,6 +96,15 @@ __device__ __forceinline__ float hi16(uint32_t w) {
   if constexpr (BF) return __uint_as_float(w & 0xFFFF0000u);
   else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
 }
+
+// the low half is an infinity or NaN
+template <bool BF>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  constexpr uint32_t EX = BF ? 0x7F80u : 0x7C00u;
+  return (w & EX) == EX;
+}
+template <bool BF>
+constexpr uint32_t kOne = BF ? 0x3F80u : 0x3C00u;
 
 // maximum over the four lanes that share a column (lanes l, l ^ 16, l ^ 32, l ^ 48)
 __device__ __forceinline__ float column_max(float v) {
@@ -209,7 +221,7 @@ __device__ __forceinline__ uint16_t to16(float x) {
 }  // namespace
 
 template <bool BF, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 || (D == 128 && MT == 2) ? 1 : 2) k_attention(AttnParams P) {
+__global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_attention(AttnParams P) {
   constexpr int TM = 16 * MT;
   constexpr int NS = D / 32;                     // 32-element slices of the head dimension (scores)
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
@@ -217,13 +229,14 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
   extern __shared__ uint32_t dyn[];
   uint32_t* rows = dyn;
   uint32_t* units = dyn + P.B + 1;
+  __shared__ u32x4 qs[MT][NS][kWave];            // the tile's queries as the first product's right operands
   __shared__ float ml[kAtWaves][2][TM];
   __shared__ float ob[kAtWaves][16][D / 4 + 1];
-  const int t = threadIdx.x, lane = t & (kWave - 1), wv = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = uni(t / kWave);
   const int g = lane >> 4, col = lane & 15;
   const bool ok = plan(P, TM, rows, units);
   Part* desc = reinterpret_cast<Part*>(P.desc);
-  const uint32_t U = units[P.B], W = min((uint32_t)gridDim.x, U);
+  const uint32_t U = (uint32_t)uni((int)units[P.B]), W = min((uint32_t)gridDim.x, U);
   const uint32_t w = blockIdx.x;
   if (w == 0 && t == 0) desc[gridDim.x].first_unit = (int)U;   // the join cuts the units the same way
   if (!ok) {                                     // the rows do not add up: every output is cleared
@@ -245,13 +258,14 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
   // the sequence that holds unit u
   int b = 0;
   for (int step = 4096; step > 0; step >>= 1)
-    if (b + step < P.B && units[b + step] <= u) b += step;
+    if (b + step < P.B && (uint32_t)uni((int)units[b + step]) <= u) b += step;
   bool first_part = true;
   while (u < u_end) {
-    while (units[b + 1] <= u) ++b;
-    const int row0 = (int)rows[b], n = (int)(rows[b + 1] - rows[b]);
-    const Extent x = seq_extent(P, b, n);
-    const uint32_t rel = u - units[b];
+    while ((uint32_t)uni((int)units[b + 1]) <= u) ++b;
+    const int row0 = uni((int)rows[b]), n = uni((int)rows[b + 1]) - row0;
+    Extent x = seq_extent(P, b, n);
+    x = Extent{uni(x.slot), uni(x.len), uni(x.blk0), uni(x.nblk)};
+    const uint32_t rel = u - (uint32_t)uni((int)units[b]);
     const int seg = (int)(rel / (uint32_t)x.nblk), b0 = (int)(rel - (uint32_t)seg * x.nblk);
     const int b1 = (int)min((uint32_t)x.nblk, b0 + (u_end - u));
     const int mb = seg / P.kv_heads, head = seg - mb * P.kv_heads;
@@ -267,7 +281,6 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
     }
     const int nrow = min(TM, n * P.group - mb * TM);   // rows of this tile
     // the rows of this lane's columns: their query, and the positions they see
-    u32x4 q[MT][NS];
     int last[MT], from[MT];
     int min_last = 0x7FFFFFFF, max_from = 0;
     {
@@ -285,7 +298,8 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
       from[m] = P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
       const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head + 8 * g;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) q[m][s] = *(const u32x4*)(qp + 32 * s);
+      for (int s = 0; s < NS; ++s)
+        if ((m * NS + s) % kAtWaves == wv) qs[m][s][lane] = *(const u32x4*)(qp + 32 * s);
     }
     f32x4 o[MT][NJ];
     float mx[MT], ls[MT];
@@ -297,20 +311,25 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
       for (int j = 0; j < NJ; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     bool bad = x.slot < 0;
-    const int32_t* table = P.table + (int64_t)max(x.slot, 0) * P.table_stride;
+    // read with scalar loads, whose counter is not the one the keys and values in flight are waited for with
+    typedef const __attribute__((address_space(4))) int32_t* Names;
+    const Names table = (Names)(uintptr_t)(P.table + (int64_t)max(x.slot, 0) * P.table_stride);
     const int pmask = (1 << P.page_log2) - 1;
     u32x4 kr[2][NS];
     uint32_t vr[8][VW];
     const char *kb[2], *vb[2];
     // first key of block blk for this wave
     auto key0 = [&](int blk) { return (x.blk0 + blk) * kUnitKeys + wv * kTileKeys; };
-    // Base addresses of the wave's two 16-key tiles.  A tile lies in one
-    // page; behind the last token the first tile's is used again (its reads
-    // stay in bounds and are masked).  A page outside the pool is replaced
-    // by page 0 and noted.
+    // The pages of the wave's two 16-key tiles (a tile lies in one page);
+    // behind the last token the first tile's is used again, so that its reads
+    // stay in bounds: they are masked.
+    int id0 = 0, id1 = 0;
+    auto names = [&](int pos) {
+      id0 = table[pos >> P.page_log2];
+      id1 = table[min(pos + 16, x.len - 1) >> P.page_log2];
+    };
+    // Base addresses; a page outside the pool is replaced by page 0 and noted.
     auto locate = [&](int pos) {
-      int id0 = __builtin_amdgcn_readfirstlane(table[pos >> P.page_log2]);
-      int id1 = pos + 16 < x.len ? __builtin_amdgcn_readfirstlane(table[(pos + 16) >> P.page_log2]) : id0;
       if ((unsigned)id0 >= (unsigned)P.num_pages || (unsigned)id1 >= (unsigned)P.num_pages) {
         bad = true;
         id0 = (unsigned)id0 >= (unsigned)P.num_pages ? 0 : id0;
@@ -350,12 +369,15 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
     int pos = key0(b0);
     const int pos_end = min(x.len, key0(b1));
     if (pos < pos_end) {
+      names(pos);
       locate(pos);
       load_k();
       load_v();
     }
+    __syncthreads();                             // the queries are in place
     for (; pos < pos_end; pos += kUnitKeys) {
       const bool more = pos + kUnitKeys < pos_end;
+      if (more) names(pos + kUnitKeys);
       f32x4 sc[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -363,7 +385,7 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
         for (int h = 0; h < 2; ++h) {
           sc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < NS; ++s) sc[m][h] = mfma<BF>(kr[h][s], q[m][s], sc[m][h]);
+          for (int s = 0; s < NS; ++s) sc[m][h] = mfma<BF>(kr[h][s], qs[m][s][lane], sc[m][h]);
         }
       if (more) {
         locate(pos + kUnitKeys);
@@ -380,8 +402,7 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
 #pragma unroll
           for (int i = 0; i < VW; ++i) {
             vr[e][i] = gone ? 0u : vr[e][i];
-            constexpr uint32_t EX = BF ? 0x7F80u : 0x7C00u;
-            strange |= (vr[e][i] & EX) == EX || (vr[e][i] >> 16 & EX) == EX;
+            strange |= not_finite<BF>(vr[e][i]) || not_finite<BF>(vr[e][i] >> 16);
           }
         }
         strange = __ballot(strange) != 0;
@@ -423,40 +444,42 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : D == 256 
           pl[m][i] = pack16<BF>(p[2 * i] - lo16<BF>(ph[m][i]), p[2 * i + 1] - hi16<BF>(ph[m][i]));
         }
       }
-      if (!strange) {
+      if (strange) {
+        // A value that is not finite next to a key that some row does not
+        // see.  Where it stands, a third product with ones in such places
+        // finds the rows that do see one; they become NaN, and the value 0.
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           u32x4 a;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+            a[i] = (not_finite<BF>(w) ? kOne<BF> : 0u) | (not_finite<BF>(w >> 16) ? kOne<BF> << 16 : 0u);
+          }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            o[m][j] = mfma<BF>(a, ph[m], o[m][j]);
-            o[m][j] = mfma<BF>(a, pl[m], o[m][j]);
+            f32x4 d = mfma<BF>(a, ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
+            d = mfma<BF>(a, pl[m], d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[m][j][r] += d[r] > 0.f ? __builtin_nanf("") : 0.f;
           }
         }
-      } else {
-        // a value that is not finite next to a key that some row does not
-        // see: one key at a time, added to the rows that see it
-        for (int kk = 0; kk < kTileKeys; ++kk) {
-          const int slot_g = (kk & 15) >> 2, slot_e = (kk >> 4) * 4 + (kk & 3);
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            u32x4 a;
+        for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-              const uint32_t keep = (slot_e >> 1) == i && slot_g == g ? ((slot_e & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
-              a[i] &= keep;
-            }
+          for (int i = 0; i < VW; ++i)
+            vr[e][i] &= (not_finite<BF>(vr[e][i]) ? 0u : 0xFFFFu) | (not_finite<BF>(vr[e][i] >> 16) ? 0u : 0xFFFF0000u);
+      }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              f32x4 d = mfma<BF>(a, ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
-              d = mfma<BF>(a, pl[m], d);
-              if (pos + kk <= last[m] && pos + kk >= from[m]) o[m][j] += d;
-            }
-          }
+      for (int j = 0; j < NJ; ++j) {
+        u32x4 a;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          o[m][j] = mfma<BF>(a, ph[m], o[m][j]);
+          o[m][j] = mfma<BF>(a, pl[m], o[m][j]);
         }
       }
       if (more) load_v();
