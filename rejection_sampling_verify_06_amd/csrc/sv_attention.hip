@@ -73,6 +73,13 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// shared memory between the lanes of one wave
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // two floats rounded to the 16-bit type (to nearest even), a in the low half
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -120,9 +127,7 @@ __device__ __forceinline__ float column_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// The round's layout as every block works it out for itself: for sequence b
-// its first packed row and its first unit of work.  Returns false where the
-// rows do not add up.  Both arrays have B + 1 entries in shared memory.
+// A sequence of the round, as every block works it out for itself.
 struct Extent {
   int slot;       // row of page_table and seq_len; -1: refused
   int len;        // cached tokens (0 for a refused sequence)
@@ -133,18 +138,18 @@ struct Extent {
 __device__ __forceinline__ Extent seq_extent(const AttnParams& P, int b, int n) {
   Extent x;
   x.slot = P.seqs ? P.seqs[b] : b;
-  if ((unsigned)x.slot >= (unsigned)P.slots) x.slot = -1;
-  x.len = x.slot < 0 ? 0 : P.seq_len[x.slot];
-  if (x.len < 0 || x.len > P.max_len) {
-    x.slot = -1;
-    x.len = 0;
-  }
+  const int len = P.seq_len[(unsigned)x.slot < (unsigned)P.slots ? x.slot : 0];
+  const bool ok = (unsigned)x.slot < (unsigned)P.slots && len >= 0 && len <= P.max_len;
+  x.slot = ok ? x.slot : -1;
+  x.len = ok ? len : 0;
   const int first = P.window > 0 ? max(0, x.len - n + 1 - P.window) : 0;
   x.blk0 = first / kUnitKeys;
   x.nblk = max(1, (x.len + kUnitKeys - 1) / kUnitKeys - x.blk0);
   return x;
 }
 
+// Prefix sums of the sequences' rows and units of work, B + 1 entries each in
+// shared memory, for tiles of TM rows.
 __device__ __forceinline__ bool plan(const AttnParams& P, int TM, uint32_t* rows, uint32_t* units) {
   __shared__ uint32_t tr[kAtWaves], tu[kAtWaves];
   __shared__ int bad;
@@ -155,14 +160,13 @@ __device__ __forceinline__ bool plan(const AttnParams& P, int TM, uint32_t* rows
   const int b0 = min(t * per, P.B), b1 = min(b0 + per, P.B);
   uint32_t r = 0, u = 0;
   for (int b = b0; b < b1; ++b) {
-    const int K = P.num_draft[b];
-    if (K < 0 || K >= P.total_rows) {
-      bad = 1;
-      continue;
-    }
-    const Extent x = seq_extent(P, b, K + 1);
-    r += (uint32_t)(K + 1);
-    u += (uint32_t)(((K + 1) * P.group + TM - 1) / TM * P.kv_heads) * (uint32_t)x.nblk;
+    const int K = P.num_draft[b], n = min(max(K, 0), P.total_rows - 1) + 1;
+    const Extent x = seq_extent(P, b, n);
+    if (n != K + 1) bad = 1;
+    rows[b] = r;                                 // within this thread's sequences for now
+    units[b] = u;
+    r += (uint32_t)n;
+    u += (uint32_t)((n * P.group + TM - 1) / TM * P.kv_heads) * (uint32_t)x.nblk;
   }
   const uint32_t ir = wave_incl_scan_u32(r), iu = wave_incl_scan_u32(u);
   if (lane == kWave - 1) {
@@ -176,18 +180,13 @@ __device__ __forceinline__ bool plan(const AttnParams& P, int TM, uint32_t* rows
     au += tu[i];
   }
   for (int b = b0; b < b1; ++b) {
-    rows[b] = ar;
-    units[b] = au;
-    const int K = P.num_draft[b];
-    if (K < 0 || K >= P.total_rows) continue;
-    const Extent x = seq_extent(P, b, K + 1);
-    ar += (uint32_t)(K + 1);
-    au += (uint32_t)(((K + 1) * P.group + TM - 1) / TM * P.kv_heads) * (uint32_t)x.nblk;
+    rows[b] += ar;
+    units[b] += au;
   }
   if (t == kAtThreads - 1) {
-    rows[P.B] = ar;
-    units[P.B] = au;
-    if (ar != (uint32_t)P.total_rows) bad = 1;
+    rows[P.B] = ar + r;
+    units[P.B] = au + u;
+    if (ar + r != (uint32_t)P.total_rows) bad = 1;
   }
   __syncthreads();
   return bad == 0;
@@ -198,7 +197,7 @@ struct Part {
   int first_unit, end_unit;   // the tile's units; first_unit -1: the block starts at a tile's beginning
   int row0, n;                // the sequence's packed rows
   int head, mb;
-  int pad[2];
+  uint32_t U, W;              // all units, and the blocks they are dealt out to
 };
 static_assert(sizeof(Part) == kAttnPartBytes, "part record");
 
@@ -213,32 +212,27 @@ __device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, 
   return P.parts + ((int64_t)w * 2 + slot) * TM * (D + 2);
 }
 
-template <bool BF>
-__device__ __forceinline__ uint16_t to16(float x) {
-  return (uint16_t)pack16<BF>(x, 0.f);
-}
-
 }  // namespace
 
 template <bool BF, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_attention(AttnParams P) {
-  constexpr int TM = 16 * MT;
+__global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) k_attention(AttnParams P) {
+  constexpr int TM = 16 * MT;                    // rows of a tile
   constexpr int NS = D / 32;                     // 32-element slices of the head dimension (scores)
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
   constexpr int VW = NJ / 2;                     // dwords of those
   extern __shared__ uint32_t dyn[];
   uint32_t* rows = dyn;
   uint32_t* units = dyn + P.B + 1;
-  __shared__ u32x4 qs[MT][NS][kWave];            // the tile's queries as the first product's right operands
+  constexpr int RS = 256 / D;                    // of a lane's 4 rows of each O^T tile, those that are joined at a time
+  __shared__ u32x4 qs[MT][NS][kWave];        // the tile's queries as the first product's right operands
   __shared__ float ml[kAtWaves][2][TM];
-  __shared__ float ob[kAtWaves][16][D / 4 + 1];
+  __shared__ float ob[kAtWaves][16][64 + 4];     // 64 of the D values of 16 rows, rows 4 banks apart
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = uni(t / kWave);
   const int g = lane >> 4, col = lane & 15;
   const bool ok = plan(P, TM, rows, units);
   Part* desc = reinterpret_cast<Part*>(P.desc);
   const uint32_t U = (uint32_t)uni((int)units[P.B]), W = min((uint32_t)gridDim.x, U);
   const uint32_t w = blockIdx.x;
-  if (w == 0 && t == 0) desc[gridDim.x].first_unit = (int)U;   // the join cuts the units the same way
   if (!ok) {                                     // the rows do not add up: every output is cleared
     if (t == 0) desc[w].first_unit = -1;
     const int64_t total = (int64_t)P.total_rows * P.heads * D;
@@ -277,6 +271,8 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_atte
       d.n = n;
       d.head = head;
       d.mb = mb;
+      d.U = U;
+      d.W = W;
       desc[w] = d;
     }
     const int nrow = min(TM, n * P.group - mb * TM);   // rows of this tile
@@ -484,7 +480,10 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_atte
       }
       if (more) load_v();
     }
-    // the waves' parts of the tile become one
+    // The waves' parts of the tile become one: a lane brings its O to the
+    // rows' common maximum (and divides by the sum, where this block has the
+    // whole tile), 64 values of 16 rows at a time go through shared memory,
+    // and a thread adds up 4 neighbours of a row.
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       ls[m] = column_sum(ls[m]);
@@ -499,49 +498,60 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_atte
     float* part = part_at(P, (int)w, b0 > 0 ? 0 : 1, TM, D);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (m * 16 >= nrow) break;
-      float M = ml[0][0][m * 16 + col];
+      const int r = m * 16 + col;
+      float M = ml[0][0][r], L = 0.f;
 #pragma unroll
-      for (int i = 1; i < kAtWaves; ++i) M = fmaxf(M, ml[i][0][m * 16 + col]);
-      const float f = mx[m] == M ? 1.f : at_exp2(mx[m] - M);
+      for (int i = 1; i < kAtWaves; ++i) M = fmaxf(M, ml[i][0][r]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int i = 0; i < kAtWaves; ++i) L += ml[i][1][r] * (ml[i][0][r] == M ? 1.f : at_exp2(ml[i][0][r] - M));
+      float f = mx[m] == M ? 1.f : at_exp2(mx[m] - M);
+      if (whole) f = L == 0.f ? 0.f : f / L;
+      if (wv == 0 && g == 0 && r < nrow) {
+        if (!whole) {
+          part[TM * D + r] = M;
+          part[TM * D + TM + r] = L;
+        } else if (P.lse) {
+          const int R = mb * TM + r, ri = R / P.group;
+          P.lse[(int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        }
+      }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) ob[wv][col][g * NJ + j] = o[m][j][r] * f;
+      for (int r0 = 0; r0 < 4; r0 += RS) {
+#pragma unroll
+        for (int rr = 0; rr < RS; ++rr)
+#pragma unroll
+          for (int j = 0; j < NJ; j += 4) {
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = o[m][j + i][r0 + rr] * f;
+            *(f32x4*)&ob[wv][col][(g * RS + rr) * NJ + j] = v;
+          }
         __syncthreads();
-        // element c of row q: head dimension NJ (4 (c / NJ) + r) + c % NJ
-        for (int i = t; i < 16 * (D / 4); i += kAtThreads) {
-          const int qr = i / (D / 4), c = i - qr * (D / 4);
-          const int rr = m * 16 + qr;
-          if (rr < nrow) {
-            const int d = NJ * (4 * (c / NJ) + r) + c % NJ;
-            float Mq = ml[0][0][rr];
+        {
+          const int qr = t >> 4, c = (t & 15) * 4;
+          const int row = m * 16 + qr;
+          f32x4 v = *(const f32x4*)&ob[0][qr][c];
 #pragma unroll
-            for (int k = 1; k < kAtWaves; ++k) Mq = fmaxf(Mq, ml[k][0][rr]);
-            float L = 0.f, v = 0.f;
+          for (int i = 1; i < kAtWaves; ++i) {
+            const f32x4 y = *(const f32x4*)&ob[i][qr][c];
 #pragma unroll
-            for (int k = 0; k < kAtWaves; ++k) {
-              L += ml[k][1][rr] * (ml[k][0][rr] == Mq ? 1.f : at_exp2(ml[k][0][rr] - Mq));
-              v += ob[k][qr][c];
-            }
+            for (int k = 0; k < 4; ++k) v[k] += y[k];
+          }
+          if (row < nrow) {
+            const int gr = c / NJ;               // g RS + rr
+            const int d = NJ * (4 * (gr / RS) + r0 + gr % RS) + c % NJ;
             if (whole) {
-              const int R = mb * TM + rr, ri = R / P.group, h = head * P.group + R - ri * P.group;
-              const int64_t at = (int64_t)(row0 + ri) * P.heads + h;
-              ((uint16_t*)P.out)[at * D + d] = to16<BF>(L == 0.f ? 0.f : v / L);
-              if (P.lse && r == 0 && c == 0) P.lse[at] = L == 0.f ? -INFINITY : (Mq + log2f(L)) * kLn2;
+              const int R = mb * TM + row, ri = R / P.group;
+              const int64_t at = (int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group;
+              *(u32x2*)((uint16_t*)P.out + at * D + d) = u32x2{pack16<BF>(v[0], v[1]), pack16<BF>(v[2], v[3])};
             } else {
-              part[rr * D + d] = v;
-              if (r == 0 && c == 0) {
-                part[TM * D + rr] = Mq;
-                part[TM * D + TM + rr] = L;
-              }
+              *(f32x4*)(part + row * D + d) = v;
             }
           }
         }
         __syncthreads();
       }
     }
-    __syncthreads();                             // ml is free again
     first_part = false;
     u += (uint32_t)(b1 - b0);
   }
@@ -549,12 +559,12 @@ __global__ void __launch_bounds__(kAtThreads, D == 64 && MT == 1 ? 3 : 2) k_atte
 
 // Adds up the parts of each tile that was cut: block (w, y) serves the tile
 // that block w of k_attention entered in its middle, if no earlier block did,
-// and rows 4 y .. 4 y + 3 of it, a row to a wave.  Bound by latency: a lane
-// has 8 parts of its 16 bytes in flight.  Further blocks check the sequences'
-// pages for `status`.
+// and rows 4 y .. 4 y + 3 of it, a row to a wave.  Bound by latency: the
+// record, then maxima, sums and the first parts' O at once, 8 parts of a
+// lane's 16 bytes in flight.  Further blocks check the sequences' pages for
+// `status`.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int TM, int W0) {
-  extern __shared__ uint32_t dyn[];
   __shared__ float wt[kAtWaves][kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
   if ((int)blockIdx.x >= W0) {
@@ -607,51 +617,52 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
   }
   const Part d = reinterpret_cast<const Part*>(P.desc)[blockIdx.x];
   if (d.first_unit < 0) return;
-  const uint32_t U = (uint32_t)reinterpret_cast<const Part*>(P.desc)[W0].first_unit, W = min((uint32_t)W0, U);
   const uint32_t w = blockIdx.x;
-  if (range_start(w - 1, W, U) > (uint32_t)d.first_unit) return;   // an earlier block joins this tile
+  if (range_start(w - 1, d.W, d.U) > (uint32_t)d.first_unit) return;   // an earlier block joins this tile
   const int row = (int)blockIdx.y * kAtWaves + wv;
   const int nrow = min(TM, d.n * P.group - d.mb * TM);
   if (row >= nrow) return;                       // whole waves; no block barrier below
-  const uint32_t w1 = range_of((uint32_t)d.end_unit - 1, W, U);
-  const int parts = (int)(w1 - w) + 2;           // part 0: slot 1 of block w - 1; part i: slot 0 of block w - 1 + i
+  const int parts = (int)(range_of((uint32_t)d.end_unit - 1, d.W, d.U) - w) + 2;
+  // part 0: slot 1 of block w - 1; part i: slot 0 of block w - 1 + i
   auto part = [&](int i) { return (const float*)part_at(P, (int)w - 1 + i, i == 0 ? 1 : 0, TM, D); };
-  float M = -INFINITY;
-  for (int i = lane; i < parts; i += kWave) M = fmaxf(M, part(i)[TM * D + row]);
-  M = wave_max(M);
   constexpr int Q = D / 4;                       // lanes that cover a row with 4 floats each
   constexpr int GR = kWave / Q;                  // parts side by side: 4, 2 or 1
   const int pg = lane / Q, dq = (lane - pg * Q) * 4;
+  f32x4 v[8];
+  auto load_o = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = *(const f32x4*)(part(min(i + k * GR, parts - 1)) + row * D + dq);
+  };
+  const float* mine = part(min(lane, parts - 1)) + TM * D + row;
+  const float m0 = mine[0], l0 = mine[TM];
+  load_o(pg);
+  float M = lane < parts ? m0 : -INFINITY;
+  for (int i = lane + kWave; i < parts; i += kWave) M = fmaxf(M, part(i)[TM * D + row]);
+  M = wave_max(M);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   float L = 0.f;
   for (int i0 = 0; i0 < parts; i0 += kWave) {
     float f = 0.f;
     if (i0 + lane < parts) {
       const float* pp = part(i0 + lane) + TM * D + row;
-      const float m = pp[0];
+      const float m = i0 ? pp[0] : m0, l = i0 ? pp[TM] : l0;
       f = m == M ? 1.f : at_exp2(m - M);
-      L += pp[TM] * f;
+      L += l * f;
     }
     wt[wv][lane] = f;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const int m = min(kWave, parts - i0);
-    for (int i = pg; i < m; i += 8 * GR) {
-      f32x4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = *(const f32x4*)(part(i0 + min(i + k * GR, m - 1)) + row * D + dq);
+    wave_sync();
+    const int e = min(kWave, parts - i0);
+    for (int i = pg; i < e; i += 8 * GR) {
+      if (i0 + i != pg) load_o(i0 + i);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (i + k * GR < m) {
+        if (i + k * GR < e) {
           const float f2 = wt[wv][i + k * GR];
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[c] = fmaf(v[k][c], f2, acc[c]);
         }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_sync();
   }
   L = wave_sum(L);
 #pragma unroll
@@ -688,8 +699,11 @@ hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
   switch (p.head_dim * 8 + mt) {
     case 64 * 8 + 1: return launch_one<BF, 64, 1>(p, W, st);
     case 64 * 8 + 2: return launch_one<BF, 64, 2>(p, W, st);
+    case 64 * 8 + 3: return launch_one<BF, 64, 3>(p, W, st);
+    case 64 * 8 + 4: return launch_one<BF, 64, 4>(p, W, st);
     case 128 * 8 + 1: return launch_one<BF, 128, 1>(p, W, st);
     case 128 * 8 + 2: return launch_one<BF, 128, 2>(p, W, st);
+    case 128 * 8 + 3: return launch_one<BF, 128, 3>(p, W, st);
     case 256 * 8 + 1: return launch_one<BF, 256, 1>(p, W, st);
   }
   return hipErrorInvalidValue;

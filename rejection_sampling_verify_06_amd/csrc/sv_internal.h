@@ -247,7 +247,7 @@ struct AttnParams {
   float* lse;                       // or NULL
   int32_t* status;                  // or NULL
   float* parts;                     // [blocks][2] parts of 16 row_tiles * (head_dim + 2) floats
-  void* desc;                       // [blocks + 1] records
+  void* desc;                       // [blocks] records
 };
 
 hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);

@@ -84,12 +84,18 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
     *s = AttnShape{1, 1, 0};
     return true;
   }
-  // The tile of a (sequence, key head) as high as the batch's average needs:
-  // a higher one would hold registers for rows that are not there, a lower
-  // one reads the keys again for every further tile.
+  // The tile of a (sequence, key head) as high as the batch's average needs,
+  // as far as the registers hold it: a higher one costs registers and products
+  // for rows that are not there, a lower one reads the keys again for every
+  // further tile, from the last-level cache at the same rate.  32 sequences of
+  // 4096, 8 key heads of 128, 36 rows: 3 tiles of 16 102 us, 2 (two blocks of
+  // work) 114; 64 rows: 2 tiles 113 us, 3 185, 4 (spilled) 187.  64 sequences,
+  // 64 rows of 64: 4 tiles 102 us, 3 160, 2 153.  16 sequences with 40 rows of
+  // 256 in a window of 4096: 1 tile 39 us, 2 (spilled) 63.
   const int64_t group = a->heads / a->kv_heads;
   const int64_t rows = (a->total_rows + a->batch - 1) / a->batch * group;
-  s->row_tiles = rows <= 16 || a->head_dim == 256 ? 1 : 2;
+  const int tiles = (int)std::min<int64_t>((rows + 15) / 16, 4);
+  s->row_tiles = a->head_dim == 256 ? 1 : a->head_dim == 64 ? tiles : tiles == 4 ? 2 : tiles;
   const int64_t tm = 16 * s->row_tiles;
   const int64_t keys = (int64_t)a->max_pages * a->page_size;
   const int64_t units = (a->total_rows * group / tm + a->batch) * a->kv_heads *
@@ -98,7 +104,13 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
     set_err("%s: %lld units of work: batch, heads and max_pages are too large together", who, (long long)units);
     return false;
   }
-  s->blocks = (int)std::min<int64_t>(units, 512);
+  // One block per CU keeps enough reads in flight for heads of 128 and 256 and
+  // leaves the fewest parts to join (32 sequences of 4096 with 24 rows of 128:
+  // 97 + 5 us, with two 101 + 9); heads of 64, and tiles that read the keys
+  // again, want two (64 sequences of 4096: 135 us with one, 95 with two; 64
+  // rows of 128: 157 and 113).
+  const bool twice = a->head_dim == 64 || (a->head_dim == 128 && rows > tm);
+  s->blocks = (int)std::min<int64_t>(units, twice ? 512 : 256);
   s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
   return true;
 }
@@ -248,7 +260,7 @@ int64_t spec_verify_attention_args_size(void) { return (int64_t)sizeof(spec_veri
 int64_t spec_verify_attention_workspace(const spec_verify_attention_args* a) {
   AttnShape s;
   if (!attention_sizes_ok("spec_verify_attention_workspace", a, &s)) return SV_ERR_INVALID;
-  return s.blocks * s.part_bytes + (int64_t)(s.blocks + 1) * sv::kAttnPartBytes;
+  return s.blocks * s.part_bytes + (int64_t)s.blocks * sv::kAttnPartBytes;
 }
 
 int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_stream) {
