@@ -586,7 +586,7 @@ class PagedCache:
         self._ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         c.page_table, c.seq_len, c.refcount = _ptr(self.page_table), _ptr(self.seq_len), _ptr(self.refcount)
         c.k, c.v, c.workspace, c.workspace_bytes = _ptr(self.k), _ptr(self.v), _ptr(self._ws), nbytes
-        self._c = c
+        self._c, self._heads = c, (c.kv_heads, c.head_dim)
         self._ref = ctypes.byref(c)
 
     def _entries(self, seqs, counts, name):
@@ -615,23 +615,22 @@ class PagedCache:
     def write(self, layer: int, k_new, v_new, slots, stream=None):
         """Puts rows of ``k_new`` / ``v_new`` ([rows, kv_heads, head_dim], unit
         stride in head_dim) into the places ``slots`` of ``reserve``."""
-        torch = self._torch
-        rows = int(slots.numel())
-        _need(slots, "slots", (torch.int64,), torch, None, self.device)
+        rows, dev, heads = slots.numel(), self.device, self._heads
+        _need(slots, "slots", (self._torch.int64,), self._torch, None, dev)
         for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-            if tuple(t.shape) != (rows, self._c.kv_heads, self._c.head_dim) or t.stride(2) != 1:
-                raise ValueError(f"{name} must be [{rows}, {self._c.kv_heads}, {self._c.head_dim}] with unit stride in the last "
-                                 f"dimension, got {tuple(t.shape)}")
+            if t.shape != (rows, *heads) or t.stride(2) != 1:
+                raise ValueError(f"{name} must be [{rows}, {heads[0]}, {heads[1]}] with unit stride in the last dimension, got "
+                                 f"{tuple(t.shape)}")
             if t.dtype != self.k.dtype:
                 raise TypeError(f"{name} is {t.dtype}, the cache {self.k.dtype}")
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        one = self._c.kv_heads == 1
-        with _on_stream(self.device, stream):
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+        # strides of dimensions of size 1 say nothing
+        r, h = rows > 1, heads[0] > 1
+        with _on_stream(dev, stream):
             _check(self._lib.spec_verify_cache_write(
-                self._ref, int(layer), rows, k_new.data_ptr(), k_new.stride(0) if rows > 1 else 0, 0 if one else k_new.stride(1),
-                v_new.data_ptr(), v_new.stride(0) if rows > 1 else 0, 0 if one else v_new.stride(1), slots.data_ptr(),
-                _queue(self.device)))
+                self._ref, int(layer), rows, k_new.data_ptr(), k_new.stride(0) if r else 0, k_new.stride(1) if h else 0,
+                v_new.data_ptr(), v_new.stride(0) if r else 0, v_new.stride(1) if h else 0, slots.data_ptr(), _queue(dev)))
 
     def attend(self, layer: int, q, num_draft, seqs=None, **kw) -> dict:
         """``paged_attention`` of ``q`` over a layer of this cache."""

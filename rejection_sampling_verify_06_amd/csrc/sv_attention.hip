@@ -131,6 +131,7 @@ __device__ __forceinline__ float column_sum(float v) {
 struct Extent {
   int slot;       // row of page_table and seq_len; -1: refused
   int len;        // cached tokens (0 for a refused sequence)
+  int first;      // first position any row sees
   int blk0;       // first 128-key block any row sees
   int nblk;       // blocks, at least 1 (an empty sequence still writes its rows)
 };
@@ -142,8 +143,8 @@ __device__ __forceinline__ Extent seq_extent(const AttnParams& P, int b, int n) 
   const bool ok = (unsigned)x.slot < (unsigned)P.slots && len >= 0 && len <= P.max_len;
   x.slot = ok ? x.slot : -1;
   x.len = ok ? len : 0;
-  const int first = P.window > 0 ? max(0, x.len - n + 1 - P.window) : 0;
-  x.blk0 = first / kUnitKeys;
+  x.first = P.window > 0 ? max(0, x.len - n + 1 - P.window) : 0;
+  x.blk0 = x.first / kUnitKeys;
   x.nblk = max(1, (x.len + kUnitKeys - 1) / kUnitKeys - x.blk0);
   return x;
 }
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
     while ((uint32_t)uni((int)units[b + 1]) <= u) ++b;
     const int row0 = uni((int)rows[b]), n = uni((int)rows[b + 1]) - row0;
     Extent x = seq_extent(P, b, n);
-    x = Extent{uni(x.slot), uni(x.len), uni(x.blk0), uni(x.nblk)};
+    x = Extent{uni(x.slot), uni(x.len), uni(x.first), uni(x.blk0), uni(x.nblk)};
     const uint32_t rel = u - (uint32_t)uni((int)units[b]);
     const int seg = (int)(rel / (uint32_t)x.nblk), b0 = (int)(rel - (uint32_t)seg * x.nblk);
     const int b1 = (int)min((uint32_t)x.nblk, b0 + (u_end - u));
@@ -324,13 +325,13 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
       id0 = table[pos >> P.page_log2];
       id1 = table[min(pos + 16, x.len - 1) >> P.page_log2];
     };
-    // Base addresses; a page outside the pool is replaced by page 0 and noted.
+    // Base addresses; a page outside the pool is replaced by page 0, and noted
+    // unless a window hides all of the tile (its pages may be gone by then).
     auto locate = [&](int pos) {
-      if ((unsigned)id0 >= (unsigned)P.num_pages || (unsigned)id1 >= (unsigned)P.num_pages) {
-        bad = true;
-        id0 = (unsigned)id0 >= (unsigned)P.num_pages ? 0 : id0;
-        id1 = (unsigned)id1 >= (unsigned)P.num_pages ? 0 : id1;
-      }
+      const bool bad0 = (unsigned)id0 >= (unsigned)P.num_pages, bad1 = (unsigned)id1 >= (unsigned)P.num_pages;
+      bad |= (bad0 && pos + 16 > x.first) || (bad1 && pos + 32 > x.first);
+      id0 = bad0 ? 0 : id0;
+      id1 = bad1 ? 0 : id1;
       const int off0 = pos & pmask, off1 = (pos + 16) & pmask;
       kb[0] = (const char*)P.k + 2 * ((int64_t)id0 * P.k_page + (int64_t)head * P.k_head + (int64_t)off0 * P.k_tok);
       kb[1] = (const char*)P.k + 2 * ((int64_t)id1 * P.k_page + (int64_t)head * P.k_head + (int64_t)off1 * P.k_tok);
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
           s = SV_ST_BAD_LENGTH;
         } else {
           const Extent x = seq_extent(P, b, n);
-          const int p0 = (x.blk0 * kUnitKeys) >> P.page_log2;
+          const int p0 = x.first >> P.page_log2;
           const int p1 = (len + (1 << P.page_log2) - 1) >> P.page_log2;
           for (int i = p0 + t; i < p1; i += kAtThreads)
             if ((unsigned)P.table[(int64_t)slot * P.table_stride + i] >= (unsigned)P.num_pages) s = SV_ST_BAD_PAGE;

@@ -40,7 +40,7 @@ constexpr int kSegs = kChunkBytes / kSegBytes;              // 64 segments to a 
 constexpr int kPasses = kSegs / (kLpThreads / 8);           // 2: segments per group of 8 lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
-constexpr float kSafe = 0x1p120f;                           // |M c| below this: fma(x, c, -M c) cannot overflow upwards
+constexpr float kSafe = 0x1p20f;                            // |M c| below this: 2^(M c - round(M c)) is near 1
 constexpr float kMinTemp = SV_MIN_TEMPERATURE;
 
 __device__ __forceinline__ float lp_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -107,13 +107,15 @@ __device__ __forceinline__ float lp_value(const LogprobParams& P, int64_t row, f
   return fminf((y - logS) * kLn2, 0.f);
 }
 
-// (S, W) of maximum m brought to maximum M >= m.  The shift is the difference
-// of the two rounded references; where one of them would overflow the sums
-// were taken against (x - m) c instead.
+// (S, W) of maximum m brought to maximum M >= m.  Sums are taken against
+// round(m c) where that is below kSafe (one rounding per term, and the same
+// reference for all), against m c itself, as (x - m) c, above; the shift is the
+// difference of the two references.
 __device__ __forceinline__ void rebase(float m, float M, float c, float& S, float& W) {
   if (m == M || m == -INFINITY) return;                     // an empty part has S = W = 0 (or NaN, which stays)
-  const bool safe = fabsf(m * c) < kSafe && fabsf(M * c) < kSafe;
-  const float d = safe ? M * c - m * c : (M - m) * c;
+  const float k = m * c, K = M * c;
+  const bool sm = fabsf(k) < kSafe, sM = fabsf(K) < kSafe;
+  const float d = sm && sM ? K - k : (M - m) * c + (sm ? fmaf(m, c, -k) : 0.f) - (sM ? fmaf(M, c, -K) : 0.f);
   const float r = lp_exp2(-d);
   W = r > 0.f ? (W + d * S) * r : (S == S ? 0.f : S);
   S = r > 0.f ? S * r : (S == S ? 0.f : S);
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(kLpThreads, 6) k_logprob_chunks(LogprobParams 
   const float K = M * c;
   if (fabsf(K) < kSafe) {
     chunk_sums<R, ENT, RANK>(v, [&](float x) { return fmaf(x, c, -K); }, xt, S, W, n);
-  } else {                                                  // no finite maximum, or K near overflow
+  } else {                                                  // no finite maximum, or a small temperature
     const float Mr = M == -INFINITY ? 0.f : M;
     chunk_sums<R, ENT, RANK>(v, [&](float x) { return (x - Mr) * c; }, xt, S, W, n);
   }

@@ -151,6 +151,42 @@ def test_what_a_row_does_not_see(sv, dtype, D, what):
     _near(sv.paged_attention(q, k, v, table, seq_len, _i32(nd), want_lse=True, window=20), ref, dtype)
 
 
+@pytest.mark.parametrize("P", [16, 64])
+def test_pages_behind_a_window_may_be_gone(sv, P):
+    dtype, L, nd, window = torch.bfloat16, [700, 300, 90], [3, 0, 5], 100
+    k, v, table, seq_len = su.make_pages(L, P, 2, 64, dtype, 18)
+    q = _q(11, 4, 64, dtype, 18)
+    want = sv.paged_attention(q, k, v, table, seq_len, _i32(nd), window=window, want_lse=True)
+    for b, n in enumerate(L):
+        gone = max(0, n - nd[b] - window) // P                   # pages no row sees anything of
+        table[b, :gone] = torch.tensor([-1, 1 << 30], dtype=torch.int32).repeat(99)[:gone].cuda()
+    got = sv.paged_attention(q, k, v, table, seq_len, _i32(nd), window=window, want_lse=True)
+    assert not got["status"].any()
+    for key in want:
+        assert torch.equal(want[key], got[key])
+    _near(got, su.attention_ref(q, k, v, table.clamp(min=0).clamp(max=k.shape[0] - 1), seq_len, _i32(nd), window=window), dtype)
+    table[0, max(0, 700 - 3 - window) // P] = -1                   # the first page that is seen
+    assert sv.paged_attention(q, k, v, table, seq_len, _i32(nd), window=window)["status"].tolist() == [1024, 0, 0]
+
+
+@pytest.mark.parametrize("D,H", [(64, 64), (128, 40), (128, 64), (256, 20)])
+def test_largest_batch(sv, D, H):
+    """4096 sequences of a few tokens, every height of row tile."""
+    dtype = torch.float16
+    L = [1 + i % 3 for i in range(4096)]
+    k, v, table, seq_len = su.make_pages(L, 16, 1, D, dtype, 19)
+    q, nd = _q(4096, H, D, dtype, 19), torch.zeros(4096, dtype=torch.int32, device="cuda")
+    o = sv.paged_attention(q, k, v, table, seq_len, nd, want_lse=True)
+    assert not o["status"].any()
+    kk = torch.stack([k[table[:, 0].long(), 0, j] for j in range(3)], 1).cpu().double()
+    vv = torch.stack([v[table[:, 0].long(), 0, j] for j in range(3)], 1).cpu().double()
+    hide = torch.arange(3)[None] >= torch.tensor(L)[:, None]
+    s = torch.matmul(q.cpu().double(), kk.transpose(1, 2).contiguous()) * D ** -0.5
+    s = s.masked_fill(hide[:, None], -torch.inf)
+    ref = torch.matmul(torch.softmax(s, -1), vv.masked_fill(hide[:, :, None], 0.0))
+    _near(o, (ref, torch.logsumexp(s, -1)), dtype)
+
+
 def test_slots(sv):
     """Sequences in another order than their slots, one slot twice."""
     dtype = torch.bfloat16

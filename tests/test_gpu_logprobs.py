@@ -130,6 +130,43 @@ def test_masked_and_extreme_values(sv, dtype):
     assert abs(lp[3].item() + np.log(V)) < 1e-5
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale,T", [(3.0, 1e-6), (3.0, 1e-4), (1e4, 1e-6), (1e5, 0.05), (1e30, 1.0), (1e38, 1.0), (3.0, 1e30)])
+def test_extreme_exponents(sv, dtype, scale, T):
+    """Logits over temperature far beyond what an exponential holds: one token
+    takes all, or all are alike; whole numbers in units of the scale, so that
+    gaps are either 0 or large."""
+    g = torch.Generator().manual_seed(int(scale) % 1000 + 7)
+    x = (torch.randint(-3, 3, (6, 40000), generator=g).float() * scale).to(dtype)
+    x[:, 100], x[1, 30000], x[2, 0] = 3 * scale, 3 * scale, 3 * scale
+    tok = torch.tensor([100, 30000, 5, 100, 6, 100], dtype=torch.int32)
+    t = torch.full((6,), T)
+    o = sv.token_logprobs(x.cuda(), tok.cuda(), temperature=t.cuda(), top=3)
+    ref = su.logprobs_ref(x, tok.numpy(), t.numpy(), 40000, 3)
+    assert not o["status"].any() and np.array_equal(o["top_tokens"].cpu().numpy(), ref["top_tokens"])
+    for k in ("logprob", "entropy", "top_logprobs"):
+        got, want = o[k].cpu().double().numpy(), ref[k]
+        want = np.where(want < -3.4e38, -np.inf, want)          # beyond float32
+        assert np.array_equal(np.isinf(got), np.isinf(want)), (k, got, want)
+        fine = np.isfinite(want)
+        np.testing.assert_allclose(got[fine], want[fine], rtol=2e-6, atol=1e-5)
+
+
+@pytest.mark.parametrize("base", [0.0, 7.0e5, 7.2682e5, 7.28e5, 1e6, -7.2682e5])
+def test_references_near_their_border(sv, base):
+    """Rows whose scaled maximum lies on both sides of the size up to which it
+    is rounded, in one row: the parts meet on the same scale."""
+    g = torch.Generator().manual_seed(4)
+    x = (torch.randint(0, 64, (2, 60000), generator=g) * 0.0625 + base).float()
+    x[:, :20000] -= 2.0
+    tok = torch.tensor([17, 40000], dtype=torch.int32)
+    o = sv.token_logprobs(x.cuda(), tok.cuda(), top=4)
+    ref = su.logprobs_ref(x, tok.numpy(), None, 60000, 4)
+    # y = x c - round(M c) is rounded once, below 2^-19 here: log2 S and y together are off by 2^-18
+    for k in ("logprob", "entropy", "top_logprobs"):
+        np.testing.assert_allclose(o[k].cpu().double().numpy(), ref[k], rtol=2e-6, atol=2.0 ** -17)
+
+
 def test_skipped_rows_are_not_read(sv):
     logits, tok = _rows(40, 4096, torch.bfloat16, 8)
     tok[::3] = -1
