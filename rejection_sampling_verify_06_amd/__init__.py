@@ -9,6 +9,10 @@ current stream.  PyTorch supplies device memory and streams.
     out = v.run(target, draft, draft_tokens, num_draft, temperature, mode, seed=step)
     out["accepted_len"], out["emitted"], out["p_at"], out["q_at"], out["status"]
 
+Around a decode loop's verify call: ``PagedCache`` (the target's keys and
+values, with ``paged_attention`` over them) and ``token_logprobs`` (of what
+was emitted).
+
 If the library has not been built, every entry point raises ``LibraryMissing``:
 there is no fallback implementation.
 """

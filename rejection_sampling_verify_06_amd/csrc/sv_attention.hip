@@ -33,6 +33,12 @@
 // itself.  A range may end inside a tile; such parts (at most two per block)
 // go to the workspace as (O, m, l), and k_attention_join adds them up in
 // order.
+//
+// Measured on one MI355X (rocprofv3, both kernels): 32 sequences of 4096
+// tokens, 8 key heads of 128, 24 rows a tile, 97 + 5 us (5.5 TB/s of keys and
+// values), of 16384 tokens 368 + 11 us (5.8 TB/s); one row, 99 + 5 us; 64
+// sequences of 4096, 8 heads of 64, 95 + 4 us (5.7 TB/s); one token of one
+// sequence of 777, 7 + 4 us.  A large device copy moves 5.1 TB/s here.
 
 #include <hip/hip_runtime.h>
 #include <math.h>

@@ -12,8 +12,15 @@
 // dependent steps, so each operation is one block of 1024 threads that keeps
 // the entries' prefix sums in shared memory; work on pages or rows is spread
 // over its threads by position, the owning entry found by a binary search of
-// those sums.  Copies of pages and rows are bound by HBM and run on the whole
-// chip, from a list that stays on the device.
+// those sums.  (Four positions of a thread at a time, so that their loads
+// overlap, measured slower: reserve 7.5 -> 10.3 us, truncate 3.2 -> 4.5; the
+// longer code costs more than the overlap saves.)  Copies of pages and rows are
+// bound by HBM and run on the whole chip, from a list that stays on the device.
+//
+// Measured on one MI355X (rocprofv3): 32 sequences growing by up to 6 tokens,
+// reserve 7.5 us and its empty copy 2.3 us, commit 3.2 us, write 2.8 us a layer;
+// 8000 prompt tokens, reserve 13 us, write 14 us a layer (67 MB, 4.8 TB/s); 180
+// pages of 32 KB in 16 pools copied on write, 35 us (5.4 TB/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -16,6 +16,12 @@
 // logits (all of them where a row ties).
 //
 // Sums are kept in 32 bits, in a fixed order; y is rounded once (fma).
+//
+// Measured on one MI355X (rocprofv3): 865 rows of 152064 bf16 logits among
+// 1410 (263 MB) with 20 alternatives, chunks 58 us (4.5 TB/s), rows 18 us;
+// every one of the 1410 rows, without alternatives, 75 us with the entropy (5.7
+// TB/s) and 70 us without (6.1 TB/s); 192 rows of 128255 floats 17 + 4 us;
+// 6 rows of 32000 bf16 with 5 alternatives 6.5 + 8.5 us.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -172,9 +178,11 @@ struct ChunkStats {
 
 }  // namespace
 
-// One block per (row, 32 KB chunk).  Bound by HBM: the 8 vectors of a thread
-// are in flight together, and the waves reduce against their own maximum, so
-// one barrier is left.
+// One block per (row, 32 KB chunk).  Bound by HBM and by its own ramp (about
+// 10 us of a launch do not scale with the bytes): the 8 vectors of a thread are
+// in flight together, and the waves reduce against their own maximum, so one
+// barrier is left.  Six waves to a SIMD: more would spill, and measured no
+// faster (80 registers 59 us, 64 with spills 64).
 template <bool BF, bool ENT, bool RANK>
 __global__ void __launch_bounds__(kLpThreads, 6) k_logprob_chunks(LogprobParams P) {
   using R = Row<BF>;
@@ -376,8 +384,11 @@ __device__ __forceinline__ float nth_of_all(const float (&x)[N], int n) {
 }  // namespace
 
 // One wave per row: merges the chunks, writes the row's values, finds its top
-// n.  Bound by latency (four dependent loads: token, partials and maxima,
-// segments, and the search between them).
+// n.  Bound by latency: the token, the partials and maxima, the segments, the
+// search and sorts between them, and the fetch of code that runs once (8 us
+// for one alternative, 14 us for 20, 35 us for 64; gathering the tokens of up
+// to 32 segments and sorting them 64 at a time took 18 us where inserting them
+// one by one took 61).
 template <bool BF>
 __global__ void __launch_bounds__(kWave) k_logprob_rows(LogprobParams P) {
   using R = Row<BF>;
