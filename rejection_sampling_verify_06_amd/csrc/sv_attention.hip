@@ -384,11 +384,13 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
       f32x4 sc[MT][2];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
+        if (m == 0 || m * 16 < nrow) {           // a short sequence leaves the higher tiles out
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          sc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int h = 0; h < 2; ++h) {
+            sc[m][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < NS; ++s) sc[m][h] = mfma<BF>(kr[h][s], qs[m][s][lane], sc[m][h]);
+            for (int s = 0; s < NS; ++s) sc[m][h] = mfma<BF>(kr[h][s], qs[m][s][lane], sc[m][h]);
+          }
         }
       if (more) {
         locate(pos + kUnitKeys);
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
       u32x4 ph[MT], pl[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        if (m > 0 && m * 16 >= nrow) continue;
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = sc[m][e >> 2][e & 3] * P.scale_log2;
@@ -461,6 +464,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
           }
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
+            if (m > 0 && m * 16 >= nrow) continue;
             f32x4 d = mfma<BF>(a, ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
             d = mfma<BF>(a, pl[m], d);
 #pragma unroll
@@ -480,10 +484,11 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
         for (int i = 0; i < 4; ++i)
           a[i] = __builtin_amdgcn_perm(vr[2 * i + 1][j >> 1], vr[2 * i][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          o[m][j] = mfma<BF>(a, ph[m], o[m][j]);
-          o[m][j] = mfma<BF>(a, pl[m], o[m][j]);
-        }
+        for (int m = 0; m < MT; ++m)
+          if (m == 0 || m * 16 < nrow) {
+            o[m][j] = mfma<BF>(a, ph[m], o[m][j]);
+            o[m][j] = mfma<BF>(a, pl[m], o[m][j]);
+          }
       }
       if (more) load_v();
     }
@@ -505,6 +510,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) 
     float* part = part_at(P, (int)w, b0 > 0 ? 0 : 1, TM, D);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      if (m * 16 >= nrow) break;
       const int r = m * 16 + col;
       float M = ml[0][0][r], L = 0.f;
 #pragma unroll
@@ -706,7 +712,6 @@ hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
   switch (p.head_dim * 8 + mt) {
     case 64 * 8 + 1: return launch_one<BF, 64, 1>(p, W, st);
     case 64 * 8 + 2: return launch_one<BF, 64, 2>(p, W, st);
-    case 64 * 8 + 3: return launch_one<BF, 64, 3>(p, W, st);
     case 64 * 8 + 4: return launch_one<BF, 64, 4>(p, W, st);
     case 128 * 8 + 1: return launch_one<BF, 128, 1>(p, W, st);
     case 128 * 8 + 2: return launch_one<BF, 128, 2>(p, W, st);

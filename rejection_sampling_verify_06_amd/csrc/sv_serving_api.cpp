@@ -84,18 +84,25 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
     *s = AttnShape{1, 1, 0};
     return true;
   }
-  // The tile of a (sequence, key head) as high as the batch's average needs,
-  // as far as the registers hold it: a higher one costs registers and products
-  // for rows that are not there, a lower one reads the keys again for every
-  // further tile, from the last-level cache at the same rate.  32 sequences of
-  // 4096, 8 key heads of 128, 36 rows: 3 tiles of 16 102 us, 2 (two blocks of
-  // work) 114; 64 rows: 2 tiles 113 us, 3 185, 4 (spilled) 187.  64 sequences,
-  // 64 rows of 64: 4 tiles 102 us, 3 160, 2 153.  16 sequences with 40 rows of
-  // 256 in a window of 4096: 1 tile 39 us, 2 (spilled) 63.
+  // A (sequence, key head)'s rows should fit one block's row tiles: every
+  // further block of tiles reads the keys again, at the same rate.  Tiles that
+  // a short sequence leaves empty cost registers and code, not products.  Only
+  // the sum of the rows is known here, so room is made for half again the
+  // average, or for all that one sequence can have.  32 sequences of 4096, 8
+  // key heads of 128: 4 rows with room for 16, 32, 48 95, 96, 97 us; 24 rows
+  // with 32, 48 97, 99 (ragged, 8 to 24 rows and 1024 to 8192 tokens: 127 and
+  // 134); 36 rows with 32, 48 114, 101.  One token of one sequence, 16 and 48 7
+  // and 10 us.  More than 48 rows of 128 do not fit the registers (64 rows: 2
+  // tiles twice 113 us, 3 tiles twice 182, 4 spilled 187), nor more than 16 of
+  // 256 (40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
+  // of 4096 with 8 heads of 64: 8 rows with room for 16, 32, 64 94, 96, 96 us,
+  // 64 rows with 64, 32 104, 153.
   const int64_t group = a->heads / a->kv_heads;
-  const int64_t rows = (a->total_rows + a->batch - 1) / a->batch * group;
-  const int tiles = (int)std::min<int64_t>((rows + 15) / 16, 4);
-  s->row_tiles = a->head_dim == 256 ? 1 : a->head_dim == 64 ? tiles : tiles == 4 ? 2 : tiles;
+  const int64_t avg = (a->total_rows * group + a->batch - 1) / a->batch;
+  const int64_t room = std::min(avg + avg / 2, (int64_t)(a->total_rows - a->batch + 1) * group);
+  if (a->head_dim == 256 || room <= 16) s->row_tiles = 1;
+  else if (room <= 32 || (a->head_dim == 128 && avg > 48)) s->row_tiles = 2;
+  else s->row_tiles = a->head_dim == 128 ? 3 : 4;
   const int64_t tm = 16 * s->row_tiles;
   const int64_t keys = (int64_t)a->max_pages * a->page_size;
   const int64_t units = (a->total_rows * group / tm + a->batch) * a->kv_heads *
@@ -106,10 +113,10 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
   }
   // One block per CU keeps enough reads in flight for heads of 128 and 256 and
   // leaves the fewest parts to join (32 sequences of 4096 with 24 rows of 128:
-  // 97 + 5 us, with two 101 + 9); heads of 64, and tiles that read the keys
-  // again, want two (64 sequences of 4096: 135 us with one, 95 with two; 64
-  // rows of 128: 157 and 113).
-  const bool twice = a->head_dim == 64 || (a->head_dim == 128 && rows > tm);
+  // 97 + 4 us, with two 101 + 9); heads of 64, and tiles that read the keys
+  // again, want two (64 sequences of 4096 with 8 heads of 64: 96 and 94 us; 64
+  // rows of 128: 156 and 113).
+  const bool twice = a->head_dim == 64 || (a->head_dim == 128 && avg > 48);
   s->blocks = (int)std::min<int64_t>(units, twice ? 512 : 256);
   s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
   return true;
