@@ -194,6 +194,10 @@ hipError_t launch_adapt_reset(const AdaptParams& p, hipStream_t st);
 // log probabilities of given tokens (sv_logprobs.hip)
 constexpr int64_t kMaxGrid = 65535;     // blocks per grid dimension
 
+constexpr int kLpChunkBytes = 16384;    // bytes of one row that a block of the chunk pass reads
+constexpr int kLpSegBytes = 512;        // a segment: 8 lanes, 4 vectors of 16 bytes each
+constexpr int kLpSegs = kLpChunkBytes / kLpSegBytes;
+
 struct LogprobParams {
   int64_t rows;
   int64_t V;
@@ -201,7 +205,7 @@ struct LogprobParams {
   const void* logits;
   int32_t bf16;
   int32_t top;
-  int64_t nch;                 // 32 KB chunks per row
+  int64_t nch;                 // chunks per row
   const int32_t* tokens;       // or NULL
   const float* temperature;    // or NULL
   float* logprob;
@@ -211,7 +215,7 @@ struct LogprobParams {
   float* top_logprobs;
   int32_t* status;
   float* partials;             // [rows][nch][4]: M, S, W, count
-  float* segmax;               // [rows][nch][64] segment maxima, or NULL (top = 0)
+  float* segmax;               // [rows][nch][kLpSegs] segment maxima, or NULL (top = 0)
 };
 
 hipError_t launch_logprobs(const LogprobParams& p, hipStream_t st);

@@ -7,7 +7,7 @@
 //   entropy   = (log2 S + W / S) ln 2            (both terms are >= 0 up to rounding)
 //   rank(t)   = 1 + the number of logits > x_t
 //   top n     = the n largest logits, the lower index first on ties
-// One read of the logits carries all of it: k_logprob_chunks reduces 32 KB of
+// One read of the logits carries all of it: k_logprob_chunks reduces 16 KB of
 // a row to (M, S, W, count) and the maximum of each 512-byte segment, and
 // k_logprob_rows merges a row's chunks and finds its top n.  It takes the
 // largest segment maximum of each lane (64 interleaved sets of segments); the
@@ -18,10 +18,9 @@
 // Sums are kept in 32 bits, in a fixed order; y is rounded once (fma).
 //
 // Measured on one MI355X (rocprofv3): 865 rows of 152064 bf16 logits among
-// 1410 (263 MB) with 20 alternatives, chunks 58 us (4.5 TB/s), rows 18 us;
-// every one of the 1410 rows, without alternatives, 75 us with the entropy (5.7
-// TB/s) and 70 us without (6.1 TB/s); 192 rows of 128255 floats 17 + 4 us;
-// 6 rows of 32000 bf16 with 5 alternatives 6.5 + 8.5 us.
+// 1410 (263 MB) with 20 alternatives, chunks 52 us (5.1 TB/s), rows 18 us; every
+// one of the 1410 rows, without alternatives, 69 us (6.2 TB/s); 192 rows of
+// 128255 floats 15 + 4 us; 6 rows of 32000 bf16 with 5 alternatives 5.3 + 8.6.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -41,9 +40,9 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWaves = kLpThreads / kWave;
-constexpr int kSegBytes = 512;                              // a segment: 8 lanes, 4 vectors of 16 bytes each
-constexpr int kSegs = kChunkBytes / kSegBytes;              // 64 segments to a chunk
-constexpr int kPasses = kSegs / (kLpThreads / 8);           // 2: segments per group of 8 lanes
+constexpr int kSegBytes = kLpSegBytes;
+constexpr int kSegs = kLpSegs;
+constexpr int kPasses = kSegs / (kLpThreads / 8);           // segments per group of 8 lanes
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kSafe = 0x1p20f;                            // |M c| below this: 2^(M c - round(M c)) is near 1
@@ -58,7 +57,7 @@ struct Row {
   static constexpr int ES = BF ? 2 : 4;
   static constexpr int VEC = 16 / ES;
   static constexpr int SEG = kSegBytes / ES;
-  static constexpr int CHUNK = kChunkBytes / ES;
+  static constexpr int CHUNK = kLpChunkBytes / ES;
   const char* base;
   int shift;
   __device__ __forceinline__ Row(const LogprobParams& P, int64_t row) {
@@ -178,13 +177,13 @@ struct ChunkStats {
 
 }  // namespace
 
-// One block per (row, 32 KB chunk).  Bound by HBM and by its own ramp (about
-// 10 us of a launch do not scale with the bytes): the 8 vectors of a thread are
+// One block per (row, 16 KB chunk).  Bound by HBM and by its own ramp (about
+// 10 us of a launch do not scale with the bytes): the 4 vectors of a thread are
 // in flight together, and the waves reduce against their own maximum, so one
-// barrier is left.  Six waves to a SIMD: more would spill, and measured no
-// faster (80 registers 59 us, 64 with spills 64).
+// barrier is left.  Chunks of 32 KB (8 vectors, 79 registers, 6 waves to a SIMD)
+// took 58 us where these (47 registers) take 52.
 template <bool BF, bool ENT, bool RANK>
-__global__ void __launch_bounds__(kLpThreads, 6) k_logprob_chunks(LogprobParams P) {
+__global__ void __launch_bounds__(kLpThreads, 8) k_logprob_chunks(LogprobParams P) {
   using R = Row<BF>;
   constexpr int VEC = R::VEC;
   __shared__ ChunkStats part[kLpWaves];

@@ -18,7 +18,7 @@ namespace {
 constexpr int64_t kMaxVocab = (int64_t)sv::kMaxTiles * sv::kTileElems;
 
 // Chunks of a row: its elements behind at most the 16-byte boundary in front of them.
-int64_t logprob_chunks(int64_t vocab, int es) { return (vocab * es + (16 - es) + sv::kChunkBytes - 1) / sv::kChunkBytes; }
+int64_t logprob_chunks(int64_t vocab, int es) { return (vocab * es + (16 - es) + sv::kLpChunkBytes - 1) / sv::kLpChunkBytes; }
 
 bool logprob_sizes_ok(const char* who, int64_t rows, int64_t vocab, int32_t dtype, int32_t top) {
   if (dtype != SV_F32 && dtype != SV_BF16) {
@@ -30,7 +30,7 @@ bool logprob_sizes_ok(const char* who, int64_t rows, int64_t vocab, int32_t dtyp
     return false;
   }
   if (rows < 0 || rows > INT32_MAX / logprob_chunks(vocab, dtype == SV_BF16 ? 2 : 4)) {
-    set_err("%s: rows %lld outside 0..2^31 / (32 KB chunks of a row)", who, (long long)rows);
+    set_err("%s: rows %lld outside 0..2^31 / (16 KB chunks of a row)", who, (long long)rows);
     return false;
   }
   if (top < 0 || top > SV_LOGPROBS_MAX_TOP || top > vocab) {
@@ -209,7 +209,7 @@ int64_t spec_verify_logprobs_args_size(void) { return (int64_t)sizeof(spec_verif
 int64_t spec_verify_logprobs_workspace(int64_t rows, int64_t vocab, int32_t dtype, int32_t top) {
   if (!logprob_sizes_ok("spec_verify_logprobs_workspace", rows, vocab, dtype, top)) return SV_ERR_INVALID;
   const int64_t chunks = rows * logprob_chunks(vocab, dtype == SV_BF16 ? 2 : 4);
-  return chunks * (16 + (top > 0 ? 4 * 64 : 0));
+  return chunks * (16 + (top > 0 ? 4 * sv::kLpSegs : 0));
 }
 
 int spec_verify_token_logprobs(const spec_verify_logprobs_args* a, void* hip_stream) {
