@@ -469,19 +469,6 @@ __global__ void __launch_bounds__(kWave) k_logprob_rows(LogprobParams P) {
     // of 256 rows 35 us against 134; up to 32 both list about as many.
     if (top > 32 && nseg > top && nseg <= NM * kWave) floor = fmaxf(floor, nth_of_all<BF, NM>(x, top));
     int held = 0;
-    auto merge_held = [&]() {
-      wave_sync();
-      for (int k0 = 0; k0 < held; k0 += kWave) {
-        uint64_t k = k0 + lane < held ? cand[k0 + lane] : 0;
-        if (__ballot(k > lane_key(best, top - 1))) {
-          sort_keys(k, lane);
-          merge_keys(best, k, lane);
-        }
-      }
-      held = 0;
-      floor = fmaxf(floor, key_value(lane_key(best, top - 1)));
-      wave_sync();
-    };
     // tokens of a segment that reach `floor`, gathered to be sorted 64 at a time and merged into the top list
     auto gather = [&](const uint32_t (&raw)[PER], int e) {
 #pragma unroll
@@ -506,58 +493,82 @@ __global__ void __launch_bounds__(kWave) k_logprob_rows(LogprobParams P) {
       for (int q = 0; q < PER; ++q) raw[q] = r.raw(e + q, V);
       gather(raw, e);
     }
-    for (int r0 = 0; r0 < nseg; r0 += NM * kWave) {
-      if (nseg > NM * kWave) load_maxima(r0);
-      int listed = 0;
-#pragma unroll
-      for (int j = 0; j < NM; ++j) {
-        const int i = r0 + j * kWave + lane;
-        const bool reach = x[j] >= floor && i >= inner0 && i < inner1;
-        const uint64_t all = __ballot(reach);
-        if (all) {
-          if (reach) list[listed + __popcll(all & lower)] = i;
-          listed += __popcll(all);
-        }
-      }
-      wave_sync();
-      for (int s0 = 0; s0 < listed; s0 += kStage) {
-        // 8 bytes a lane, all in flight: a batch costs one latency of the logits
-        u32x2 w[kStage];
-#pragma unroll
-        for (int j = 0; j < kStage; ++j)
-          w[j] = *(const u32x2*)(r.base + (int64_t)(list[min(s0 + j, listed - 1)] * R::SEG - r.shift + lane * PER) * R::ES);
-        float m = -INFINITY;                                // the lanes' largest tokens may raise the floor
-#pragma unroll
-        for (int j = 0; j < kStage; ++j) {
-          stage[j][lane] = w[j];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (s0 + j < listed) m = fmaxf(m, __uint_as_float(BF ? w[j][q] & 0xFFFF0000u : w[j][q]));
-            if (BF && s0 + j < listed) m = fmaxf(m, __uint_as_float(w[j][q] << 16));
-          }
-        }
-        floor = fmaxf(floor, nth_of_wave<BF>(m, top));
-        wave_sync();
-        const int names = list[min(s0 + lane, listed - 1)], n_here = min(kStage, listed - s0);
-        for (int j0 = 0; j0 < n_here; j0 += 4) {
+    // A list of the whole segments that reach the floor, batches of it read
+    // into shared memory, their tokens gathered until there are enough to
+    // sort: one loop, so that its code, most of which runs once, is there once.
+    int r0 = 0, listed = 0, s0 = 0, j0 = 0, here = 0, names = 0;
+    bool done = false;
+    while (true) {
+      while (!done && held <= kHeldMore) {
+        if (j0 < here) {                                    // four segments of the batch
           u32x2 v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = stage[j0 + j][lane];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (j0 + j >= n_here) break;
+            if (j0 + j >= here) break;
             uint32_t raw[PER];
 #pragma unroll
             for (int q = 0; q < PER; ++q) raw[q] = BF ? (v[j][q / 2] >> (q & 1) * 16) & 0xFFFFu : v[j][q & 1];
             gather(raw, __builtin_amdgcn_readlane(names, j0 + j) * R::SEG - r.shift + lane * PER);
           }
-          if (held > kHeldMore) merge_held();
+          j0 += 4;
+        } else if (s0 < listed) {                           // the next batch: 8 bytes a lane, all in flight
+          wave_sync();
+          u32x2 w[kStage];
+          here = min(kStage, listed - s0);
+          names = list[min(s0 + lane, listed - 1)];
+#pragma unroll
+          for (int j = 0; j < kStage; ++j)
+            w[j] = *(const u32x2*)(r.base + (int64_t)(__builtin_amdgcn_readlane(names, j) * R::SEG - r.shift + lane * PER) * R::ES);
+          float m = -INFINITY;                              // the lanes' largest tokens may raise the floor
+#pragma unroll
+          for (int j = 0; j < kStage; ++j) {
+            stage[j][lane] = w[j];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              m = fmaxf(m, __uint_as_float(BF ? w[j][q] & 0xFFFF0000u : w[j][q]));
+              if (BF) m = fmaxf(m, __uint_as_float(w[j][q] << 16));
+            }
+          }
+          // a batch that is not full repeats its last segment in every lane alike: lane maxima stay what they are
+          floor = fmaxf(floor, nth_of_wave<BF>(m, top));
+          wave_sync();
+          s0 += kStage;
+          j0 = 0;
+        } else if (r0 < nseg) {                             // the next 1024 segments
+          if (nseg > NM * kWave) load_maxima(r0);
+          wave_sync();
+          listed = s0 = 0;
+#pragma unroll
+          for (int j = 0; j < NM; ++j) {
+            const int i = r0 + j * kWave + lane;
+            const bool reach = x[j] >= floor && i >= inner0 && i < inner1;
+            const uint64_t all = __ballot(reach);
+            if (all) {
+              if (reach) list[listed + __popcll(all & lower)] = i;
+              listed += __popcll(all);
+            }
+          }
+          wave_sync();
+          r0 += NM * kWave;
+        } else {
+          done = true;
         }
-        wave_sync();
       }
-      wave_sync();                                          // the list is written again
+      wave_sync();
+      for (int k0 = 0; k0 < held; k0 += kWave) {
+        uint64_t k = k0 + lane < held ? cand[k0 + lane] : 0;
+        if (__ballot(k > lane_key(best, top - 1))) {
+          sort_keys(k, lane);
+          merge_keys(best, k, lane);
+        }
+      }
+      if (done) break;
+      held = 0;
+      floor = fmaxf(floor, key_value(lane_key(best, top - 1)));
+      wave_sync();
     }
-    merge_held();
   }
   if (lane < top) {
     float out = skip ? -INFINITY : __builtin_nanf("");
