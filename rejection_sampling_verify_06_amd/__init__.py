@@ -397,18 +397,43 @@ class DraftLengthController:
         return self.next_k
 
 
+def _int32(v, name) -> int:
+    """An argument of the C interface that is an int32 (ctypes would wrap it)."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} {v} does not fit 32 bits")
+    return v
+
+
 _AS_IT_IS = contextlib.nullcontext()
 
 
-def _on_stream(dev, stream):
+def _on_stream(dev, stream, *inputs):
     """A context in which a call's stream is torch's current one (so that what
-    the call allocates belongs to it) and its device the current device."""
+    the call allocates belongs to it) and its device the current device.  On a
+    stream that is given, the inputs may have been allocated on another one:
+    their memory is kept until this one has passed the call."""
     import torch
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
         return torch.cuda.stream(stream)
     return _AS_IT_IS if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _for_caller(out, dev, stream):
+    """The outputs of a call on a stream that was given: allocated there, and
+    kept until the stream the caller works on has passed its use of them."""
+    if stream is not None:
+        import torch
+        caller = torch.cuda.current_stream(dev)
+        for t in out.values() if isinstance(out, dict) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+    return out
 
 
 def _queue(dev) -> int:
@@ -444,11 +469,11 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab
     dtype = _logits_dtype(logits, torch)
     _need(tokens, "tokens", (torch.int32,), torch, R, dev)
     _need(temperature, "temperature", (torch.float32,), torch, R, dev)
-    top = int(top)
+    top = _int32(top, "top")
     nbytes = lib.spec_verify_logprobs_workspace(R, V, dtype, top)
     if nbytes < 0:
         _check(int(nbytes))
-    with _on_stream(dev, stream):
+    with _on_stream(dev, stream, logits, tokens, temperature):
         f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
         out = {
             "logprob": torch.empty(R, **f32) if tokens is not None else None,
@@ -465,7 +490,7 @@ def token_logprobs(logits, tokens=None, *, top: int = 0, temperature=None, vocab
             out["top_tokens"].data_ptr() if top else None, out["top_logprobs"].data_ptr() if top else None,
             _ptr(out["status"]), ws.data_ptr(), nbytes)
         _check(lib.spec_verify_token_logprobs(ctypes.byref(a), _queue(dev)))
-    return out
+    return _for_caller(out, dev, stream)
 
 
 def _cache_dtype(t, name, torch):
@@ -517,7 +542,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     if seqs is None and B > page_table.shape[0]:
         raise ValueError(f"{B} sequences, but page_table has {page_table.shape[0]} rows")
     a = _lib.SpecVerifyAttentionArgs(
-        B, N, H, KV, D, _cache_dtype(q, "q", torch), P, int(window), pages, page_table.shape[0], page_table.shape[1],
+        B, N, H, KV, D, _cache_dtype(q, "q", torch), P, _int32(window, "window"), pages, page_table.shape[0], page_table.shape[1],
         page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1],
         q.data_ptr(), q.stride(0) if N > 1 else 0, q.stride(1) if H > 1 else 0,
         k_pages.data_ptr(), *_page_strides(k_pages), v_pages.data_ptr(), *_page_strides(v_pages),
@@ -526,7 +551,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     nbytes = lib.spec_verify_attention_workspace(ctypes.byref(a))
     if nbytes < 0:
         _check(int(nbytes))
-    with _on_stream(dev, stream):
+    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs):
         out = {
             "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
             "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,
@@ -536,7 +561,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         a.out, a.lse, a.status = out["out"].data_ptr(), _ptr(out["lse"]), _ptr(out["status"])
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
         _check(lib.spec_verify_paged_attention(ctypes.byref(a), _queue(dev)))
-    return out
+    return _for_caller(out, dev, stream)
 
 
 def _page_strides(t):
@@ -574,8 +599,9 @@ class PagedCache:
         dev = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"cached keys and values are bfloat16 or float16, got {dtype}")
-        c = _lib.SpecVerifyCache(int(max_seqs), int(max_pages), int(page_size), int(num_pages), int(layers), int(kv_heads),
-                                 int(head_dim))
+        c = _lib.SpecVerifyCache(*(_int32(v, name) for v, name in (
+            (max_seqs, "max_seqs"), (max_pages, "max_pages"), (page_size, "page_size"), (num_pages, "num_pages"),
+            (layers, "layers"), (kv_heads, "kv_heads"), (head_dim, "head_dim"))))
         nbytes = self._lib.spec_verify_cache_workspace(ctypes.byref(c))
         if nbytes < 0:
             _check(int(nbytes))
@@ -593,6 +619,11 @@ class PagedCache:
         self._c, self._heads = c, (c.kv_heads, c.head_dim)
         self._ref = ctypes.byref(c)
 
+    def _on_stream(self, stream, *inputs):
+        if stream is None:
+            return _on_stream(self.device, None)
+        return _on_stream(self.device, stream, self.k, self.v, self.page_table, self.seq_len, self.refcount, self._ws, *inputs)
+
     def _entries(self, seqs, counts, name):
         """The batch size, with the index arrays checked."""
         torch = self._torch
@@ -608,13 +639,13 @@ class PagedCache:
         and ``status``; -1 in the first two where an entry was refused."""
         torch = self._torch
         B, n = self._entries(seqs, num_new, "num_new"), int(total_new)
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream, seqs, num_new):
             out = {"start": torch.empty(B, dtype=torch.int32, device=self.device),
                    "slots": torch.empty(max(n, 0), dtype=torch.int64, device=self.device),
                    "status": torch.empty(B, dtype=torch.int32, device=self.device)}
             _check(self._lib.spec_verify_cache_reserve(self._ref, B, _ptr(seqs), num_new.data_ptr(), n, _ptr(out["start"]),
                                                        _ptr(out["slots"]), _ptr(out["status"]), _queue(self.device)))
-        return out
+        return _for_caller(out, self.device, stream)
 
     def write(self, layer: int, k_new, v_new, slots, stream=None):
         """Puts rows of ``k_new`` / ``v_new`` ([rows, kv_heads, head_dim], unit
@@ -631,9 +662,9 @@ class PagedCache:
                 raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
         # strides of dimensions of size 1 say nothing
         r, h = rows > 1, heads[0] > 1
-        with _on_stream(dev, stream):
+        with self._on_stream(stream, k_new, v_new, slots):
             _check(self._lib.spec_verify_cache_write(
-                self._ref, int(layer), rows, k_new.data_ptr(), k_new.stride(0) if r else 0, k_new.stride(1) if h else 0,
+                self._ref, _int32(layer, "layer"), rows, k_new.data_ptr(), k_new.stride(0) if r else 0, k_new.stride(1) if h else 0,
                 v_new.data_ptr(), v_new.stride(0) if r else 0, v_new.stride(1) if h else 0, slots.data_ptr(), _queue(dev)))
 
     def attend(self, layer: int, q, num_draft, seqs=None, **kw) -> dict:
@@ -648,50 +679,50 @@ class PagedCache:
         torch = self._torch
         B = self._entries(seqs, num_draft, "num_draft")
         _need(accepted_len, "accepted_len", (torch.int32,), torch, B, self.device)
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream, seqs, num_draft, accepted_len):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_commit(self._ref, B, _ptr(seqs), num_draft.data_ptr(), accepted_len.data_ptr(),
                                                       _ptr(status), _queue(self.device)))
-        return status
+        return _for_caller(status, self.device, stream)
 
     def truncate(self, seqs, drop, stream=None):
         """Takes the last ``drop`` tokens (int32 [batch]) off each sequence."""
         torch = self._torch
         B = self._entries(seqs, drop, "drop")
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream, seqs, drop):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_truncate(self._ref, B, _ptr(seqs), drop.data_ptr() if B else None,
                                                         _ptr(status), _queue(self.device)))
-        return status
+        return _for_caller(status, self.device, stream)
 
     def release(self, seqs, stream=None):
         """Empties the sequences (int32 [batch])."""
         torch = self._torch
         B = self._entries(None, seqs, "seqs")
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream, seqs):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_truncate(self._ref, B, seqs.data_ptr(), None, _ptr(status), _queue(self.device)))
-        return status
+        return _for_caller(status, self.device, stream)
 
     def fork(self, parents, children, stream=None):
         """The empty slots ``children`` share everything ``parents`` hold (both
         int32 [batch]; a parent may be named more than once)."""
         torch = self._torch
         B = self._entries(children, parents, "parents")
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream, parents, children):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_fork(self._ref, B, parents.data_ptr(), children.data_ptr(), _ptr(status),
                                                     _queue(self.device)))
-        return status
+        return _for_caller(status, self.device, stream)
 
     def compact(self, stream=None):
         """Moves the pages in use to the front of the pool; returns their
         number (int32 [1]).  ``slots`` handed out before are void."""
         torch = self._torch
-        with _on_stream(self.device, stream):
+        with self._on_stream(stream):
             live = torch.empty(1, dtype=torch.int32, device=self.device)
             _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), _queue(self.device)))
-        return live
+        return _for_caller(live, self.device, stream)
 
 
 def library_loaded_path() -> str:

@@ -292,3 +292,29 @@ def test_streams_graph_and_repeats(sv):
         for graph, o in graphs:
             for key in fresh:
                 assert torch.equal(fresh[key].nan_to_num(), o[key].nan_to_num()), (i, key)
+
+
+def test_refused_by_the_host(sv):
+    dtype = torch.bfloat16
+    k, v, table, seq_len = su.make_pages([100, 40], 16, 2, 64, dtype, 20)
+    q, nd = _q(3, 4, 64, dtype, 20), _i32([1, 0])
+
+    def call(**kw):
+        a = dict(q=q, k_pages=k, v_pages=v, page_table=table, seq_len=seq_len, num_draft=nd)
+        extra = {n: kw.pop(n) for n in ("seqs", "window", "scale") if n in kw}
+        a.update(kw)
+        return sv.paged_attention(*a.values(), **extra)
+    call()
+    for kw in (dict(q=q[0]), dict(q=q[:, :, :32]), dict(v_pages=v[:, :1]), dict(page_table=table.long()), dict(page_table=table.t()),
+               dict(seq_len=seq_len[:1]), dict(q=q.cpu()), dict(k_pages=k.cpu()), dict(seqs=_i32([0])), dict(num_draft=_i32([0, 0, 0])),
+               dict(window=1 << 32), dict(k_pages=k.transpose(2, 3).contiguous().transpose(2, 3))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(q=q.float()), dict(k_pages=k.half()), dict(num_draft=nd.long()), dict(seqs=nd.float())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    odd = torch.empty(q.numel() + 1, dtype=dtype, device="cuda")[1:].view(q.shape)
+    for kw in (dict(window=-1), dict(scale=float("nan")), dict(q=odd), dict(q=torch.cat([q, q[:, :1]], 1)), dict(q=q[:1]),
+               dict(page_table=table[:, :0])):
+        with pytest.raises(sv.VerifyError):
+            call(**kw)

@@ -257,6 +257,12 @@ def test_refused_by_the_host(sv):
     at = torch.zeros(2, dtype=torch.int64, device="cuda")
     with pytest.raises(sv.VerifyError):
         c.write(2, x, x, at)
+    with pytest.raises(ValueError):
+        c.write(1 << 32, x, x, at)                                         # would be layer 0 in 32 bits
+    with pytest.raises(ValueError):
+        sv.PagedCache(1, (1 << 32) + 10, 16, 1, 64, 2, 2)
+    with pytest.raises(ValueError):
+        sv.token_logprobs(torch.zeros(1, 50, device="cuda"), top=1 << 32)
     with pytest.raises(TypeError):
         c.write(0, x.half(), x, at)
     with pytest.raises(ValueError):
@@ -388,3 +394,43 @@ def test_speculative_rounds(sv):
             at += K[b] + 1
         assert [c.seq_len[s].item() for s in seqs] == [len(hist[s]) for s in seqs]
     ver.close()
+
+
+def test_memory_of_another_stream(sv):
+    """Inputs that are freed, and their memory written, while the stream the
+    calls were queued on has not reached them yet."""
+    c, m = _cache(sv, pages=80, slots=4, width=20)
+    _write(c, m, 0, _reserve(c, m, None, [200, 100]), 1)
+    nd = _i32([1, 0])
+    q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+    x = torch.randn(64, 40000, device="cuda")
+    tok = torch.arange(64, dtype=torch.int32, device="cuda")
+    want = c.attend(0, q, nd)["out"].clone()
+    lp = sv.token_logprobs(x, tok, top=5)
+    rows = torch.randn(2, 2, 64, device="cuda").to(torch.bfloat16)
+    keep = rows.cpu()
+    a = torch.randn(4096, 4096, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            a = torch.tanh(a @ a)
+    sizes = [t.shape for t in (q, nd, x, tok, rows)]
+    o = c.attend(0, q, nd, stream=s)
+    l2 = sv.token_logprobs(x, tok, top=5, stream=s)
+    new = _i32([1, 1])
+    r = c.reserve(None, new, 2, stream=s)
+    c.write(0, rows, rows, r["slots"], stream=s)
+    st = c.commit(None, nd, _i32([0, 0]), stream=s)
+    kinds = [t.dtype for t in (q, nd, x, tok, rows)]
+    del q, nd, x, tok, rows, new
+    junk = [torch.full(size, 77, dtype=kind, device="cuda") for size, kind in zip(sizes, kinds) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(o["out"], want) and st.tolist() == [0, 0] and len(junk) == 15
+    for k in lp:
+        assert torch.equal(lp[k], l2[k]), k
+    slots = m.reserve([0, 1], [1, 1], 2)[1]
+    assert r["slots"].tolist() == slots
+    m.write(0, keep, keep, slots)
+    m.commit([0, 1], [1, 0], [0, 0])
+    m.check(c)
