@@ -318,3 +318,22 @@ def test_refused_by_the_host(sv):
                dict(page_table=table[:, :0])):
         with pytest.raises(sv.VerifyError):
             call(**kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_weights_far_below_the_largest(sv, dtype):
+    """One key far above 30000 others whose weights, 2.7e-5 of its own and
+    below the smallest normal float16, still make up almost half of the sum."""
+    L, D = 30001, 64
+    k, v, table, seq_len = su.make_pages([L], 16, 1, D, dtype, 21)
+    pages = table[0].long()
+    k.zero_(), v.fill_(1.0)
+    k[pages[0], 0, 0, 0] = 10.5 * 8
+    v[pages[0], 0, 0] = -1.0
+    q = torch.zeros(1, 2, D, dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    o = sv.paged_attention(q, k, v, table, seq_len, _i32([0]), want_lse=True)
+    small = (L - 1) * np.exp(-10.5)
+    want = (small - 1) / (small + 1)
+    assert (o["out"].double().cpu() - want).abs().max() < abs(want) * RTOL[dtype] + 2.0 ** -12
+    assert abs(o["lse"][0, 0].item() - (10.5 + np.log1p(small))) < 1e-4

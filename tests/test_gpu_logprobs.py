@@ -105,6 +105,17 @@ def test_ties(sv, dtype):
     _check(sv, rows, tok, top=64)
 
 
+@pytest.mark.parametrize("top", [5, 64])
+def test_ties_over_a_long_row(sv, top):
+    """Rows of one and of few values, longer than what is listed at a time."""
+    V = 600001
+    i = torch.arange(V, dtype=torch.float32)
+    rows = torch.stack([torch.zeros(V), i % 2, (i > V - 30).float(), (i % 9973 == 5).float() * 2,
+                        torch.where(i < 300000, -torch.inf, -3.0)]).to(torch.bfloat16).cuda()
+    tok = torch.tensor([7, 8, V - 1, 5, V - 1], dtype=torch.int32).cuda()
+    _check(sv, rows, tok, top=top)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_masked_and_extreme_values(sv, dtype):
     """-inf and the type's lowest value as masks, all but one token masked,
