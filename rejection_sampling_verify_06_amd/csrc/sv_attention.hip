@@ -222,7 +222,7 @@ __device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, 
 }  // namespace
 
 template <bool BF, int D, int MT>
-__global__ void __launch_bounds__(kAtThreads, D * MT <= 256 && D < 256 ? 2 : 1) k_attention(AttnParams P) {
+__global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : D * MT <= 256 && D < 256 ? 2 : 1) k_attention(AttnParams P) {
   constexpr int TM = 16 * MT;                    // rows of a tile
   constexpr int NS = D / 32;                     // 32-element slices of the head dimension (scores)
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row

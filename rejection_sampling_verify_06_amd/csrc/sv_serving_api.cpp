@@ -113,11 +113,16 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
   }
   // One block per CU keeps enough reads in flight for heads of 128 and 256 and
   // leaves the fewest parts to join (32 sequences of 4096 with 24 rows of 128:
-  // 97 + 4 us, with two 101 + 9); heads of 64, and tiles that read the keys
-  // again, want two (64 sequences of 4096 with 8 heads of 64: 96 and 94 us; 64
-  // rows of 128: 156 and 113).
-  const bool twice = a->head_dim == 64 || (a->head_dim == 128 && avg > 48);
-  s->blocks = (int)std::min<int64_t>(units, twice ? 512 : 256);
+  // 97 + 4 us, with two 101 + 9; ragged 126 + 6 and 128 + 8, with four 132 +
+  // 10); heads of 64, and tiles that read the keys again, want two (64
+  // sequences of 4096 with 8 heads of 64: 96 and 94 us; 64 rows of 128: 156 and
+  // 113).  One row tile of 64 leaves room for four, which hide each other's
+  // changes from tile to tile (256 ragged sequences of 125 to 1000 tokens, 16
+  // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
+  int per_cu = 1;
+  if (a->head_dim == 64) per_cu = s->row_tiles == 1 ? 4 : 2;
+  else if (a->head_dim == 128 && avg > 48) per_cu = 2;
+  s->blocks = (int)std::min<int64_t>(units, 256 * per_cu);
   s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
   return true;
 }
