@@ -526,26 +526,28 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     pages, KV, P, Dk = k_pages.shape
     if D != Dk:
         raise ValueError(f"q has head_dim {D}, the pages {Dk}")
-    for t, name in ((q, "q"), (k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name} is {t.dtype}, q {q.dtype}")
-        if not t.is_cuda or t.device != dev:
-            raise ValueError(f"{name} must be a device tensor on q's device")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name} must have unit stride in its last dimension")
+    if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
+        raise TypeError(f"q is {q.dtype}, the pages {k_pages.dtype} and {v_pages.dtype}")
+    if not q.is_cuda or k_pages.device != dev or v_pages.device != dev:
+        raise ValueError(f"q, k_pages and v_pages must be on one GPU, got {dev}, {k_pages.device} and {v_pages.device}")
+    qs, ks, vs = q.stride(), k_pages.stride(), v_pages.stride()
+    if qs[2] != 1 or ks[3] != 1 or vs[3] != 1:
+        raise ValueError("q, k_pages and v_pages must have unit stride in their last dimension")
     _need(num_draft, "num_draft", (torch.int32,), torch, None, dev)
-    B = int(num_draft.numel())
+    B, (slots, width), ts = num_draft.numel(), page_table.shape, page_table.stride()
     _need(seqs, "seqs", (torch.int32,), torch, B, dev)
-    _need(seq_len, "seq_len", (torch.int32,), torch, int(page_table.shape[0]), dev)
-    if page_table.dtype != torch.int32 or page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    _need(seq_len, "seq_len", (torch.int32,), torch, slots, dev)
+    if page_table.dtype != torch.int32 or page_table.device != dev or (width > 1 and ts[1] != 1):
         raise ValueError("page_table must be int32 on q's device with unit column stride")
-    if seqs is None and B > page_table.shape[0]:
-        raise ValueError(f"{B} sequences, but page_table has {page_table.shape[0]} rows")
+    if seqs is None and B > slots:
+        raise ValueError(f"{B} sequences, but page_table has {slots} rows")
     a = _lib.SpecVerifyAttentionArgs(
-        B, N, H, KV, D, _cache_dtype(q, "q", torch), P, _int32(window, "window"), pages, page_table.shape[0], page_table.shape[1],
-        page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1],
-        q.data_ptr(), q.stride(0) if N > 1 else 0, q.stride(1) if H > 1 else 0,
-        k_pages.data_ptr(), *_page_strides(k_pages), v_pages.data_ptr(), *_page_strides(v_pages),
+        B, N, H, KV, D, _cache_dtype(q, "q", torch), P, _int32(window, "window"), pages, slots, width,
+        ts[0] if slots > 1 else width,
+        # strides of dimensions of size 1 say nothing
+        q.data_ptr(), qs[0] if N > 1 else 0, qs[1] if H > 1 else 0,
+        k_pages.data_ptr(), ks[0] if pages > 1 else 0, ks[1] if KV > 1 else 0, ks[2],
+        v_pages.data_ptr(), vs[0] if pages > 1 else 0, vs[1] if KV > 1 else 0, vs[2],
         page_table.data_ptr(), seq_len.data_ptr(), _ptr(seqs), num_draft.data_ptr(),
         D ** -0.5 if scale is None else float(scale))
     nbytes = lib.spec_verify_attention_workspace(ctypes.byref(a))
@@ -562,11 +564,6 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
         _check(lib.spec_verify_paged_attention(ctypes.byref(a), _queue(dev)))
     return _for_caller(out, dev, stream)
-
-
-def _page_strides(t):
-    """Page, head and token strides; those of a dimension of size 1 say nothing."""
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
 
 
 class PagedCache:
