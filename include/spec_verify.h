@@ -507,7 +507,7 @@ typedef struct spec_verify_attention_args {
   const int32_t* seq_len;
   const int32_t* seqs;
   const int32_t* num_draft;
-  double scale;                /* finite; head_dim^-0.5 for the usual attention */
+  double scale;                /* |scale| < 2.3e38; head_dim^-0.5 for the usual attention */
   void* out;
   float* lse;
   int32_t* status;

@@ -297,8 +297,9 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
     set_err("%s: page_table_stride %lld < max_pages %d", who, (long long)a->page_table_stride, a->max_pages);
     return SV_ERR_INVALID;
   }
-  if (!isfinite(a->scale)) {
-    set_err("%s: scale is not finite", who);
+  const float scale_log2 = (float)(a->scale * 1.4426950408889634);
+  if (!isfinite(scale_log2)) {
+    set_err("%s: scale %g (times log2 e) is not finite in 32 bits", who, a->scale);
     return SV_ERR_INVALID;
   }
   const int64_t need = spec_verify_attention_workspace(a);
@@ -320,7 +321,7 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
   p.slots = a->slots;
   p.max_len = a->max_pages * a->page_size;
   p.num_pages = a->num_pages;
-  p.scale_log2 = (float)(a->scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.q = a->q;
   p.q_row = a->q_row_stride;
   p.q_head = a->q_head_stride;

@@ -259,3 +259,18 @@ def test_cache_rejects_bad_arguments():
     assert lib.spec_verify_cache_write(r, 0, 0, None, 0, 0, None, 0, 0, None, None) == OK
     assert lib.spec_verify_cache_reserve(r, 0, None, None, 0, None, None, None, None) == OK
     assert lib.spec_verify_cache_fork(r, 0, None, None, None, None) == OK
+
+
+@pytest.mark.parametrize("scale", [1e39, -1e39, 3e38])
+def test_paged_attention_rejects_a_scale_outside_32_bits(scale):
+    """The scores are float32: a scale (times log2 e) that is infinite there
+    would turn a score of 0 into NaN."""
+    _lib, lib = _lib_loaded()
+    a = _lib.SpecVerifyAttentionArgs(
+        batch=2, total_rows=6, heads=8, kv_heads=2, head_dim=128, dtype=_lib.SV_BF16, page_size=16, num_pages=10, slots=2,
+        max_pages=4, page_table_stride=4, q=0x1000, q_row_stride=1024, q_head_stride=128, k=0x1000, k_page_stride=4096,
+        k_head_stride=2048, k_token_stride=128, v=0x1000, v_page_stride=4096, v_head_stride=2048, v_token_stride=128,
+        page_table=0x1000, seq_len=0x1000, num_draft=0x1000, scale=scale, out=0x1000, workspace=0x1000,
+        workspace_bytes=1 << 30)
+    assert lib.spec_verify_paged_attention(ctypes.byref(a), None) == _lib.SV_ERR_INVALID
+    assert b"scale" in lib.spec_verify_last_error()
