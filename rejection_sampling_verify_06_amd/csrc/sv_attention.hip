@@ -24,7 +24,12 @@
 //
 // P is split into two halves of the 16-bit type, p = hi + lo, each its own
 // product: rounding p once would put an error of the output's own rounding
-// on top of it, and the second product hides behind the cache's reads.
+// on top of it, and the second product hides behind the cache's reads.  A
+// bfloat16 pair holds a weight to 2^-16, a float16 pair to 2^-22 and no finer
+// than its smallest step of 2^-24: there m is the maximum less 14, so that the
+// weights reach up to 2^14 and the step is 2^-38 of the largest.  (Three
+// bfloat16 hold all 24 bits: 32 sequences of 1024 to 8192 tokens, 8 to 24 rows
+// of 128, 134 -> 140 us, for the last bit of 1 in 1000 outputs.)
 //
 // Work is cut into units of 128 keys of one (sequence, row tile, key head)
 // and dealt out in equal contiguous ranges, one per block, so that neither a
@@ -108,6 +113,14 @@ template <bool BF>
 __device__ __forceinline__ float hi16(uint32_t w) {
   if constexpr (BF) return __uint_as_float(w & 0xFFFF0000u);
   else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+}
+
+// What the weights of a row with maximum m are taken against.  Lowered by 14
+// for float16; above 2^24, where 14 less may not be a float32, scores are known
+// to no better than 1, and the weights stay at or below 1.
+template <bool BF>
+__device__ __forceinline__ float reference(float m) {
+  return !BF && fabsf(m) < 0x1p24f ? m - 14.f : m;
 }
 
 // the low half is an infinity or NaN
@@ -214,7 +227,7 @@ __device__ __forceinline__ uint32_t range_of(uint32_t u, uint32_t W, uint32_t U)
   return (uint32_t)((((uint64_t)u + 1) * W - 1) / U);
 }
 
-// a part in the workspace: TM rows of O, then TM maxima, then TM sums
+// a part in the workspace: TM rows of O, then what their weights were taken against, then TM sums
 __device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, int TM, int D) {
   return P.parts + ((int64_t)w * 2 + slot) * TM * (D + 2);
 }
@@ -431,13 +444,13 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : D * MT <= 256 &
         for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
         if (__ballot(top > mx[m])) {             // a new maximum in some row: rescale
           const float nm = fmaxf(mx[m], column_max(top));
-          const float f = mx[m] == nm ? 1.f : at_exp2(mx[m] - nm);
+          const float f = mx[m] == nm ? 1.f : at_exp2(reference<BF>(mx[m]) - reference<BF>(nm));
           mx[m] = nm;
           ls[m] *= f;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) o[m][j] *= f;
         }
-        const float ref = mx[m] == -INFINITY ? 0.f : mx[m];
+        const float ref = mx[m] == -INFINITY ? 0.f : reference<BF>(mx[m]);
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -498,6 +511,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : D * MT <= 256 &
     // and a thread adds up 4 neighbours of a row.
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      mx[m] = reference<BF>(mx[m]);              // from here on all parts are compared by what they were taken against
       ls[m] = column_sum(ls[m]);
       if (bad) ls[m] = __builtin_nanf("");
       if (g == 0) {
