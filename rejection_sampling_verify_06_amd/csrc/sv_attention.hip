@@ -451,12 +451,13 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : D * MT <= 256 &
           for (int j = 0; j < NJ; ++j) o[m][j] *= f;
         }
         const float ref = mx[m] == -INFINITY ? 0.f : reference<BF>(mx[m]);
-        float p[8];
+        float p[8], eight;                       // summed up first: next to ls the weights of a long tail are below half a step
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           p[e] = at_exp2(s[e] - ref);
-          ls[m] += p[e];
+          eight = e ? eight + p[e] : p[e];
         }
+        ls[m] += eight;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ph[m][i] = pack16<BF>(p[2 * i], p[2 * i + 1]);

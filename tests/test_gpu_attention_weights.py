@@ -127,3 +127,28 @@ def test_scores_of_any_size(sv, dtype, size):
             assert ((got - want).abs() <= U[dtype] * want.abs() + 2.0 ** -15).all(), (b, h)
             top = (x * sign).max().item() * scale
             assert abs(o["lse"][b, h].item() - top) <= abs(top) * 2.0 ** -22 + math.log(best.sum().item()) + 1e-3
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_the_sum_over_a_long_row(sv, dtype):
+    """131072 keys 17.4 nats below a sink that their block reads first: one at
+    a time each is less than half a step of the sum next to it.
+
+    The sink's lane holds 1/16 of the keys and adds them up in eights, L / 128
+    additions to a sum near the sink's weight, each off by half a step, 2^-24
+    of it.  The rest, 2^-17, is as in the test above."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    KV, B, D, P, L, gap = 8, 32, 128, 1024, 131073, 17.375
+    per = -(-L // P)
+    k = torch.zeros(per, KV, P, D, dtype=dtype, device="cuda")
+    v = torch.full_like(k, 64.0)
+    k[0, :, 0, 0] = gap
+    v[0, :, 0] = 0.0
+    table = torch.arange(per, **i32).repeat(B, 1)           # every sequence the same pages
+    q = torch.zeros(B, KV, D, dtype=dtype, device="cuda")
+    q[:, :, 0] = 1.0
+    o = sv.paged_attention(q, k, v, table, torch.full((B,), L, **i32), torch.zeros(B, **i32), scale=1.0, want_lse=True)
+    tail = (L - 1) * math.exp(-gap)
+    assert (o["lse"].cpu().double() - (gap + math.log1p(tail))).abs().max() < 2.0 ** -17 + L / 128 * 2.0 ** -24
+    want = 64 * tail / (1 + tail)
+    assert (o["out"].cpu().double() - want).abs().max() <= want * (U[dtype] * 17 / 16 + 2.0 ** -12)
