@@ -28,8 +28,9 @@
 // bfloat16 pair holds a weight to 2^-16, a float16 pair to 2^-22 and no finer
 // than its smallest step of 2^-24: there m is the maximum less 14, so that the
 // weights reach up to 2^14 and the step is 2^-38 of the largest.  (Three
-// bfloat16 hold all 24 bits: 32 sequences of 1024 to 8192 tokens, 8 to 24 rows
-// of 128, 134 -> 140 us, for the last bit of 1 in 1000 outputs.)
+// bfloat16 hold all 24 bits, for the last bit of 1 in 1000 outputs: 8 to 24 rows
+// of 128 133.5 -> 134.5 us, 16 and 36 rows of two long sequences 87 -> 89.5, 64
+// rows of 64 106 -> 111.)
 //
 // Work is cut into units of 128 keys of one (sequence, row tile, key head)
 // and dealt out in equal contiguous ranges, one per block, so that neither a
@@ -464,6 +465,9 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : D * MT <= 256 &
           pl[m][i] = pack16<BF>(p[2 * i] - lo16<BF>(ph[m][i]), p[2 * i + 1] - hi16<BF>(ph[m][i]));
         }
       }
+      // The schedule that the compiler takes without this holds up to 16
+      // registers more: two float16 tiles of 128 spilled two (134 us, 133 with it).
+      __builtin_amdgcn_sched_barrier(0);
       if (strange) {
         // A value that is not finite next to a key that some row does not
         // see.  Where it stands, a third product with ones in such places
