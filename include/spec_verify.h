@@ -478,7 +478,7 @@ int64_t spec_verify_logprobs_args_size(void);
  * holds visible tokens is outside the pool) gets NaN, and no such page is read.
  * Enqueues two kernels on `hip_stream`, which belongs to the calling
  * thread's current device; allocates nothing, does not synchronise.
- * SV_ERR_INVALID: nothing was enqueued.  batch == 0 is a no-op. */
+ * SV_ERR_INVALID: nothing was enqueued.  batch == 0 (without rows) is a no-op. */
 typedef struct spec_verify_attention_args {
   int32_t batch;
   int32_t total_rows;

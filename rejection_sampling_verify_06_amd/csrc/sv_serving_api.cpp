@@ -74,6 +74,10 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
     set_err("%s: batch %d outside 0..4096, or total_rows %d outside batch..524288", who, a->batch, a->total_rows);
     return false;
   }
+  if (a->batch == 0 && a->total_rows != 0) {
+    set_err("%s: total_rows %d belong to no sequence", who, a->total_rows);
+    return false;
+  }
   if (a->window < 0 || a->num_pages < 1 || a->num_pages > INT32_MAX || a->slots < 1 || a->max_pages < 1 ||
       (int64_t)a->max_pages * a->page_size > INT32_MAX - 4096) {
     set_err("%s: window %d < 0, or num_pages %lld, slots %d, max_pages %d outside their range", who, a->window,

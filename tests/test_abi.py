@@ -274,3 +274,14 @@ def test_paged_attention_rejects_a_scale_outside_32_bits(scale):
         workspace_bytes=1 << 30)
     assert lib.spec_verify_paged_attention(ctypes.byref(a), None) == _lib.SV_ERR_INVALID
     assert b"scale" in lib.spec_verify_last_error()
+
+
+def test_paged_attention_rejects_rows_without_a_sequence():
+    """No sequences, but rows: the outputs would be left as they were."""
+    _lib, lib = _lib_loaded()
+    good = dict(batch=0, total_rows=0, heads=8, kv_heads=2, head_dim=128, dtype=_lib.SV_BF16, page_size=16, num_pages=10, slots=2,
+                max_pages=4)
+    for rows, want in ((0, _lib.SV_OK), (1, _lib.SV_ERR_INVALID), (3, _lib.SV_ERR_INVALID)):
+        a = _lib.SpecVerifyAttentionArgs(**{**good, "total_rows": rows})
+        assert lib.spec_verify_paged_attention(ctypes.byref(a), None) == want
+        assert (lib.spec_verify_attention_workspace(ctypes.byref(a)) < 0) == (want != _lib.SV_OK)

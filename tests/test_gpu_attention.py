@@ -337,3 +337,9 @@ def test_weights_far_below_the_largest(sv, dtype):
     want = (small - 1) / (small + 1)
     assert (o["out"].double().cpu() - want).abs().max() < abs(want) * RTOL[dtype] + 2.0 ** -12
     assert abs(o["lse"][0, 0].item() - (10.5 + np.log1p(small))) < 1e-4
+
+
+def test_rows_without_a_sequence(sv):
+    k, v, table, seq_len = su.make_pages([10], 16, 1, 64, torch.bfloat16, 16)
+    with pytest.raises(sv.VerifyError):
+        sv.paged_attention(_q(3, 4, 64, torch.bfloat16, 1), k, v, table, seq_len, _i32([]))
