@@ -459,6 +459,9 @@ int64_t spec_verify_logprobs_args_size(void);
  *   seqs           [batch] int32: sequence b is row seqs[b] of page_table and
  *                  seq_len (a slot may be named more than once); NULL: row b
  *   num_draft      [batch] int32, sum of (num_draft + 1) = total_rows
+ *   start          [batch] int32 or NULL: what spec_verify_cache_reserve gave
+ *                  for the n new tokens; a sequence that it refused (-1), or
+ *                  whose seq_len is not start + n, has none and is refused
  *   out            [total_rows][heads][head_dim], contiguous
  *   lse            [total_rows][heads] float or NULL
  *   status         [batch] int32 or NULL
@@ -474,8 +477,9 @@ int64_t spec_verify_logprobs_args_size(void);
  * What only the device can see: num_draft that does not add up sets
  * SV_ST_BAD_LAYOUT for every sequence and every output is NaN; a sequence
  * with SV_ST_BAD_SEQ (slot outside 0..slots-1), SV_ST_BAD_LENGTH (seq_len
- * negative or above max_pages * page_size) or SV_ST_BAD_PAGE (a page that
- * holds visible tokens is outside the pool) gets NaN, and no such page is read.
+ * negative, above max_pages * page_size or not what start says) or
+ * SV_ST_BAD_PAGE (a page that holds visible tokens is outside the pool) gets
+ * NaN, and no such page is read.
  * Enqueues two kernels on `hip_stream`, which belongs to the calling
  * thread's current device; allocates nothing, does not synchronise.
  * SV_ERR_INVALID: nothing was enqueued.  batch == 0 (without rows) is a no-op. */
@@ -513,6 +517,7 @@ typedef struct spec_verify_attention_args {
   int32_t* status;
   void* workspace;
   int64_t workspace_bytes;
+  const int32_t* start;
 } spec_verify_attention_args;
 int spec_verify_paged_attention(const spec_verify_attention_args* args, void* hip_stream);
 
@@ -564,7 +569,12 @@ int64_t spec_verify_attention_args_size(void);
  * spec_verify_cache_commit: entry b, which reserved num_draft[b] + 1 tokens,
  * keeps accepted_len[b] + 1 of them (its last emitted token and the accepted
  * drafts; the token the verify call drew is the next round's first), or none
- * for accepted_len[b] = -1 (not verified).
+ * for accepted_len[b] = -1 (not verified).  It takes the entry's word that
+ * these tokens are there: an entry whose reserve was refused has grown by
+ * none, and would lose older ones.
+ * spec_verify_cache_commit_reserved: the same with reserve's start, [batch];
+ * an entry that reserve refused (-1), or whose length is not start[b] +
+ * num_draft[b] + 1, keeps what it has: SV_ST_BAD_LENGTH.
  * spec_verify_cache_fork: slot children[b], of length 0, gets the length and
  * pages of slot parents[b] (which may be named more than once), as they were
  * before the call.  SV_ST_BAD_LENGTH: the child is not empty.
@@ -603,6 +613,9 @@ int spec_verify_cache_truncate(const spec_verify_cache* cache, int32_t batch, co
                                int32_t* status, void* hip_stream);
 int spec_verify_cache_commit(const spec_verify_cache* cache, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
                              const int32_t* accepted_len, int32_t* status, void* hip_stream);
+int spec_verify_cache_commit_reserved(const spec_verify_cache* cache, int32_t batch, const int32_t* seqs,
+                                      const int32_t* num_draft, const int32_t* accepted_len, const int32_t* start,
+                                      int32_t* status, void* hip_stream);
 int spec_verify_cache_fork(const spec_verify_cache* cache, int32_t batch, const int32_t* parents, const int32_t* children,
                            int32_t* status, void* hip_stream);
 int spec_verify_cache_compact(const spec_verify_cache* cache, int32_t* live, void* hip_stream);

@@ -502,7 +502,7 @@ def _cache_dtype(t, name, torch):
 
 
 def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs=None, scale: Optional[float] = None,
-                    window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None) -> dict:
+                    window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None, start=None) -> dict:
     """Attention of a round's new tokens over a paged key-value cache
     (spec_verify_paged_attention).
 
@@ -514,7 +514,9 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     [slots]: the cached tokens, the new ones last.  Sequence b uses slot
     ``seqs[b]`` (int32), or b.  Row i sees positions up to seq_len -
     num_draft - 1 + i, with ``window`` > 0 only the last ``window`` of them.
-    ``scale`` defaults to head_dim ** -0.5.  Returns ``out`` like ``q``
+    ``scale`` defaults to head_dim ** -0.5.  ``start`` (int32 [batch], from
+    ``PagedCache.reserve``): a sequence whose reserve was refused has no new
+    tokens, and gets NaN and a status.  Returns ``out`` like ``q``
     (contiguous), ``lse`` (float32 [total_rows, heads]) and ``status`` (int32
     [batch]); what was not asked for is None."""
     import torch
@@ -536,6 +538,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     _need(num_draft, "num_draft", (torch.int32,), torch, None, dev)
     B, (slots, width), ts = num_draft.numel(), page_table.shape, page_table.stride()
     _need(seqs, "seqs", (torch.int32,), torch, B, dev)
+    _need(start, "start", (torch.int32,), torch, B, dev)
     _need(seq_len, "seq_len", (torch.int32,), torch, slots, dev)
     if page_table.dtype != torch.int32 or page_table.device != dev or (width > 1 and ts[1] != 1):
         raise ValueError("page_table must be int32 on q's device with unit column stride")
@@ -549,11 +552,11 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         k_pages.data_ptr(), ks[0] if pages > 1 else 0, ks[1] if KV > 1 else 0, ks[2],
         v_pages.data_ptr(), vs[0] if pages > 1 else 0, vs[1] if KV > 1 else 0, vs[2],
         page_table.data_ptr(), seq_len.data_ptr(), _ptr(seqs), num_draft.data_ptr(),
-        D ** -0.5 if scale is None else float(scale))
+        D ** -0.5 if scale is None else float(scale), start=_ptr(start))
     nbytes = lib.spec_verify_attention_workspace(ctypes.byref(a))
     if nbytes < 0:
         _check(int(nbytes))
-    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs):
+    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start):
         out = {
             "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
             "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,
@@ -576,14 +579,17 @@ class PagedCache:
 
         r = cache.reserve(seqs, num_draft + 1, total)      # places for the new tokens
         cache.write(layer, k_new, v_new, r["slots"])       # every layer, before it attends
-        o = cache.attend(layer, q, num_draft, seqs)
+        o = cache.attend(layer, q, num_draft, seqs, start=r["start"])
         ...                                                # logits, Verifier.run
-        cache.commit(seqs, num_draft, out["accepted_len"]) # the rejected tokens leave
+        cache.commit(seqs, num_draft, out["accepted_len"], start=r["start"])   # the rejected tokens leave
 
     ``seqs`` (int32 [batch], distinct slots, or None for 0 .. batch - 1) and
     the counts are device tensors; nothing here waits for the device.  The
     calls return a status per entry (0, or SV_ST_* bits of why it was refused
-    and changed nothing).  Calls on one cache must be ordered on one stream."""
+    and changed nothing).  With ``start`` a sequence that could not be reserved
+    for sits its round out: its rows of ``o`` are NaN, so that a verify call
+    over their logits refuses it, and ``commit`` leaves it as it was.  Calls on
+    one cache must be ordered on one stream."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
                  max_pages: int, dtype=None, device=None):
@@ -670,16 +676,23 @@ class PagedCache:
             raise ValueError(f"layer {layer} outside 0..{self.layers - 1}")
         return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, num_draft, seqs=seqs, **kw)
 
-    def commit(self, seqs, num_draft, accepted_len, stream=None):
+    def commit(self, seqs, num_draft, accepted_len, stream=None, *, start=None):
         """Keeps ``accepted_len`` + 1 of the ``num_draft`` + 1 tokens each
-        sequence reserved for its round (none where it is -1: not verified)."""
+        sequence reserved for its round (none where it is -1: not verified).
+        With ``start`` (int32 [batch], from ``reserve``) a sequence whose
+        reserve was refused keeps what it has; without, every one of them has
+        to have been carried out."""
         torch = self._torch
         B = self._entries(seqs, num_draft, "num_draft")
         _need(accepted_len, "accepted_len", (torch.int32,), torch, B, self.device)
-        with self._on_stream(stream, seqs, num_draft, accepted_len):
+        _need(start, "start", (torch.int32,), torch, B, self.device)
+        with self._on_stream(stream, seqs, num_draft, accepted_len, start):
             status = torch.empty(B, dtype=torch.int32, device=self.device)
-            _check(self._lib.spec_verify_cache_commit(self._ref, B, _ptr(seqs), num_draft.data_ptr(), accepted_len.data_ptr(),
-                                                      _ptr(status), _queue(self.device)))
+            a = (self._ref, B, _ptr(seqs), num_draft.data_ptr(), accepted_len.data_ptr())
+            if start is None:
+                _check(self._lib.spec_verify_cache_commit(*a, _ptr(status), _queue(self.device)))
+            else:
+                _check(self._lib.spec_verify_cache_commit_reserved(*a, _ptr(start), _ptr(status), _queue(self.device)))
         return _for_caller(status, self.device, stream)
 
     def truncate(self, seqs, drop, stream=None):

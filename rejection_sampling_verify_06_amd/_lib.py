@@ -54,8 +54,9 @@ EXPORTED = (
     "spec_verify_adapt_args_size", "spec_verify_run_noalloc",
     "spec_verify_token_logprobs", "spec_verify_logprobs_workspace", "spec_verify_logprobs_args_size",
     "spec_verify_paged_attention", "spec_verify_attention_workspace", "spec_verify_attention_args_size",
-    "spec_verify_cache_reserve", "spec_verify_cache_truncate", "spec_verify_cache_commit", "spec_verify_cache_fork",
-    "spec_verify_cache_compact", "spec_verify_cache_write", "spec_verify_cache_workspace", "spec_verify_cache_size",
+    "spec_verify_cache_reserve", "spec_verify_cache_truncate", "spec_verify_cache_commit",
+    "spec_verify_cache_commit_reserved", "spec_verify_cache_fork", "spec_verify_cache_compact", "spec_verify_cache_write",
+    "spec_verify_cache_workspace", "spec_verify_cache_size",
 )
 SV_CACHE_MAX_SLOTS = 4096
 SV_LOGPROBS_MAX_TOP = 64
@@ -178,6 +179,7 @@ class SpecVerifyAttentionArgs(ctypes.Structure):
         ("status", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_int64),
+        ("start", ctypes.c_void_p),
     ]
 
 
@@ -266,7 +268,7 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_attention_args_size.restype = ctypes.c_int64
     C, i32, i64 = ctypes.POINTER(SpecVerifyCache), ctypes.c_int32, ctypes.c_int64
     for name, types in (("reserve", [C, i32, P, P, i64, P, P, P, P]), ("truncate", [C, i32, P, P, P, P]),
-                        ("commit", [C, i32, P, P, P, P, P]), ("fork", [C, i32, P, P, P, P]), ("compact", [C, P, P]),
+                        ("commit", [C, i32, P, P, P, P, P]), ("commit_reserved", [C, i32, P, P, P, P, P, P]), ("fork", [C, i32, P, P, P, P]), ("compact", [C, P, P]),
                         ("write", [C, i32, i64, P, i64, i64, P, i64, i64, P, P])):
         f = getattr(lib, "spec_verify_cache_" + name)
         f.argtypes, f.restype = types, ctypes.c_int

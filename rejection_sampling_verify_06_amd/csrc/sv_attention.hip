@@ -156,11 +156,16 @@ struct Extent {
   int nblk;       // blocks, at least 1 (an empty sequence still writes its rows)
 };
 
+// the n new tokens lie where they were reserved
+__device__ __forceinline__ bool in_place(const AttnParams& P, int b, int n, int len) {
+  return !P.start || (P.start[b] >= 0 && P.start[b] == len - n);
+}
+
 __device__ __forceinline__ Extent seq_extent(const AttnParams& P, int b, int n) {
   Extent x;
   x.slot = P.seqs ? P.seqs[b] : b;
   const int len = P.seq_len[(unsigned)x.slot < (unsigned)P.slots ? x.slot : 0];
-  const bool ok = (unsigned)x.slot < (unsigned)P.slots && len >= 0 && len <= P.max_len;
+  const bool ok = (unsigned)x.slot < (unsigned)P.slots && len >= 0 && len <= P.max_len && in_place(P, b, n, len);
   x.slot = ok ? x.slot : -1;
   x.len = ok ? len : 0;
   x.first = P.window > 0 ? max(0, x.len - n + 1 - P.window) : 0;
@@ -630,7 +635,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
         s = SV_ST_BAD_SEQ;
       } else {
         const int len = P.seq_len[slot];
-        if (len < 0 || len > P.max_len) {
+        if (len < 0 || len > P.max_len || !in_place(P, b, n, len)) {
           s = SV_ST_BAD_LENGTH;
         } else {
           const Extent x = seq_extent(P, b, n);

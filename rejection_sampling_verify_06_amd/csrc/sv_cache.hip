@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(kCaThreads) k_cache_truncate(CacheParams P) {
         } else if (P.num_draft) {
           const int K = P.num_draft[b], A = P.accepted[b];
           ok = ok && K >= 0 && A >= -1 && A <= K;
+          // what a refused reserve did not add is not there to be dropped
+          if (P.reserved) ok = ok && P.reserved[b] >= 0 && (int64_t)P.reserved[b] + K + 1 == L;
           d = (int64_t)K - A;                    // A = -1, not verified: all K + 1 new tokens
         }
         ok = ok && d >= 0 && d <= L;

@@ -247,6 +247,7 @@ struct AttnParams {
   const int32_t* seq_len;
   const int32_t* num_draft;
   const int32_t* seqs;              // or NULL
+  const int32_t* start;             // or NULL: the lengths in front of the new tokens, as reserve gave them
   void* out;
   float* lse;                       // or NULL
   int32_t* status;                  // or NULL
@@ -282,6 +283,7 @@ struct CacheParams {
   const int32_t* drop;              // truncate: these, or what num_draft / accepted say, or all
   const int32_t* num_draft;
   const int32_t* accepted;
+  const int32_t* reserved;          // commit, or NULL: the lengths in front of the new tokens, as reserve gave them
   const int32_t* children;          // fork
   int32_t* live;                    // compact, or NULL
   int32_t* status;                  // or NULL

@@ -342,6 +342,7 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
   p.seq_len = a->seq_len;
   p.num_draft = a->num_draft;
   p.seqs = a->seqs;
+  p.start = a->start;
   p.out = a->out;
   p.lse = a->lse;
   p.status = a->status;
@@ -393,9 +394,8 @@ int spec_verify_cache_truncate(const spec_verify_cache* c, int32_t batch, const 
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
 }
 
-int spec_verify_cache_commit(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
-                             const int32_t* accepted_len, int32_t* status, void* hip_stream) {
-  const char* who = "spec_verify_cache_commit";
+static int cache_commit(const char* who, const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
+                        const int32_t* accepted_len, const int32_t* start, int32_t* status, void* hip_stream) {
   sv::CacheParams p;
   if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
   if (batch == 0) return SV_OK;
@@ -406,9 +406,25 @@ int spec_verify_cache_commit(const spec_verify_cache* c, int32_t batch, const in
   p.seqs = seqs;
   p.num_draft = num_draft;
   p.accepted = accepted_len;
+  p.reserved = start;
   p.status = status;
   hipError_t e = sv::launch_cache_truncate(p, (hipStream_t)hip_stream);
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_commit(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
+                             const int32_t* accepted_len, int32_t* status, void* hip_stream) {
+  return cache_commit("spec_verify_cache_commit", c, batch, seqs, num_draft, accepted_len, nullptr, status, hip_stream);
+}
+
+int spec_verify_cache_commit_reserved(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_draft,
+                                      const int32_t* accepted_len, const int32_t* start, int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_commit_reserved";
+  if (batch != 0 && !start) {
+    set_err("%s: start is required", who);
+    return SV_ERR_INVALID;
+  }
+  return cache_commit(who, c, batch, seqs, num_draft, accepted_len, start, status, hip_stream);
 }
 
 int spec_verify_cache_fork(const spec_verify_cache* c, int32_t batch, const int32_t* parents, const int32_t* children,

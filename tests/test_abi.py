@@ -285,3 +285,16 @@ def test_paged_attention_rejects_rows_without_a_sequence():
         a = _lib.SpecVerifyAttentionArgs(**{**good, "total_rows": rows})
         assert lib.spec_verify_paged_attention(ctypes.byref(a), None) == want
         assert (lib.spec_verify_attention_workspace(ctypes.byref(a)) < 0) == (want != _lib.SV_OK)
+
+
+def test_commit_reserved_rejects_bad_arguments():
+    _lib, lib = _lib_loaded()
+    good = dict(slots=4, max_pages=8, page_size=16, num_pages=20, layers=2, kv_heads=2, head_dim=64, page_table=0x1000,
+                seq_len=0x1000, refcount=0x1000, k=0x1000, v=0x1000, workspace=0x1000, workspace_bytes=1 << 20)
+    P, call, r = 0x1000, lib.spec_verify_cache_commit_reserved, ctypes.byref(_lib.SpecVerifyCache(**good))
+    for a in ((None, 2, P, P, P, P, P), (r, -1, P, P, P, P, P), (r, 5, P, P, P, P, P), (r, 2, P, None, P, P, P),
+              (r, 2, P, P, None, P, P), (r, 2, P, P, P, None, P),
+              (ctypes.byref(_lib.SpecVerifyCache(**{**good, "workspace": None})), 2, P, P, P, P, P)):
+        assert call(*a, None) == _lib.SV_ERR_INVALID, a
+        assert b"spec_verify_cache_commit_reserved" in lib.spec_verify_last_error()
+    assert call(r, 0, None, None, None, None, None, None) == _lib.SV_OK

@@ -434,3 +434,97 @@ def test_memory_of_another_stream(sv):
     m.write(0, keep, keep, slots)
     m.commit([0, 1], [1, 0], [0, 0])
     m.check(c)
+
+
+def test_a_refused_reserve_sits_the_round_out(sv):
+    """Sequences that could not be reserved for (the pool is full, the table row too short, a slot named twice): with
+    reserve's `start` the round's other calls leave them as they were, whatever the verify call says of them."""
+    dtype, V = torch.bfloat16, 50
+    c, m = _cache(sv, pages=8, H=2, D=64, slots=6, width=3, layers=1)
+    _write(c, m, 0, _reserve(c, m, None, [40, 33, 16, 16]), 1)
+    seqs, K = [2, 0, 1, 0, 3, 5], [3, 1, 9, 0, 0, 0]
+    n = [k + 1 for k in K]
+    total = sum(n)
+    q = torch.randn(total, 4, 64, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    # no page is left for slots 2, 3 and 5; slot 0 is named twice
+    r = c.reserve(_i32(seqs), _i32(n), total)
+    want = m.reserve(seqs, n, total)
+    assert r["status"].tolist() == want[2] == [2048, 0, 0, 256, 2048, 2048]
+    assert r["start"].tolist() == want[0] == [-1, 40, 33, -1, -1, -1]
+    _write(c, m, 0, (r["slots"], want[1]), 3)
+    m.check(c)
+    nd = _i32(K)
+    o = c.attend(0, q, nd, _i32(seqs), start=r["start"], want_lse=True)
+    assert o["status"].tolist() == [512, 0, 0, 512, 512, 512]
+    plain = c.attend(0, q, nd, _i32(seqs), want_lse=True)
+    at = 0
+    for b, rows in enumerate(n):
+        part = slice(at, at + rows)
+        if want[0][b] < 0:
+            assert torch.isnan(o["out"][part]).all() and torch.isnan(o["lse"][part]).all(), b
+        else:
+            assert torch.equal(o["out"][part], plain["out"][part]) and torch.equal(o["lse"][part], plain["lse"][part]), b
+        at += rows
+    logits = (o["out"].view(total, -1).float() @ torch.randn(256, V, device="cuda")).to(dtype)
+    ver = sv.Verifier(max_batch=8, max_k=16, max_vocab=V)
+    mode = torch.full((len(seqs),), sv.SV_ONEHOT, dtype=torch.uint8, device="cuda")
+    out = ver.run(logits, None, torch.zeros(sum(K), dtype=torch.int32, device="cuda"), nd, mode=mode, seed=1)
+    A = out["accepted_len"].tolist()
+    assert [a for a, s in zip(A, want[0]) if s < 0] == [-1] * 4 and min(A[1], A[2]) >= 0
+    lp = sv.token_logprobs(logits, out["emitted"])
+    assert (lp["logprob"][:4] == 0).all() and not lp["status"][:4].any()
+    # whatever is said to be accepted of a refused entry
+    for a in ([-1, 0, 0], [0, 0, 0], [3, 0, 0]):
+        assert c.commit(_i32([2, 3, 5]), _i32([3, 0, 0]), _i32(a), start=_i32([-1, -1, -1])).tolist() == [512] * 3
+        m.check(c)
+    st = c.commit(_i32(seqs), nd, out["accepted_len"], start=r["start"])
+    assert st.tolist() == [512, 0, 0, 256, 512, 512]
+    m.commit([0, 1], [1, 9], [A[1], A[2]])
+    m.check(c)
+    # a start that is not where the tokens are: the round was committed already, or another one's start
+    for start in (m.len[0], m.len[0] - 2, -1, 2147483647, -2147483648):
+        assert c.commit(_i32([0]), _i32([0]), _i32([-1]), start=_i32([start])).tolist() == [512]
+        m.check(c)
+        assert c.attend(0, q[:1], _i32([0]), _i32([3]), start=_i32([start]))["status"].tolist() == [512]
+    assert c.attend(0, q[:1], _i32([0]), _i32([3]), start=_i32([15]))["status"].tolist() == [0]
+    ver.close()
+
+
+def test_a_captured_round_that_fills_the_pool(sv):
+    """The whole round in one graph: it is carried out until the pool is full, and then changes nothing."""
+    c, m = _cache(sv, pages=6, H=2, D=64, slots=2, width=5, layers=1)
+    _write(c, m, 0, _reserve(c, m, None, [30, 3]), 0)
+    K = [7, 5]
+    nd, acc, new, total = _i32(K), _i32([7, 4]), _i32([8, 6]), 14
+    q = torch.randn(total, 4, 64, device="cuda").to(torch.bfloat16)
+    x = torch.randn(total, 2, 64, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16)
+    xd = x.cuda()
+
+    def step():
+        r = c.reserve(None, new, total)
+        c.write(0, xd, xd, r["slots"])
+        o = c.attend(0, q, nd, start=r["start"])
+        return r, o, c.commit(None, nd, acc, start=r["start"])
+    state = [t.clone() for t in (c.page_table, c.seq_len, c.refcount, c.k, c.v)]
+    step()
+    torch.cuda.synchronize()
+    for t, was in zip((c.page_table, c.seq_len, c.refcount, c.k, c.v), state):
+        t.copy_(was)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, o, st = step()
+    refused = 0
+    for i in range(12):
+        graph.replay()
+        torch.cuda.synchronize()
+        start, slots, status = m.reserve([0, 1], [8, 6], total)
+        m.write(0, x, x, slots)
+        for s in (0, 1):
+            if start[s] >= 0:
+                m.truncate([s], [K[s] - [7, 4][s]])
+        refused += sum(a < 0 for a in start)
+        assert (r["start"].tolist(), r["slots"].tolist(), r["status"].tolist()) == (start, slots, status), i
+        assert o["status"].tolist() == st.tolist() == [512 if a < 0 else 0 for a in start], i
+        assert [bool(torch.isnan(o["out"][p]).all()) for p in (slice(0, 8), slice(8, 14))] == [a < 0 for a in start], i
+        m.check(c)
+    assert refused > 10
