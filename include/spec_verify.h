@@ -560,9 +560,12 @@ int64_t spec_verify_attention_args_size(void);
  * entry, nothing changes).  start[b] is its old length (-1: refused), slots
  * (int64 [total_new]) the place of each new token, page * page_size + offset
  * (-1: refused).  A partly filled last page that other sequences use too is
- * first copied to a page of its own, in every layer.  SV_ST_BAD_LENGTH: the
- * table row would be too short; SV_ST_CACHE_FULL: too few free pages (so are
- * the entries behind it that need any).
+ * first copied to a page of its own, in every layer.  Users and free pages are
+ * counted as they were before the call: where all users of such a page append
+ * in one call, each gets a copy, one page more than they need, and the old page
+ * is free afterwards.  SV_ST_BAD_LENGTH: the table row would be too short;
+ * SV_ST_CACHE_FULL: too few free pages (so are the entries behind it that need
+ * any).
  * spec_verify_cache_truncate: entry b loses its last drop[b] tokens, or all
  * of them with drop == NULL; pages that hold none of its tokens any more
  * lose it as a user.  SV_ST_BAD_LENGTH: drop outside 0 .. length.

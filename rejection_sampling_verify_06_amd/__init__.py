@@ -639,7 +639,10 @@ class PagedCache:
         """Grows each sequence by ``num_new`` tokens (int32 [batch], summing to
         ``total_new``).  Returns ``start`` (int32 [batch]: the old lengths),
         ``slots`` (int64 [total_new]: the new tokens' places, for ``write``)
-        and ``status``; -1 in the first two where an entry was refused."""
+        and ``status``; -1 in the first two where an entry was refused.  Users
+        of a partly filled last page that all append in one call each get a
+        copy of it, and it is free only afterwards: one page more than in two
+        calls."""
         torch = self._torch
         B, n = self._entries(seqs, num_new, "num_new"), int(total_new)
         with self._on_stream(stream, seqs, num_new):

@@ -528,3 +528,26 @@ def test_a_captured_round_that_fills_the_pool(sv):
         assert [bool(torch.isnan(o["out"][p]).all()) for p in (slice(0, 8), slice(8, 14))] == [a < 0 for a in start], i
         m.check(c)
     assert refused > 10
+
+
+def test_both_users_of_a_last_page_append(sv):
+    """In one call each asks for a copy, the second in vain with one free page; the old page is free afterwards.  In two
+    calls the second keeps the page."""
+    for both in (True, False):
+        c, m = _cache(sv, pages=3, slots=2, width=2)
+        _write(c, m, 0, _reserve(c, m, [0], [20]), 1)
+        c.fork(_i32([0]), _i32([1]))
+        m.fork([0], [1])
+        if both:
+            _reserve(c, m, [0, 1], [1, 1])
+            assert m.len == [21, 20] and m.ref == [2, 1, 1]
+        else:
+            _reserve(c, m, [0], [1])
+            _reserve(c, m, [1], [1])
+            assert m.len == [21, 21]
+    c, m = _cache(sv, pages=4, slots=2, width=2)
+    _reserve(c, m, [0], [20])
+    c.fork(_i32([0]), _i32([1]))
+    m.fork([0], [1])
+    _reserve(c, m, [0, 1], [1, 1])
+    assert m.len == [21, 21] and m.ref == [2, 0, 1, 1]
