@@ -472,7 +472,9 @@ int64_t spec_verify_logprobs_args_size(void);
  * and out 16-byte aligned with strides in multiples of 8 elements; batch <=
  * 4096, total_rows <= 524288, heads / kv_heads <= 256.
  * Scores, softmax and sums are float32, the softmax's weights enter the
- * second product as the sum of two 16-bit values, the result is rounded once.
+ * second product as the sum of two 16-bit values (held to 2^-16 of themselves
+ * for SV_BF16; to 2^-22, or 2^-39 of a row's largest, for SV_F16), the result
+ * is rounded once.
  * Repeated calls are bitwise identical.
  * What only the device can see: num_draft that does not add up sets
  * SV_ST_BAD_LAYOUT for every sequence and every output is NaN; a sequence

@@ -18,9 +18,11 @@
 // bound by HBM and run on the whole chip, from a list that stays on the device.
 //
 // Measured on one MI355X (rocprofv3): 32 sequences growing by up to 6 tokens,
-// reserve 7.5 us and its empty copy 2.3 us, commit 3.2 us, write 2.8 us a layer;
-// 8000 prompt tokens, reserve 13 us, write 14 us a layer (67 MB, 4.8 TB/s); 180
-// pages of 32 KB in 16 pools copied on write, 35 us (5.4 TB/s).
+// reserve 7.1 us and its empty copy 1.9 us, commit 3.2 us, write 2.9 us a layer;
+// 6905 prompt tokens, reserve 13 us, write 14 us a layer (57 MB, 4.0 TB/s); 180
+// pages of 32 KB in 16 pools copied on write, 36 us (189 MB, 5.2 TB/s; where
+// three branches copy the same page it is read behind the L2 about twice, 166
+// MB in all by the counters).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -98,7 +98,7 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
   // 134); 36 rows with 32, 48 114, 101.  One token of one sequence, 16 and 48 7
   // and 10 us.  More than 48 rows of 128 do not fit the registers (64 rows: 2
   // tiles twice 113 us, 3 tiles twice 182, 4 spilled 187), nor more than 16 of
-  // 256 (40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
+  // 256 (16 to 40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
   // of 4096 with 8 heads of 64: 8 rows with room for 16, 32, 64 94, 96, 96 us,
   // 64 rows with 64, 32 104, 153.
   const int64_t group = a->heads / a->kv_heads;
