@@ -268,7 +268,8 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_attention_args_size.restype = ctypes.c_int64
     C, i32, i64 = ctypes.POINTER(SpecVerifyCache), ctypes.c_int32, ctypes.c_int64
     for name, types in (("reserve", [C, i32, P, P, i64, P, P, P, P]), ("truncate", [C, i32, P, P, P, P]),
-                        ("commit", [C, i32, P, P, P, P, P]), ("commit_reserved", [C, i32, P, P, P, P, P, P]), ("fork", [C, i32, P, P, P, P]), ("compact", [C, P, P]),
+                        ("commit", [C, i32, P, P, P, P, P]), ("commit_reserved", [C, i32, P, P, P, P, P, P]),
+                        ("fork", [C, i32, P, P, P, P]), ("compact", [C, P, P]),
                         ("write", [C, i32, i64, P, i64, i64, P, i64, i64, P, P])):
         f = getattr(lib, "spec_verify_cache_" + name)
         f.argtypes, f.restype = types, ctypes.c_int

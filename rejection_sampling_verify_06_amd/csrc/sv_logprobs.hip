@@ -20,7 +20,8 @@
 // Measured on one MI355X (rocprofv3): 865 rows of 152064 bf16 logits among
 // 1410 (263 MB) with 20 alternatives, chunks 52 us (5.1 TB/s), rows 18 us; every
 // one of the 1410 rows, without alternatives, 69 us (6.2 TB/s); 119 rows of
-// 128255 floats (61 MB) 15 + 4 us (4.0 TB/s: 3808 blocks, a short launch); 6 rows of 32000 bf16 with 5 alternatives 5.3 + 8.6.
+// 128255 floats (61 MB) 15 + 4 us (4.0 TB/s: 3808 blocks, a short launch); 6
+// rows of 32000 bf16 with 5 alternatives 5.3 + 8.4.
 
 #include <hip/hip_runtime.h>
 #include <math.h>

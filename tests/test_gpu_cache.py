@@ -467,10 +467,11 @@ def test_a_refused_reserve_sits_the_round_out(sv):
         at += rows
     logits = (o["out"].view(total, -1).float() @ torch.randn(256, V, device="cuda")).to(dtype)
     ver = sv.Verifier(max_batch=8, max_k=16, max_vocab=V)
-    mode = torch.full((len(seqs),), sv.SV_ONEHOT, dtype=torch.uint8, device="cuda")
-    out = ver.run(logits, None, torch.zeros(sum(K), dtype=torch.int32, device="cuda"), nd, mode=mode, seed=1)
-    A = out["accepted_len"].tolist()
-    assert [a for a, s in zip(A, want[0]) if s < 0] == [-1] * 4 and min(A[1], A[2]) >= 0
+    for kind in (sv.SV_GREEDY, sv.SV_ONEHOT):
+        mode = torch.full((len(seqs),), kind, dtype=torch.uint8, device="cuda")
+        out = ver.run(logits, None, torch.zeros(sum(K), dtype=torch.int32, device="cuda"), nd, mode=mode, seed=1)
+        A = out["accepted_len"].tolist()
+        assert [a for a, s in zip(A, want[0]) if s < 0] == [-1] * 4 and min(A[1], A[2]) >= 0
     lp = sv.token_logprobs(logits, out["emitted"])
     assert (lp["logprob"][:4] == 0).all() and not lp["status"][:4].any()
     # whatever is said to be accepted of a refused entry
