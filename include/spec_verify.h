@@ -635,6 +635,123 @@ int64_t spec_verify_cache_workspace(const spec_verify_cache* cache);
 /* sizeof(spec_verify_cache) as compiled into the library. */
 int64_t spec_verify_cache_size(void);
 
+/* ---- a cache held in 8 bits ----------------------------------------------------
+ * The same paged cache with k and v as 8-bit codes, half the bytes to keep and
+ * to read.  A vector (one token's key or value of one head) is head_dim codes
+ * and one float32 scale, x ~ scale * code:
+ *   SV_CODES_E4M3  8-bit floating point (4 exponent, 3 mantissa bits, largest
+ *                  448); the scale is the smallest power of two under which no
+ *                  element is above 448, the code x / scale to nearest even
+ *   SV_CODES_INT8  scale = max |x| / 127, code = round(x * (127 / max |x|))
+ * both in float32.  A vector whose largest magnitude is below 2^-100 is held as
+ * 0, one that is not finite as NaN.
+ *   k, v of spec_verify_cache  [layers][num_pages][kv_heads][page_size][head_dim] codes
+ *   k_scale, v_scale           [layers][num_pages][kv_heads][page_size] float, 16-byte aligned
+ *   dtype                      SV_BF16 or SV_F16: what is written and read back
+ * head_dim is a multiple of 16, at most 512.  spec_verify_cache_truncate,
+ * _commit, _commit_reserved and _fork touch no page and serve both kinds; the
+ * calls that do take the codes as well, with codes = NULL for a 16-bit cache:
+ *
+ * spec_verify_coded_cache_reserve, _compact: as without; reserve also gives
+ * positions, int32 [total_new] or NULL: each new token's place in its sequence
+ * (-1: refused).
+ * spec_verify_coded_cache_write: as spec_verify_cache_write, rows of the 16-bit
+ * type, held as codes (codes is required).
+ * spec_verify_cache_read: tokens first[b] .. first[b] + count[b] - 1 of each
+ * sequence's keys and values in a layer, packed [total][kv_heads][head_dim] of
+ * the 16-bit type `dtype` (codes times scale, rounded, at most its largest
+ * finite value), k_out and v_out 16-byte aligned.  total = sum count <= 524288,
+ * batch <= 4096, seqs (or NULL) may name a slot twice.  status (int32 [batch]
+ * or NULL): SV_ST_BAD_LAYOUT (counts that do not add up: for every entry, all
+ * rows are NaN), SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH (tokens the sequence does not
+ * have): the entry's rows are NaN; SV_ST_BAD_PAGE: those of the page are.
+ *
+ * Streams, errors and no-ops as for the paged cache. */
+enum { SV_CODES_NONE = 0, SV_CODES_E4M3 = 1, SV_CODES_INT8 = 2 };
+typedef struct spec_verify_codes {
+  int32_t codes;               /* SV_CODES_E4M3 or SV_CODES_INT8 */
+  int32_t dtype;
+  float* k_scale;
+  float* v_scale;
+} spec_verify_codes;
+int spec_verify_coded_cache_reserve(const spec_verify_cache* cache, const spec_verify_codes* codes, int32_t batch,
+                                    const int32_t* seqs, const int32_t* num_new, int64_t total_new, int32_t* start,
+                                    int64_t* slots, int32_t* positions, int32_t* status, void* hip_stream);
+int spec_verify_coded_cache_compact(const spec_verify_cache* cache, const spec_verify_codes* codes, int32_t* live,
+                                    void* hip_stream);
+int spec_verify_coded_cache_write(const spec_verify_cache* cache, const spec_verify_codes* codes, int32_t layer, int64_t rows,
+                                  const void* k_new, int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
+                                  int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots, void* hip_stream);
+int spec_verify_cache_read(const spec_verify_cache* cache, const spec_verify_codes* codes, int32_t dtype, int32_t layer,
+                           int32_t batch, const int32_t* seqs, const int32_t* first, const int32_t* count, int64_t total,
+                           void* k_out, void* v_out, int32_t* status, void* hip_stream);
+
+/* sizeof(spec_verify_codes) as compiled into the library. */
+int64_t spec_verify_codes_size(void);
+
+/* ---- norms and position rotation of queries and keys ---------------------------
+ * What a layer does to its projections' rows before it attends, in one pass.
+ * For each head's vector x of row r, a token at positions[r]:
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (y = x where the weight is NULL)
+ *   pair i of rotary / 2: (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ *   with t = positions[r] * inv_freq[i], the pair (y_i, y_{i + rotary/2}) or,
+ *   interleaved, (y_2i, y_2i+1); numbers from rotary on stay y
+ * in float32 (angles in float64), rounded once.
+ *   q, k           [rows][heads], [rows][kv_heads][head_dim] of dtype SV_BF16 or
+ *                  SV_F16, strides in elements for row and head
+ *   positions      [rows] int32; a row with a negative one is left out: NaN in
+ *                  q_out and k_out, nothing in the cache
+ *   inv_freq       [rotary / 2] double, radians for each position
+ *   q_weight, k_weight   [head_dim] of weight_dtype (dtype, or SV_F32), each
+ *                  may be NULL
+ *   q_out          [rows][heads][head_dim], contiguous
+ * Without a cache, k_out is [rows][kv_heads][head_dim], contiguous, and v and
+ * slots are NULL.  With one, the keys go to the places slots[r] (int64, from
+ * reserve) of `layer` instead, with them v ([rows][kv_heads][head_dim], as it
+ * is), and k_out is NULL; codes as for spec_verify_coded_cache_write (keys are
+ * held straight from float32); places outside the pool are left out, none may
+ * be named twice.
+ * head_dim a multiple of 16, at most 512; rotary a multiple of 16 from 0 to
+ * head_dim; rows <= 524288; heads >= 1, kv_heads >= 1, together at most 4096;
+ * eps >= 0; q, k, v, weights and outputs 16-byte aligned, strides in multiples
+ * of 8 elements.  Outputs must not overlap inputs.
+ * Enqueues one kernel on `hip_stream`, which belongs to the calling thread's
+ * current device; allocates nothing, does not synchronise.  SV_ERR_INVALID:
+ * nothing was enqueued.  rows == 0 is a no-op. */
+typedef struct spec_verify_rope_args {
+  int64_t rows;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t rotary;
+  int32_t interleaved;
+  int32_t dtype;
+  int32_t weight_dtype;
+  int32_t layer;
+  double eps;
+  const void* q;
+  int64_t q_row_stride;
+  int64_t q_head_stride;
+  const void* k;
+  int64_t k_row_stride;
+  int64_t k_head_stride;
+  const void* v;
+  int64_t v_row_stride;
+  int64_t v_head_stride;
+  const int32_t* positions;
+  const double* inv_freq;
+  const void* q_weight;
+  const void* k_weight;
+  void* q_out;
+  void* k_out;
+  const int64_t* slots;
+} spec_verify_rope_args;
+int spec_verify_qk_norm_rope(const spec_verify_rope_args* args, const spec_verify_cache* cache,
+                             const spec_verify_codes* codes, void* hip_stream);
+
+/* sizeof(spec_verify_rope_args) as compiled into the library. */
+int64_t spec_verify_rope_args_size(void);
+
 /* Library version string. */
 const char* spec_verify_version(void);
 

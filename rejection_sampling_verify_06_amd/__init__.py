@@ -27,13 +27,14 @@ from ._lib import (  # noqa: F401
     SV_F32, SV_BF16, SV_F16, SV_SAMPLE, SV_GREEDY, SV_ONEHOT, SV_STRICT,
     SV_ST_BAD_LAYOUT, SV_ST_K_TOO_LARGE, SV_ST_BAD_MODE, SV_ST_BAD_TEMPERATURE,
     SV_ST_NO_DRAFT_LOGITS, SV_ST_BAD_TOKEN, SV_ST_NONFINITE, SV_ST_ZERO_RESIDUAL,
-    SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH, SV_ST_BAD_PAGE, SV_ST_CACHE_FULL,
+    SV_ST_BAD_SEQ, SV_ST_BAD_LENGTH, SV_ST_BAD_PAGE, SV_ST_CACHE_FULL, SV_CODES_NONE, SV_CODES_E4M3, SV_CODES_INT8,
     KERNEL_NAMES, LibraryMissing,
     SV_ADAPT_WINDOW, SV_ADAPT_MULTIPLICATIVE, SV_ADAPT_OPTIMAL_K, SV_ADAPT_COUNT_EMITTED, SV_ADAPT_COUNT_DRAFT_ONLY,
 )
 
 __all__ = ["Verifier", "VerifyError", "verify", "propose_ngram", "NgramProposer", "AcceptanceStats",
            "DraftLengthController", "token_logprobs", "paged_attention", "PagedCache",
+           "qk_norm_rope",
            "LibraryMissing", "KERNEL_NAMES"]
 
 
@@ -569,6 +570,72 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     return _for_caller(out, dev, stream)
 
 
+def _rope_rows(t, name, dtype, dev, rows, torch, heads=None):
+    """A [rows, heads, head_dim] tensor with unit stride in its last
+    dimension: its strides of row and head (0 where the dimension is 1)."""
+    if t.dim() != 3 or t.shape[0] != rows or (heads is not None and tuple(t.shape[1:]) != heads):
+        raise ValueError(f"{name} must be [{rows}, {'heads, head_dim' if heads is None else f'{heads[0]}, {heads[1]}'}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return t.stride(0) if rows > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream, cache=None, layer=0, v=None, slots=None):
+    import torch
+    lib = _lib.load()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim]")
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    N, H, D = q.shape
+    dt = _cache_dtype(q, "q", torch)
+    KV = int(k.shape[1])
+    qs, ks = _rope_rows(q, "q", q.dtype, dev, N, torch), _rope_rows(k, "k", q.dtype, dev, N, torch, (KV, D))
+    vs = (0, 0) if v is None else _rope_rows(v, "v", q.dtype, dev, N, torch, (KV, D))
+    _need(positions, "positions", (torch.int32,), torch, N, dev)
+    _need(inv_freq, "inv_freq", (torch.float64,), torch, None, dev)
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(w, name, (q.dtype, torch.float32), torch, D, dev)
+    if len({w.dtype for w in weights}) > 1:
+        raise TypeError(f"q_weight is {q_weight.dtype}, k_weight {k_weight.dtype}")
+    _need(slots, "slots", (torch.int64,), torch, N, dev)
+    with _on_stream(dev, stream, q, k, v, positions, inv_freq, q_weight, k_weight, slots):
+        out = {"q": torch.empty((N, H, D), dtype=q.dtype, device=dev),
+               "k": torch.empty((N, KV, D), dtype=q.dtype, device=dev) if cache is None else None}
+        a = _lib.SpecVerifyRopeArgs(
+            N, H, KV, D, _int32(2 * inv_freq.numel(), "rotary"), int(bool(interleaved)), dt,
+            SV_F32 if weights and weights[0].dtype == torch.float32 else dt, _int32(layer, "layer"), float(eps),
+            q.data_ptr(), *qs, k.data_ptr(), *ks, _ptr(v), *vs, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
+            _ptr(k_weight), out["q"].data_ptr(), _ptr(out["k"]), _ptr(slots))
+        _check(lib.spec_verify_qk_norm_rope(ctypes.byref(a), None if cache is None else cache._ref,
+                                            None if cache is None else cache._codes, _queue(dev)))
+    return _for_caller(out, dev, stream)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 stream=None) -> dict:
+    """Norms of queries and keys for each head and their position rotation, in
+    one pass (spec_verify_qk_norm_rope).
+
+    ``q`` is [rows, heads, head_dim], ``k`` [rows, kv_heads, head_dim],
+    bfloat16 or float16 (any strides of the first two: views of a fused
+    projection's output).  With ``q_weight`` / ``k_weight`` ([head_dim], that
+    type or float32) each head's vector becomes x / sqrt(mean x^2 + eps) *
+    weight.  Then its first ``2 * len(inv_freq)`` numbers are rotated by
+    ``positions`` (int32 [rows]) times ``inv_freq`` (float64, radians for each
+    position): pairs (i, i + len(inv_freq)), or with ``interleaved``
+    neighbours.  Rows with a negative position (those that a ``reserve``
+    refused) become NaN.  Returns new, contiguous ``q`` and ``k``.
+    ``PagedCache.write_rotated`` puts the keys into the cache instead."""
+    return _qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream)
+
+
 class PagedCache:
     """A paged key-value cache on the device (spec_verify_cache_*): ``k`` and
     ``v`` [layers, num_pages, kv_heads, page_size, head_dim], ``page_table``
@@ -586,15 +653,20 @@ class PagedCache:
     ``seqs`` (int32 [batch], distinct slots, or None for 0 .. batch - 1) and
     the counts are device tensors; nothing here waits for the device.  The
     calls return a status per entry (0, or SV_ST_* bits of why it was refused
-    and changed nothing).  With ``start`` a sequence that could not be reserved
+    and changed nothing).  ``quant`` "e4m3" or "int8" holds keys and values in 8
+    bits: ``k`` and ``v`` are codes (torch.float8_e4m3fn or int8), ``k_scale`` and
+    ``v_scale`` ([layers, num_pages, kv_heads, page_size], float32) one scale for
+    each token and head; ``dtype`` is what goes in and comes out.  With ``start`` a sequence that could not be reserved
     for sits its round out: its rows of ``o`` are NaN, so that a verify call
     over their logits refuses it, and ``commit`` leaves it as it was.  Calls on
     one cache must be ordered on one stream."""
 
     def __init__(self, layers: int, num_pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
-                 max_pages: int, dtype=None, device=None):
+                 max_pages: int, dtype=None, device=None, quant: Optional[str] = None):
         import torch
         self._torch, self._lib = torch, _lib.load()
+        if quant not in (None, "e4m3", "int8"):
+            raise ValueError(f"quant is None, 'e4m3' or 'int8', got {quant!r}")
         dtype = torch.bfloat16 if dtype is None else dtype
         dev = torch.device("cuda", 0) if device is None else torch.device(device)
         if dev.type != "cuda":
@@ -610,8 +682,18 @@ class PagedCache:
             _check(int(nbytes))
         self.device, self.layers, self.page_size = dev, int(layers), int(page_size)
         shape = (c.layers, c.num_pages, c.kv_heads, c.page_size, c.head_dim)
-        self.k = torch.empty(shape, dtype=dtype, device=dev)
-        self.v = torch.empty(shape, dtype=dtype, device=dev)
+        held = {None: dtype, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[quant]
+        if quant is not None and (c.head_dim % 16 or c.head_dim > 512):
+            raise ValueError(f"a cache in 8 bits has a head_dim that is a multiple of 16, at most 512, got {c.head_dim}")
+        self.k = torch.empty(shape, dtype=held, device=dev)
+        self.v = torch.empty(shape, dtype=held, device=dev)
+        self.dtype, self.quant = dtype, quant
+        self.k_scale = self.v_scale = self._codes = None
+        if quant is not None:
+            self.k_scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            self.v_scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+            self._codes = _lib.SpecVerifyCodes(SV_CODES_E4M3 if quant == "e4m3" else SV_CODES_INT8,
+                                               SV_BF16 if dtype == torch.bfloat16 else SV_F16, _ptr(self.k_scale), _ptr(self.v_scale))
         i32 = dict(dtype=torch.int32, device=dev)
         self.page_table = torch.full((c.slots, c.max_pages), -1, **i32)
         self.seq_len = torch.zeros(c.slots, **i32)
@@ -625,7 +707,8 @@ class PagedCache:
     def _on_stream(self, stream, *inputs):
         if stream is None:
             return _on_stream(self.device, None)
-        return _on_stream(self.device, stream, self.k, self.v, self.page_table, self.seq_len, self.refcount, self._ws, *inputs)
+        return _on_stream(self.device, stream, self.k, self.v, self.k_scale, self.v_scale, self.page_table, self.seq_len, self.refcount,
+                          self._ws, *inputs)
 
     def _entries(self, seqs, counts, name):
         """The batch size, with the index arrays checked."""
@@ -635,22 +718,28 @@ class PagedCache:
         _need(seqs, "seqs", (torch.int32,), torch, B, self.device)
         return B
 
-    def reserve(self, seqs, num_new, total_new: int, stream=None) -> dict:
+    def reserve(self, seqs, num_new, total_new: int, stream=None, *, want_positions: bool = False) -> dict:
         """Grows each sequence by ``num_new`` tokens (int32 [batch], summing to
         ``total_new``).  Returns ``start`` (int32 [batch]: the old lengths),
-        ``slots`` (int64 [total_new]: the new tokens' places, for ``write``)
-        and ``status``; -1 in the first two where an entry was refused.  Users
-        of a partly filled last page that all append in one call each get a
-        copy of it, and it is free only afterwards: one page more than in two
-        calls."""
+        ``slots`` (int64 [total_new]: the new tokens' places, for ``write``),
+        ``positions`` if asked for (int32 [total_new]: the new tokens' numbers
+        in their sequences, for ``write_rotated``) and ``status``; -1 in the first
+        three where an entry was refused.  Users of a partly filled last page that
+        all append in one call each get a copy of it, and it is free only
+        afterwards: one page more than in two calls."""
         torch = self._torch
         B, n = self._entries(seqs, num_new, "num_new"), int(total_new)
         with self._on_stream(stream, seqs, num_new):
             out = {"start": torch.empty(B, dtype=torch.int32, device=self.device),
                    "slots": torch.empty(max(n, 0), dtype=torch.int64, device=self.device),
                    "status": torch.empty(B, dtype=torch.int32, device=self.device)}
-            _check(self._lib.spec_verify_cache_reserve(self._ref, B, _ptr(seqs), num_new.data_ptr(), n, _ptr(out["start"]),
-                                                       _ptr(out["slots"]), _ptr(out["status"]), _queue(self.device)))
+            a = (B, _ptr(seqs), num_new.data_ptr(), n, _ptr(out["start"]), _ptr(out["slots"]))
+            if self._codes is None and not want_positions:
+                _check(self._lib.spec_verify_cache_reserve(self._ref, *a, _ptr(out["status"]), _queue(self.device)))
+            else:
+                out["positions"] = torch.empty(max(n, 0), dtype=torch.int32, device=self.device) if want_positions else None
+                _check(self._lib.spec_verify_coded_cache_reserve(self._ref, self._codes, *a, _ptr(out["positions"]), _ptr(out["status"]),
+                                                                 _queue(self.device)))
         return _for_caller(out, self.device, stream)
 
     def write(self, layer: int, k_new, v_new, slots, stream=None):
@@ -662,16 +751,55 @@ class PagedCache:
             if t.shape != (rows, *heads) or t.stride(2) != 1:
                 raise ValueError(f"{name} must be [{rows}, {heads[0]}, {heads[1]}] with unit stride in the last dimension, got "
                                  f"{tuple(t.shape)}")
-            if t.dtype != self.k.dtype:
-                raise TypeError(f"{name} is {t.dtype}, the cache {self.k.dtype}")
+            if t.dtype != self.dtype:
+                raise TypeError(f"{name} is {t.dtype}, the cache {self.dtype}")
             if t.device != dev:
                 raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
         # strides of dimensions of size 1 say nothing
         r, h = rows > 1, heads[0] > 1
         with self._on_stream(stream, k_new, v_new, slots):
-            _check(self._lib.spec_verify_cache_write(
-                self._ref, _int32(layer, "layer"), rows, k_new.data_ptr(), k_new.stride(0) if r else 0, k_new.stride(1) if h else 0,
-                v_new.data_ptr(), v_new.stride(0) if r else 0, v_new.stride(1) if h else 0, slots.data_ptr(), _queue(dev)))
+            a = (_int32(layer, "layer"), rows, k_new.data_ptr(), k_new.stride(0) if r else 0, k_new.stride(1) if h else 0,
+                 v_new.data_ptr(), v_new.stride(0) if r else 0, v_new.stride(1) if h else 0, slots.data_ptr(), _queue(dev))
+            if self._codes is None:
+                _check(self._lib.spec_verify_cache_write(self._ref, *a))
+            else:
+                _check(self._lib.spec_verify_coded_cache_write(self._ref, self._codes, *a))
+
+    def write_rotated(self, layer: int, q, k_new, v_new, slots, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      interleaved: bool = False, stream=None):
+        """``qk_norm_rope`` of a layer's new rows with the keys, and ``v_new`` as
+        they are, going into the places ``slots`` (``slots`` and ``positions`` of
+        ``reserve``).  Returns the rotated queries."""
+        if q.device != self.device:
+            raise ValueError(f"q is on {q.device}, the cache on {self.device}")
+        if q.dtype != self.dtype:
+            raise TypeError(f"q is {q.dtype}, the cache {self.dtype}")
+        if k_new.dim() != 3 or tuple(k_new.shape[1:]) != self._heads:
+            raise ValueError(f"k_new must be [rows, {self._heads[0]}, {self._heads[1]}], got {tuple(k_new.shape)}")
+        if stream is not None:
+            self._on_stream(stream)
+        return _qk_norm_rope(q, k_new, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream, self, layer, v_new, slots)["q"]
+
+    def read(self, layer: int, seqs, first, count, total: int, stream=None) -> dict:
+        """Tokens ``first`` .. ``first + count - 1`` (int32 [batch] each) of the
+        sequences out of a layer, packed: ``k`` and ``v`` [total, kv_heads,
+        head_dim] of the cache's dtype, and ``status``.  ``total`` is the sum
+        of ``count``; a sequence may be named more than once.  Rows of a refused
+        entry are NaN."""
+        torch = self._torch
+        _need(first, "first", (torch.int32,), torch, None, self.device)
+        B, n = int(first.numel()), int(total)
+        _need(count, "count", (torch.int32,), torch, B, self.device)
+        _need(seqs, "seqs", (torch.int32,), torch, B, self.device)
+        with self._on_stream(stream, seqs, first, count):
+            shape = (max(n, 0), *self._heads)
+            out = {"k": torch.empty(shape, dtype=self.dtype, device=self.device),
+                   "v": torch.empty(shape, dtype=self.dtype, device=self.device),
+                   "status": torch.empty(B, dtype=torch.int32, device=self.device)}
+            _check(self._lib.spec_verify_cache_read(
+                self._ref, self._codes, SV_BF16 if self.dtype == torch.bfloat16 else SV_F16, _int32(layer, "layer"), B, _ptr(seqs),
+                first.data_ptr(), count.data_ptr(), n, _ptr(out["k"]), _ptr(out["v"]), _ptr(out["status"]), _queue(self.device)))
+        return _for_caller(out, self.device, stream)
 
     def attend(self, layer: int, q, num_draft, seqs=None, **kw) -> dict:
         """``paged_attention`` of ``q`` over a layer of this cache."""
@@ -734,7 +862,10 @@ class PagedCache:
         torch = self._torch
         with self._on_stream(stream):
             live = torch.empty(1, dtype=torch.int32, device=self.device)
-            _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), _queue(self.device)))
+            if self._codes is None:
+                _check(self._lib.spec_verify_cache_compact(self._ref, live.data_ptr(), _queue(self.device)))
+            else:
+                _check(self._lib.spec_verify_coded_cache_compact(self._ref, self._codes, live.data_ptr(), _queue(self.device)))
         return _for_caller(live, self.device, stream)
 
 

@@ -22,6 +22,7 @@ SV_ST_BAD_SEQ = 256
 SV_ST_BAD_LENGTH = 512
 SV_ST_BAD_PAGE = 1024
 SV_ST_CACHE_FULL = 2048
+SV_CODES_NONE, SV_CODES_E4M3, SV_CODES_INT8 = 0, 1, 2
 SV_NUM_KERNELS = 4
 KERNEL_NAMES = ("row_stats", "filter", "final", "select")
 
@@ -57,6 +58,8 @@ EXPORTED = (
     "spec_verify_cache_reserve", "spec_verify_cache_truncate", "spec_verify_cache_commit",
     "spec_verify_cache_commit_reserved", "spec_verify_cache_fork", "spec_verify_cache_compact", "spec_verify_cache_write",
     "spec_verify_cache_workspace", "spec_verify_cache_size",
+    "spec_verify_coded_cache_reserve", "spec_verify_coded_cache_compact", "spec_verify_coded_cache_write",
+    "spec_verify_cache_read", "spec_verify_codes_size", "spec_verify_qk_norm_rope", "spec_verify_rope_args_size",
 )
 SV_CACHE_MAX_SLOTS = 4096
 SV_LOGPROBS_MAX_TOP = 64
@@ -202,6 +205,46 @@ class SpecVerifyCache(ctypes.Structure):
     ]
 
 
+class SpecVerifyCodes(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+    ]
+
+
+class SpecVerifyRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("layer", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+        ("q", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_row_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -273,6 +316,18 @@ def load() -> ctypes.CDLL:
                         ("write", [C, i32, i64, P, i64, i64, P, i64, i64, P, P])):
         f = getattr(lib, "spec_verify_cache_" + name)
         f.argtypes, f.restype = types, ctypes.c_int
+    Q = ctypes.POINTER(SpecVerifyCodes)
+    for name, types in (("coded_cache_reserve", [C, Q, i32, P, P, i64, P, P, P, P, P]), ("coded_cache_compact", [C, Q, P, P]),
+                        ("coded_cache_write", [C, Q, i32, i64, P, i64, i64, P, i64, i64, P, P]),
+                        ("cache_read", [C, Q, i32, i32, i32, P, P, P, i64, P, P, P, P]),
+                        ("qk_norm_rope", [ctypes.POINTER(SpecVerifyRopeArgs), C, Q, P])):
+        f = getattr(lib, "spec_verify_" + name)
+        f.argtypes, f.restype = types, ctypes.c_int
+    for name, view in (("codes", SpecVerifyCodes), ("rope_args", SpecVerifyRopeArgs)):
+        f = getattr(lib, f"spec_verify_{name}_size")
+        f.argtypes, f.restype = [], i64
+        if f() != ctypes.sizeof(view):
+            raise RuntimeError(f"spec_verify_{name} layout differs between the library and the binding")
     lib.spec_verify_cache_workspace.argtypes = [C]
     lib.spec_verify_cache_workspace.restype = ctypes.c_int64
     lib.spec_verify_cache_size.argtypes = []

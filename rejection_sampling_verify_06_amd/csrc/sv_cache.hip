@@ -176,7 +176,10 @@ __global__ void __launch_bounds__(kCaThreads) k_cache_reserve(CacheParams P) {
       P.start[b] = -1;
       if (P.status) P.status[b] = SV_ST_BAD_LAYOUT;
     }
-    for (int64_t r = t; r < P.total_new; r += kCaThreads) P.new_slots[r] = -1;
+    for (int64_t r = t; r < P.total_new; r += kCaThreads) {
+      P.new_slots[r] = -1;
+      if (P.positions) P.positions[r] = -1;
+    }
     if (t == 0) *P.count = 0;
     return;
   }
@@ -245,11 +248,13 @@ __global__ void __launch_bounds__(kCaThreads) k_cache_reserve(CacheParams P) {
     }
     const int start = P.start[lo];
     int64_t at = -1;
+    int pos = -1;
     if (start >= 0) {
-      const int pos = start + (int)((uint32_t)r - (lo ? rend[lo - 1] : 0u));
+      pos = start + (int)((uint32_t)r - (lo ? rend[lo - 1] : 0u));
       at = (int64_t)P.table[(int64_t)slot_of(P, P.seqs, lo) * P.max_pages + (pos >> P.page_log2)] * P.page_size + (pos & mask);
     }
     P.new_slots[r] = at;
+    if (P.positions) P.positions[r] = pos;
   }
   if (t == 0) *P.count = (int)sh.count;
 }
@@ -415,8 +420,9 @@ __global__ void __launch_bounds__(kCaThreads) k_cache_compact(CacheParams P) {
   }
 }
 
-// The pages of the list, in every layer, K and V; with `remap` the first
-// blocks give the page tables their new names (which the copies do not read).
+// The pages of the list, in every layer, K and V (and their scales, behind the
+// page's codes); with `remap` the first blocks give the page tables their new
+// names (which the copies do not read).
 __global__ void __launch_bounds__(kCopyThreads) k_cache_copy(CacheParams P, int remap) {
   const int t = threadIdx.x;
   if ((int)blockIdx.x < remap) {
@@ -431,17 +437,22 @@ __global__ void __launch_bounds__(kCopyThreads) k_cache_copy(CacheParams P, int 
     return;
   }
   const int count = *P.count;
-  const int64_t chunks = (P.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t data_chunks = (P.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t chunks = data_chunks + (P.scale_bytes + kCopyBytes - 1) / kCopyBytes;
   const int64_t total = (int64_t)count * P.layers * 2 * chunks;
   for (int64_t i = blockIdx.x - remap; i < total; i += gridDim.x - remap) {
-    const int64_t c = i % chunks, r = i / chunks;
+    int64_t c = i % chunks;
+    const int64_t r = i / chunks;
     const int which = (int)(r & 1);
     const int64_t r2 = r >> 1, layer = r2 / count, k = r2 - layer * count;
     const int2 m = P.pairs[k];
-    char* pool = (char*)(which ? P.v : P.k) + layer * P.layer_bytes;
-    const char* src = pool + (int64_t)m.x * P.page_bytes + c * kCopyBytes;
-    char* dst = pool + (int64_t)m.y * P.page_bytes + c * kCopyBytes;
-    const int64_t n = min((int64_t)kCopyBytes, P.page_bytes - c * kCopyBytes);
+    const bool scales = c >= data_chunks;
+    c -= scales ? data_chunks : 0;
+    const int64_t bytes = scales ? P.scale_bytes : P.page_bytes;
+    char* pool = scales ? (char*)(which ? P.vs : P.ks) + layer * P.scale_bytes * P.num_pages : (char*)(which ? P.v : P.k) + layer * P.layer_bytes;
+    const char* src = pool + (int64_t)m.x * bytes + c * kCopyBytes;
+    char* dst = pool + (int64_t)m.y * bytes + c * kCopyBytes;
+    const int64_t n = min((int64_t)kCopyBytes, bytes - c * kCopyBytes);
     u32x4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -482,7 +493,7 @@ size_t lds_bytes(const CacheParams& p) { return 4 * (2 * (size_t)p.B + (size_t)p
 // Blocks of a copy whose length only the device knows: enough to fill the
 // chip when there is work, few enough to cost little when there is none.
 int copy_blocks(const CacheParams& p, int64_t most) {
-  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes + (p.scale_bytes + kCopyBytes - 1) / kCopyBytes;
   const int64_t n = most * p.layers * 2 * chunks;
   return (int)(n < 2048 ? n : 2048);
 }

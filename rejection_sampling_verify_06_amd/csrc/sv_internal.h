@@ -275,11 +275,15 @@ struct CacheParams {
   void* k;                          // [layers][num_pages] pages of page_bytes
   void* v;
   int64_t page_bytes, layer_bytes;
+  float* ks;                        // the codes' scales, [layers][num_pages] pages of scale_bytes, or NULL
+  float* vs;
+  int64_t scale_bytes;              // 0: no scales
   const int32_t* seqs;              // or NULL (fork: the parents)
   const int32_t* num_new;           // reserve
   int64_t total_new;
   int32_t* start;
   int64_t* new_slots;
+  int32_t* positions;               // or NULL
   const int32_t* drop;              // truncate: these, or what num_draft / accepted say, or all
   const int32_t* num_draft;
   const int32_t* accepted;
@@ -305,6 +309,59 @@ struct CacheWriteParams {
   int64_t k_row, k_head, v_row, v_head;   // strides in elements
   const int64_t* new_slots;
 };
+
+// norms and rotation of queries and keys, writes of codes, and reading a cache back (sv_rope.hip)
+struct RopeParams {
+  int64_t rows;
+  int32_t H, KV, NV;                // heads of queries, keys and values (0: none)
+  int32_t D, R;                     // head dimension, and how much of it is rotated
+  int32_t bf16;                     // else float16
+  int32_t neighbours;               // pairs (2i, 2i + 1); else (i, i + R / 2)
+  int32_t weight_f32;
+  float eps, inv_dim;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;   // strides in elements
+  const int32_t* positions;         // NULL: nothing is rotated
+  const double* inv_freq;           // [R / 2]
+  const void* q_weight;             // or NULL: no norm
+  const void* k_weight;
+  void* q_out;                      // [rows][H][D]
+  void* k_out;                      // [rows][KV][D], or NULL: into the cache
+  const int64_t* slots;             // places in the cache
+  int64_t places;
+  int32_t page_log2;
+  int32_t codes;
+  void* ck;                         // one layer's pages
+  void* cv;
+  float* ks;
+  float* vs;
+  int32_t parts, per;               // waves of a row, and groups of heads a wave takes (set by the launch)
+};
+
+struct CacheReadParams {
+  int32_t B, slots, max_pages, page_size, page_log2, num_pages, max_len;
+  int32_t kv_heads, D, head_vecs;
+  int32_t bf16, codes;
+  int32_t total;                    // rows
+  const int32_t* table;
+  const int32_t* seq_len;
+  const int32_t* seqs;              // or NULL
+  const int32_t* first;
+  const int32_t* count;
+  const void* k;                    // one layer's pages
+  const void* v;
+  const float* ks;
+  const float* vs;
+  void* k_out;                      // [total][kv_heads][D]
+  void* v_out;
+  int32_t* status;                  // or NULL
+  int32_t work;                     // blocks that serve rows (set by the launch)
+};
+
+hipError_t launch_rope(RopeParams p, hipStream_t st);
+hipError_t launch_cache_read(CacheReadParams p, hipStream_t st);
 
 hipError_t launch_cache_reserve(const CacheParams& p, hipStream_t st);
 hipError_t launch_cache_truncate(const CacheParams& p, hipStream_t st);

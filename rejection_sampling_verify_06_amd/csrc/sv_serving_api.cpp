@@ -1,5 +1,6 @@
 // Host side of the serving operators declared in include/spec_verify.h (token
-// log probabilities, attention over a paged cache, the cache itself): argument validation and workspace layout.
+// log probabilities, attention over a paged cache, the cache itself in 16 or 8
+// bits, norms and rotation): argument validation and workspace layout.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -172,8 +173,29 @@ bool cache_sizes_ok(const char* who, const spec_verify_cache* c, CacheLayout* l)
   return true;
 }
 
+bool codes_ok(const char* who, const spec_verify_codes* q, int32_t head_dim) {
+  if (q->codes != SV_CODES_E4M3 && q->codes != SV_CODES_INT8) {
+    set_err("%s: codes %d is neither SV_CODES_E4M3 nor SV_CODES_INT8", who, q->codes);
+    return false;
+  }
+  if (q->dtype != SV_BF16 && q->dtype != SV_F16) {
+    set_err("%s: dtype %d is neither SV_BF16 nor SV_F16", who, q->dtype);
+    return false;
+  }
+  if (head_dim % 16 || head_dim > 512) {
+    set_err("%s: a head_dim of %d in 8 bits is not a multiple of 16, at most 512", who, head_dim);
+    return false;
+  }
+  if (!q->k_scale || !q->v_scale || !aligned16(q->k_scale) || !aligned16(q->v_scale)) {
+    set_err("%s: k_scale and v_scale (16-byte aligned) are required", who);
+    return false;
+  }
+  return true;
+}
+
 // The checks every call on a cache shares, and its parameters.
-bool cache_params(const char* who, const spec_verify_cache* c, int32_t batch, sv::CacheParams* p) {
+bool cache_params(const char* who, const spec_verify_cache* c, int32_t batch, sv::CacheParams* p,
+                  const spec_verify_codes* q = nullptr) {
   CacheLayout l;
   if (!cache_sizes_ok(who, c, &l)) return false;
   if (!c->page_table || !c->seq_len || !c->refcount || !c->k || !c->v || !c->workspace || !aligned16(c->refcount) ||
@@ -186,6 +208,7 @@ bool cache_params(const char* who, const spec_verify_cache* c, int32_t batch, sv
     set_err("%s: batch %d outside 0..%d slots", who, batch, c->slots);
     return false;
   }
+  if (q && !codes_ok(who, q, c->head_dim)) return false;
   *p = sv::CacheParams{};
   p->B = batch;
   p->slots = c->slots;
@@ -200,13 +223,34 @@ bool cache_params(const char* who, const spec_verify_cache* c, int32_t batch, sv
   p->refcount = c->refcount;
   p->k = c->k;
   p->v = c->v;
-  p->page_bytes = (int64_t)c->kv_heads * c->head_dim * c->page_size * 2;
+  p->page_bytes = (int64_t)c->kv_heads * c->head_dim * c->page_size * (q ? 1 : 2);
+  if (q) {
+    p->ks = q->k_scale;
+    p->vs = q->v_scale;
+    p->scale_bytes = (int64_t)c->kv_heads * c->page_size * 4;
+  }
   p->layer_bytes = p->page_bytes * c->num_pages;
   char* ws = static_cast<char*>(c->workspace);
   p->count = reinterpret_cast<int32_t*>(ws);
   p->ids = reinterpret_cast<int32_t*>(ws + l.ids);
   p->pairs = reinterpret_cast<int2*>(ws + l.pairs);
   return true;
+}
+
+// Where a layer of the cache takes rows, for the kernel that norms, rotates and codes.
+void rope_cache(const spec_verify_cache* c, const spec_verify_codes* q, int32_t layer, const int64_t* slots,
+                const sv::CacheParams& p, sv::RopeParams* r) {
+  r->NV = c->kv_heads;
+  r->slots = slots;
+  r->places = (int64_t)c->num_pages * c->page_size;
+  r->page_log2 = p.page_log2;
+  r->codes = q ? q->codes : SV_CODES_NONE;
+  r->ck = static_cast<char*>(c->k) + layer * p.layer_bytes;
+  r->cv = static_cast<char*>(c->v) + layer * p.layer_bytes;
+  if (q) {
+    r->ks = q->k_scale + layer * (p.scale_bytes / 4) * c->num_pages;
+    r->vs = q->v_scale + layer * (p.scale_bytes / 4) * c->num_pages;
+  }
 }
 
 }  // namespace
@@ -360,11 +404,11 @@ int64_t spec_verify_cache_workspace(const spec_verify_cache* c) {
   return cache_sizes_ok("spec_verify_cache_workspace", c, &l) ? l.bytes : SV_ERR_INVALID;
 }
 
-int spec_verify_cache_reserve(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_new,
-                              int64_t total_new, int32_t* start, int64_t* slots, int32_t* status, void* hip_stream) {
-  const char* who = "spec_verify_cache_reserve";
+static int cache_reserve(const char* who, const spec_verify_cache* c, const spec_verify_codes* q, int32_t batch,
+                         const int32_t* seqs, const int32_t* num_new, int64_t total_new, int32_t* start, int64_t* slots,
+                         int32_t* positions, int32_t* status, void* hip_stream) {
   sv::CacheParams p;
-  if (!cache_params(who, c, batch, &p)) return SV_ERR_INVALID;
+  if (!cache_params(who, c, batch, &p, q)) return SV_ERR_INVALID;
   if (batch == 0) return SV_OK;
   if (!num_new || !start || total_new < 0 || total_new > sv::kCacheMaxRows || (total_new > 0 && !slots)) {
     set_err("%s: num_new, start and slots are required, total_new %lld in 0..%d", who, (long long)total_new,
@@ -376,9 +420,23 @@ int spec_verify_cache_reserve(const spec_verify_cache* c, int32_t batch, const i
   p.total_new = total_new;
   p.start = start;
   p.new_slots = slots;
+  p.positions = positions;
   p.status = status;
   hipError_t e = sv::launch_cache_reserve(p, (hipStream_t)hip_stream);
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_reserve(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* num_new,
+                              int64_t total_new, int32_t* start, int64_t* slots, int32_t* status, void* hip_stream) {
+  return cache_reserve("spec_verify_cache_reserve", c, nullptr, batch, seqs, num_new, total_new, start, slots, nullptr, status,
+                       hip_stream);
+}
+
+int spec_verify_coded_cache_reserve(const spec_verify_cache* c, const spec_verify_codes* q, int32_t batch, const int32_t* seqs,
+                                    const int32_t* num_new, int64_t total_new, int32_t* start, int64_t* slots,
+                                    int32_t* positions, int32_t* status, void* hip_stream) {
+  return cache_reserve("spec_verify_coded_cache_reserve", c, q, batch, seqs, num_new, total_new, start, slots, positions, status,
+                       hip_stream);
 }
 
 int spec_verify_cache_truncate(const spec_verify_cache* c, int32_t batch, const int32_t* seqs, const int32_t* drop,
@@ -444,13 +502,20 @@ int spec_verify_cache_fork(const spec_verify_cache* c, int32_t batch, const int3
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
 }
 
-int spec_verify_cache_compact(const spec_verify_cache* c, int32_t* live, void* hip_stream) {
-  const char* who = "spec_verify_cache_compact";
+static int cache_compact(const char* who, const spec_verify_cache* c, const spec_verify_codes* q, int32_t* live, void* hip_stream) {
   sv::CacheParams p;
-  if (!cache_params(who, c, 0, &p)) return SV_ERR_INVALID;
+  if (!cache_params(who, c, 0, &p, q)) return SV_ERR_INVALID;
   p.live = live;
   hipError_t e = sv::launch_cache_compact(p, (hipStream_t)hip_stream);
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_compact(const spec_verify_cache* c, int32_t* live, void* hip_stream) {
+  return cache_compact("spec_verify_cache_compact", c, nullptr, live, hip_stream);
+}
+
+int spec_verify_coded_cache_compact(const spec_verify_cache* c, const spec_verify_codes* q, int32_t* live, void* hip_stream) {
+  return cache_compact("spec_verify_coded_cache_compact", c, q, live, hip_stream);
 }
 
 int spec_verify_cache_write(const spec_verify_cache* c, int32_t layer, int64_t rows, const void* k_new,
@@ -488,6 +553,198 @@ int spec_verify_cache_write(const spec_verify_cache* c, int32_t layer, int64_t r
   w.v_head = v_head_stride;
   w.new_slots = slots;
   hipError_t e = sv::launch_cache_write(w, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int64_t spec_verify_codes_size(void) { return (int64_t)sizeof(spec_verify_codes); }
+
+int spec_verify_coded_cache_write(const spec_verify_cache* c, const spec_verify_codes* q, int32_t layer, int64_t rows,
+                                  const void* k_new, int64_t k_row_stride, int64_t k_head_stride, const void* v_new,
+                                  int64_t v_row_stride, int64_t v_head_stride, const int64_t* slots, void* hip_stream) {
+  const char* who = "spec_verify_coded_cache_write";
+  if (!q) {
+    set_err("%s: codes is NULL", who);
+    return SV_ERR_INVALID;
+  }
+  sv::CacheParams p;
+  if (!cache_params(who, c, 0, &p, q)) return SV_ERR_INVALID;
+  if (layer < 0 || layer >= c->layers || rows < 0 || rows > sv::kCacheMaxRows || c->kv_heads > 2048) {
+    set_err("%s: layer %d outside 0..%d, rows %lld outside 0..%d, or kv_heads %d above 2048", who, layer, c->layers - 1,
+            (long long)rows, sv::kCacheMaxRows, c->kv_heads);
+    return SV_ERR_INVALID;
+  }
+  if (rows == 0) return SV_OK;
+  if (!k_new || !v_new || !slots || !aligned16(k_new) || !aligned16(v_new) ||
+      !strides_ok(k_row_stride, k_head_stride, 0) || !strides_ok(v_row_stride, v_head_stride, 0)) {
+    set_err("%s: k_new and v_new (16-byte aligned, strides in multiples of 8 elements) and slots are required", who);
+    return SV_ERR_INVALID;
+  }
+  sv::RopeParams r{};
+  r.rows = rows;
+  r.KV = c->kv_heads;
+  r.D = c->head_dim;
+  r.bf16 = q->dtype == SV_BF16;
+  r.k = k_new;
+  r.k_row = k_row_stride;
+  r.k_head = k_head_stride;
+  r.v = v_new;
+  r.v_row = v_row_stride;
+  r.v_head = v_head_stride;
+  rope_cache(c, q, layer, slots, p, &r);
+  hipError_t e = sv::launch_rope(r, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int spec_verify_cache_read(const spec_verify_cache* c, const spec_verify_codes* q, int32_t dtype, int32_t layer, int32_t batch,
+                           const int32_t* seqs, const int32_t* first, const int32_t* count, int64_t total, void* k_out,
+                           void* v_out, int32_t* status, void* hip_stream) {
+  const char* who = "spec_verify_cache_read";
+  sv::CacheParams p;
+  if (!cache_params(who, c, 0, &p, q)) return SV_ERR_INVALID;
+  if (batch < 0 || batch > SV_CACHE_MAX_SLOTS) {
+    set_err("%s: batch %d outside 0..%d", who, batch, SV_CACHE_MAX_SLOTS);
+    return SV_ERR_INVALID;
+  }
+  if ((dtype != SV_BF16 && dtype != SV_F16) || (q && q->dtype != dtype)) {
+    set_err("%s: dtype %d is neither SV_BF16 nor SV_F16, or not what the codes were written from", who, dtype);
+    return SV_ERR_INVALID;
+  }
+  if (layer < 0 || layer >= c->layers || total < 0 || total > sv::kCacheMaxRows) {
+    set_err("%s: layer %d outside 0..%d, or total %lld outside 0..%d", who, layer, c->layers - 1, (long long)total,
+            sv::kCacheMaxRows);
+    return SV_ERR_INVALID;
+  }
+  if (batch == 0 && total != 0) {
+    set_err("%s: total %lld belongs to no sequence", who, (long long)total);
+    return SV_ERR_INVALID;
+  }
+  if (batch == 0) return SV_OK;
+  if (!first || !count || (total > 0 && (!k_out || !v_out)) || !aligned16(k_out) || !aligned16(v_out)) {
+    set_err("%s: first, count, k_out and v_out (16-byte aligned) are required", who);
+    return SV_ERR_INVALID;
+  }
+  sv::CacheReadParams r{};
+  r.B = batch;
+  r.slots = c->slots;
+  r.max_pages = c->max_pages;
+  r.page_size = c->page_size;
+  r.page_log2 = p.page_log2;
+  r.num_pages = c->num_pages;
+  r.max_len = p.max_len;
+  r.kv_heads = c->kv_heads;
+  r.D = c->head_dim;
+  r.head_vecs = c->head_dim / 8;
+  r.bf16 = dtype == SV_BF16;
+  r.codes = q ? q->codes : SV_CODES_NONE;
+  r.total = (int32_t)total;
+  r.table = c->page_table;
+  r.seq_len = c->seq_len;
+  r.seqs = seqs;
+  r.first = first;
+  r.count = count;
+  r.k = static_cast<char*>(c->k) + layer * p.layer_bytes;
+  r.v = static_cast<char*>(c->v) + layer * p.layer_bytes;
+  if (q) {
+    r.ks = q->k_scale + layer * (p.scale_bytes / 4) * c->num_pages;
+    r.vs = q->v_scale + layer * (p.scale_bytes / 4) * c->num_pages;
+  }
+  r.k_out = k_out;
+  r.v_out = v_out;
+  r.status = status;
+  hipError_t e = sv::launch_cache_read(r, (hipStream_t)hip_stream);
+  return e == hipSuccess ? SV_OK : hip_fail(who, e);
+}
+
+int64_t spec_verify_rope_args_size(void) { return (int64_t)sizeof(spec_verify_rope_args); }
+
+int spec_verify_qk_norm_rope(const spec_verify_rope_args* a, const spec_verify_cache* c, const spec_verify_codes* q,
+                             void* hip_stream) {
+  const char* who = "spec_verify_qk_norm_rope";
+  if (!a) {
+    set_err("%s: args is NULL", who);
+    return SV_ERR_INVALID;
+  }
+  if (a->dtype != SV_BF16 && a->dtype != SV_F16) {
+    set_err("%s: dtype %d is neither SV_BF16 nor SV_F16", who, a->dtype);
+    return SV_ERR_INVALID;
+  }
+  if (a->head_dim < 16 || a->head_dim > 512 || a->head_dim % 16 || a->rotary < 0 || a->rotary > a->head_dim || a->rotary % 16) {
+    set_err("%s: head_dim %d or rotary %d is not a multiple of 16, up to 512 and head_dim", who, a->head_dim, a->rotary);
+    return SV_ERR_INVALID;
+  }
+  if (a->heads < 1 || a->kv_heads < 1 || (int64_t)a->heads + a->kv_heads > 4096 || a->rows < 0 || a->rows > sv::kCacheMaxRows) {
+    set_err("%s: heads %d and kv_heads %d outside 1..4096 together, or rows %lld outside 0..%d", who, a->heads, a->kv_heads,
+            (long long)a->rows, sv::kCacheMaxRows);
+    return SV_ERR_INVALID;
+  }
+  if ((a->q_weight || a->k_weight) && a->weight_dtype != SV_F32 && a->weight_dtype != a->dtype) {
+    set_err("%s: weight_dtype %d is neither SV_F32 nor the dtype", who, a->weight_dtype);
+    return SV_ERR_INVALID;
+  }
+  if (!(a->eps >= 0) || !isfinite((float)a->eps)) {
+    set_err("%s: eps %g is negative or not finite", who, a->eps);
+    return SV_ERR_INVALID;
+  }
+  sv::CacheParams p;
+  if (c) {
+    if (!cache_params(who, c, 0, &p, q)) return SV_ERR_INVALID;
+    if (c->kv_heads != a->kv_heads || c->head_dim != a->head_dim || (q && q->dtype != a->dtype)) {
+      set_err("%s: the cache has %d heads of %d, the keys %d of %d (or another type)", who, c->kv_heads, c->head_dim, a->kv_heads,
+              a->head_dim);
+      return SV_ERR_INVALID;
+    }
+    if (a->layer < 0 || a->layer >= c->layers) {
+      set_err("%s: layer %d outside 0..%d", who, a->layer, c->layers - 1);
+      return SV_ERR_INVALID;
+    }
+  } else if (q) {
+    set_err("%s: codes without a cache", who);
+    return SV_ERR_INVALID;
+  }
+  if (a->rows == 0) return SV_OK;
+  if (!a->q || !a->k || !a->positions || !a->q_out || (a->rotary > 0 && !a->inv_freq) || (c != nullptr) != (a->v != nullptr) ||
+      (c != nullptr) != (a->slots != nullptr) || (c != nullptr) != (a->k_out == nullptr)) {
+    set_err("%s: q, k, positions, inv_freq and q_out are required, and k_out, or with a cache v and slots", who);
+    return SV_ERR_INVALID;
+  }
+  for (const void* x : {a->q, a->k, a->v, a->q_weight, a->k_weight, (const void*)a->q_out, (const void*)a->k_out})
+    if (!aligned16(x)) {
+      set_err("%s: q, k, v, weights and outputs need 16-byte alignment", who);
+      return SV_ERR_INVALID;
+    }
+  if (!strides_ok(a->q_row_stride, a->q_head_stride, 0) || !strides_ok(a->k_row_stride, a->k_head_stride, 0) ||
+      (c && !strides_ok(a->v_row_stride, a->v_head_stride, 0))) {
+    set_err("%s: strides need to be multiples of 8 elements", who);
+    return SV_ERR_INVALID;
+  }
+  sv::RopeParams r{};
+  r.rows = a->rows;
+  r.H = a->heads;
+  r.KV = a->kv_heads;
+  r.D = a->head_dim;
+  r.R = a->rotary;
+  r.bf16 = a->dtype == SV_BF16;
+  r.neighbours = a->interleaved != 0;
+  r.weight_f32 = a->weight_dtype == SV_F32;
+  r.eps = (float)a->eps;
+  r.inv_dim = 1.f / (float)a->head_dim;
+  r.q = a->q;
+  r.q_row = a->q_row_stride;
+  r.q_head = a->q_head_stride;
+  r.k = a->k;
+  r.k_row = a->k_row_stride;
+  r.k_head = a->k_head_stride;
+  r.v = a->v;
+  r.v_row = a->v_row_stride;
+  r.v_head = a->v_head_stride;
+  r.positions = a->positions;
+  r.inv_freq = a->inv_freq;
+  r.q_weight = a->q_weight;
+  r.k_weight = a->k_weight;
+  r.q_out = a->q_out;
+  r.k_out = a->k_out;
+  if (c) rope_cache(c, q, a->layer, a->slots, p, &r);
+  hipError_t e = sv::launch_rope(r, (hipStream_t)hip_stream);
   return e == hipSuccess ? SV_OK : hip_fail(who, e);
 }
 

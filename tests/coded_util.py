@@ -1,0 +1,70 @@
+"""Plain float64 forms of the 8-bit cache, of norms with rotation, and of attention over codes, for their tests."""
+import numpy as np
+import torch
+
+E4M3 = "e4m3"
+INT8 = "int8"
+
+
+def e4m3_values():
+    """What the 256 codes of the 8-bit floating type stand for: 1 sign, 4 exponent (bias 7) and 3 mantissa bits."""
+    out = np.empty(256)
+    for c in range(256):
+        e, m = (c >> 3) & 15, c & 7
+        v = np.ldexp(1 + m / 8, e - 7) if e else np.ldexp(m / 8, -6)
+        out[c] = np.nan if (c & 127) == 127 else (-v if c & 128 else v)
+    return out
+
+
+def quantise_ref(x, quant):
+    """Vectors along the last axis (a CPU tensor of a 16-bit type): codes as
+    uint8, scales as float32, and the values they stand for in float64.  A
+    float32 product or quotient is formed in float64 and rounded, which is the
+    same number (53 bits hold more than twice 24)."""
+    x = x.double().numpy()
+    top = np.abs(x).max(-1)
+    finite = np.isfinite(x).all(-1)
+    small = top < 2.0 ** -100
+    ok = finite & ~small
+    t = np.where(ok, top, 1.0)
+    if quant == E4M3:
+        n = np.ceil(np.log2(t / 448.0))
+        n = np.where(448.0 * np.exp2(n - 1) >= t, n - 1, n)
+        n = np.where(448.0 * np.exp2(n) < t, n + 1, n)
+        scale = np.exp2(n)
+        y = np.where(ok[..., None], x, 0) / scale[..., None]
+        a = np.abs(y)
+        step = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+        q = np.rint(a / step) * step                                       # to even: multiples of the step
+        mag = e4m3_values()[:127]
+        codes = np.searchsorted(mag, q)
+        assert (mag[codes] == q).all()
+        codes = codes | (np.signbit(y) << 7)
+        values = np.copysign(q, y)
+    else:
+        t32 = t.astype(np.float32)
+        scale = (t32 / np.float32(127)).astype(np.float64)
+        inv = np.float32(127) / t32
+        y = (np.where(ok[..., None], x, 0).astype(np.float32) * inv[..., None])
+        values = np.rint(y).astype(np.float64)
+        codes = values.astype(np.int8).view(np.uint8).astype(np.int64)
+    codes = np.where(ok[..., None], codes, 0)
+    scale = np.where(finite, np.where(small, 0.0, scale), np.nan).astype(np.float32)
+    values = np.where(ok[..., None], values, 0.0) * scale.astype(np.float64)[..., None]
+    return torch.from_numpy(codes.astype(np.uint8)), torch.from_numpy(scale), torch.from_numpy(values)
+
+
+def rope_ref(x, positions, inv_freq, weight=None, eps=1e-6, interleaved=False):
+    """[rows, heads, D] in float64, and next to each number the size of the pair it came from."""
+    y = x.double()
+    if weight is not None:
+        y = y / torch.sqrt(y.square().mean(-1, keepdim=True) + eps) * weight.double()
+    R = 2 * inv_freq.numel()
+    i = torch.arange(R // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + R // 2)
+    t = positions.double()[:, None, None] * inv_freq
+    out, size = y.clone(), y.abs()
+    out[..., a] = y[..., a] * t.cos() - y[..., b] * t.sin()
+    out[..., b] = y[..., b] * t.cos() + y[..., a] * t.sin()
+    size[..., a] = size[..., b] = y[..., a].abs() + y[..., b].abs()
+    return out, size
