@@ -689,6 +689,38 @@ int spec_verify_cache_read(const spec_verify_cache* cache, const spec_verify_cod
 /* sizeof(spec_verify_codes) as compiled into the library. */
 int64_t spec_verify_codes_size(void);
 
+/* ---- attention over a cache held in 8 bits --------------------------------------
+ * spec_verify_paged_attention with more than its own arguments say: options
+ * (NULL, or all zero: the call as it is).
+ *   codes     SV_CODES_E4M3 or SV_CODES_INT8: k and v of args are codes, their
+ *             strides count codes (multiples of 16); dtype is that of q and out
+ *   k_scale, v_scale   float, strides in elements for page and head (multiples
+ *             of 4), neighbouring tokens side by side, 16-byte aligned
+ * Scores are products of q and the codes, times the key's scale; the weights
+ * take the value's scale on before they are split in two bfloat16 (also for
+ * SV_F16: held to 2^-16 of themselves).  A scale or code that is not a number
+ * makes the rows that see it NaN, and no others.
+ * workspace: spec_verify_attention_options_workspace() bytes. */
+typedef struct spec_verify_attention_options {
+  int32_t codes;
+  const float* k_scale;
+  int64_t k_scale_page_stride;
+  int64_t k_scale_head_stride;
+  const float* v_scale;
+  int64_t v_scale_page_stride;
+  int64_t v_scale_head_stride;
+} spec_verify_attention_options;
+int spec_verify_paged_attention_options(const spec_verify_attention_args* args, const spec_verify_attention_options* options,
+                                        void* hip_stream);
+
+/* Bytes of workspace for a call with these sizes (pointers, strides and tables
+ * are not looked at), or SV_ERR_INVALID. */
+int64_t spec_verify_attention_options_workspace(const spec_verify_attention_args* args,
+                                                const spec_verify_attention_options* options);
+
+/* sizeof(spec_verify_attention_options) as compiled into the library. */
+int64_t spec_verify_attention_options_size(void);
+
 /* ---- norms and position rotation of queries and keys ---------------------------
  * What a layer does to its projections' rows before it attends, in one pass.
  * For each head's vector x of row r, a token at positions[r]:

@@ -502,10 +502,28 @@ def _cache_dtype(t, name, torch):
     raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
 
 
+def _code_options(k, v, k_scale, v_scale, dev, torch):
+    """The part of an attention call that says what 8-bit pages stand for."""
+    codes = {torch.float8_e4m3fn: SV_CODES_E4M3, torch.int8: SV_CODES_INT8}.get(k.dtype)
+    if codes is None or v.dtype != k.dtype:
+        raise TypeError(f"pages with scales are both float8_e4m3fn or both int8, got {k.dtype} and {v.dtype}")
+    strides = []
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is None or s.dtype != torch.float32 or s.shape != k.shape[:3]:
+            raise ValueError(f"{name} must be float32 {list(k.shape[:3])}")
+        if s.device != dev:
+            raise ValueError(f"{name} is on {s.device}, expected {dev}")
+        if s.stride(2) != 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+        strides += [s.data_ptr(), s.stride(0) if s.shape[0] > 1 else 0, s.stride(1) if s.shape[1] > 1 else 0]
+    return _lib.SpecVerifyAttentionOptions(codes, *strides)
+
+
 def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs=None, scale: Optional[float] = None,
-                    window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None, start=None) -> dict:
+                    window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None, start=None,
+                    k_scale=None, v_scale=None) -> dict:
     """Attention of a round's new tokens over a paged key-value cache
-    (spec_verify_paged_attention).
+    (spec_verify_paged_attention_options).
 
     ``q`` is [total_rows, heads, head_dim], bfloat16 or float16: for each
     sequence its ``num_draft`` + 1 rows, packed like a verify call's target
@@ -517,7 +535,9 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     num_draft - 1 + i, with ``window`` > 0 only the last ``window`` of them.
     ``scale`` defaults to head_dim ** -0.5.  ``start`` (int32 [batch], from
     ``PagedCache.reserve``): a sequence whose reserve was refused has no new
-    tokens, and gets NaN and a status.  Returns ``out`` like ``q``
+    tokens, and gets NaN and a status.  Pages of 8-bit codes (float8_e4m3fn or
+    int8) go with ``k_scale`` / ``v_scale`` (float32 [num_pages, kv_heads,
+    page_size], tokens side by side).  Returns ``out`` like ``q``
     (contiguous), ``lse`` (float32 [total_rows, heads]) and ``status`` (int32
     [batch]); what was not asked for is None."""
     import torch
@@ -529,8 +549,12 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     pages, KV, P, Dk = k_pages.shape
     if D != Dk:
         raise ValueError(f"q has head_dim {D}, the pages {Dk}")
-    if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
-        raise TypeError(f"q is {q.dtype}, the pages {k_pages.dtype} and {v_pages.dtype}")
+    if k_scale is None and v_scale is None:
+        if k_pages.dtype != q.dtype or v_pages.dtype != q.dtype:
+            raise TypeError(f"q is {q.dtype}, the pages {k_pages.dtype} and {v_pages.dtype}")
+        more = None
+    else:
+        more = _code_options(k_pages, v_pages, k_scale, v_scale, dev, torch)
     if not q.is_cuda or k_pages.device != dev or v_pages.device != dev:
         raise ValueError(f"q, k_pages and v_pages must be on one GPU, got {dev}, {k_pages.device} and {v_pages.device}")
     qs, ks, vs = q.stride(), k_pages.stride(), v_pages.stride()
@@ -554,10 +578,10 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         v_pages.data_ptr(), vs[0] if pages > 1 else 0, vs[1] if KV > 1 else 0, vs[2],
         page_table.data_ptr(), seq_len.data_ptr(), _ptr(seqs), num_draft.data_ptr(),
         D ** -0.5 if scale is None else float(scale), start=_ptr(start))
-    nbytes = lib.spec_verify_attention_workspace(ctypes.byref(a))
+    nbytes = lib.spec_verify_attention_options_workspace(a, more)
     if nbytes < 0:
         _check(int(nbytes))
-    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start):
+    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start, k_scale, v_scale):
         out = {
             "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
             "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,
@@ -566,7 +590,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         a.out, a.lse, a.status = out["out"].data_ptr(), _ptr(out["lse"]), _ptr(out["status"])
         a.workspace, a.workspace_bytes = ws.data_ptr(), nbytes
-        _check(lib.spec_verify_paged_attention(ctypes.byref(a), _queue(dev)))
+        _check(lib.spec_verify_paged_attention_options(a, more, _queue(dev)))
     return _for_caller(out, dev, stream)
 
 
@@ -805,6 +829,10 @@ class PagedCache:
         """``paged_attention`` of ``q`` over a layer of this cache."""
         if not 0 <= int(layer) < self.layers:
             raise ValueError(f"layer {layer} outside 0..{self.layers - 1}")
+        if self.quant is not None:
+            if q.dtype != self.dtype:
+                raise TypeError(f"q is {q.dtype}, the cache {self.dtype}")
+            kw.update(k_scale=self.k_scale[layer], v_scale=self.v_scale[layer])
         return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, num_draft, seqs=seqs, **kw)
 
     def commit(self, seqs, num_draft, accepted_len, stream=None, *, start=None):

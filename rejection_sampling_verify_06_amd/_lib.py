@@ -60,6 +60,7 @@ EXPORTED = (
     "spec_verify_cache_workspace", "spec_verify_cache_size",
     "spec_verify_coded_cache_reserve", "spec_verify_coded_cache_compact", "spec_verify_coded_cache_write",
     "spec_verify_cache_read", "spec_verify_codes_size", "spec_verify_qk_norm_rope", "spec_verify_rope_args_size",
+    "spec_verify_paged_attention_options", "spec_verify_attention_options_workspace", "spec_verify_attention_options_size",
 )
 SV_CACHE_MAX_SLOTS = 4096
 SV_LOGPROBS_MAX_TOP = 64
@@ -214,6 +215,18 @@ class SpecVerifyCodes(ctypes.Structure):
     ]
 
 
+class SpecVerifyAttentionOptions(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_int32),
+        ("k_scale", ctypes.c_void_p),
+        ("k_scale_page_stride", ctypes.c_int64),
+        ("k_scale_head_stride", ctypes.c_int64),
+        ("v_scale", ctypes.c_void_p),
+        ("v_scale_page_stride", ctypes.c_int64),
+        ("v_scale_head_stride", ctypes.c_int64),
+    ]
+
+
 class SpecVerifyRopeArgs(ctypes.Structure):
     _fields_ = [
         ("rows", ctypes.c_int64),
@@ -323,7 +336,12 @@ def load() -> ctypes.CDLL:
                         ("qk_norm_rope", [ctypes.POINTER(SpecVerifyRopeArgs), C, Q, P])):
         f = getattr(lib, "spec_verify_" + name)
         f.argtypes, f.restype = types, ctypes.c_int
-    for name, view in (("codes", SpecVerifyCodes), ("rope_args", SpecVerifyRopeArgs)):
+    A, O = ctypes.POINTER(SpecVerifyAttentionArgs), ctypes.POINTER(SpecVerifyAttentionOptions)
+    lib.spec_verify_paged_attention_options.argtypes = [A, O, P]
+    lib.spec_verify_paged_attention_options.restype = ctypes.c_int
+    lib.spec_verify_attention_options_workspace.argtypes = [A, O]
+    lib.spec_verify_attention_options_workspace.restype = i64
+    for name, view in (("codes", SpecVerifyCodes), ("rope_args", SpecVerifyRopeArgs), ("attention_options", SpecVerifyAttentionOptions)):
         f = getattr(lib, f"spec_verify_{name}_size")
         f.argtypes, f.restype = [], i64
         if f() != ctypes.sizeof(view):

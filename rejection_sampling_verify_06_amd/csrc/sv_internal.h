@@ -224,6 +224,22 @@ hipError_t launch_logprobs(const LogprobParams& p, hipStream_t st);
 constexpr int kAttnUnitKeys = 128;      // keys of a unit of work
 constexpr int kAttnPartBytes = 32;      // a block's record for the join
 
+// What a call with a shared prefix works out once, in its workspace: packed
+// rows and units of work as prefix sums, and each sequence's and group's keys.
+struct AttnPlan {
+  int32_t* bad;                     // [1] rows or groups do not add up
+  int32_t* rows;                    // [B + 1]
+  int32_t* units;                   // [B + 1]
+  int32_t* slot;                    // [B] -1: refused
+  int32_t* len;                     // [B]
+  int32_t* first;                   // [B] the prefix's length
+  int32_t* flags;                   // [B] status, pages looked at
+  int32_t* group_rows;              // [G + 1]
+  int32_t* group_units;             // [G + 1]
+  int32_t* group_slot;              // [G]
+  int32_t* group_len;               // [G]
+};
+
 struct AttnParams {
   int32_t B;
   int32_t total_rows;
@@ -253,9 +269,23 @@ struct AttnParams {
   int32_t* status;                  // or NULL
   float* parts;                     // [blocks][2] parts of 16 row_tiles * (head_dim + 2) floats
   void* desc;                       // [blocks] records
+  // codes: k and v are bytes, their strides too
+  const float* ks;                  // scales, neighbouring tokens side by side
+  const float* vs;
+  int64_t ks_page, ks_head, vs_page, vs_head;
+  // a shared prefix
+  int32_t G;                        // groups
+  const int32_t* groups;            // [G + 1] first sequence of each
+  const int32_t* prefix_len;        // [G]
+  AttnPlan plan;
+  float* state_o;                   // [total_rows][heads][head_dim]: what the prefix gives a row
+  float* state_m;                   // [total_rows][heads]: log2 of its sum of weights
 };
 
 hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_int8(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_join(const AttnParams& p, int stage, int tm, int W, hipStream_t st);
 
 // the paged cache's own operations (sv_cache.hip)
 constexpr int kCacheMaxSlots = 4096;

@@ -50,13 +50,18 @@ struct AttnShape {
 
 bool is_pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
-bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, AttnShape* s) {
+bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, const spec_verify_attention_options* o, AttnShape* s) {
   if (!a) {
     set_err("%s: args is NULL", who);
     return false;
   }
   if (a->dtype != SV_BF16 && a->dtype != SV_F16) {
     set_err("%s: dtype %d is neither SV_BF16 nor SV_F16", who, a->dtype);
+    return false;
+  }
+  const int32_t codes = o ? o->codes : SV_CODES_NONE;
+  if (codes != SV_CODES_NONE && codes != SV_CODES_E4M3 && codes != SV_CODES_INT8) {
+    set_err("%s: codes %d is none of SV_CODES_*", who, codes);
     return false;
   }
   if (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256) {
@@ -126,7 +131,7 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, At
   // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
   int per_cu = 1;
   if (a->head_dim == 64) per_cu = s->row_tiles == 1 ? 4 : 2;
-  else if (a->head_dim == 128 && avg > 48) per_cu = 2;
+  else if (a->head_dim == 128 && (avg > 48 || codes != SV_CODES_NONE)) per_cu = 2;
   s->blocks = (int)std::min<int64_t>(units, 256 * per_cu);
   s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
   return true;
@@ -317,17 +322,29 @@ int spec_verify_token_logprobs(const spec_verify_logprobs_args* a, void* hip_str
 
 int64_t spec_verify_attention_args_size(void) { return (int64_t)sizeof(spec_verify_attention_args); }
 
-int64_t spec_verify_attention_workspace(const spec_verify_attention_args* a) {
+int64_t spec_verify_attention_options_size(void) { return (int64_t)sizeof(spec_verify_attention_options); }
+
+int64_t spec_verify_attention_options_workspace(const spec_verify_attention_args* a, const spec_verify_attention_options* o) {
   AttnShape s;
-  if (!attention_sizes_ok("spec_verify_attention_workspace", a, &s)) return SV_ERR_INVALID;
+  if (!attention_sizes_ok("spec_verify_attention_workspace", a, o, &s)) return SV_ERR_INVALID;
   return s.blocks * s.part_bytes + (int64_t)s.blocks * sv::kAttnPartBytes;
 }
 
+int64_t spec_verify_attention_workspace(const spec_verify_attention_args* a) {
+  return spec_verify_attention_options_workspace(a, nullptr);
+}
+
 int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_stream) {
+  return spec_verify_paged_attention_options(a, nullptr, hip_stream);
+}
+
+int spec_verify_paged_attention_options(const spec_verify_attention_args* a, const spec_verify_attention_options* o,
+                                        void* hip_stream) {
   const char* who = "spec_verify_paged_attention";
   AttnShape s;
-  if (!attention_sizes_ok(who, a, &s)) return SV_ERR_INVALID;
+  if (!attention_sizes_ok(who, a, o, &s)) return SV_ERR_INVALID;
   if (a->batch == 0) return SV_OK;
+  const int32_t codes = o ? o->codes : SV_CODES_NONE;
   if (!a->q || !a->k || !a->v || !a->page_table || !a->seq_len || !a->num_draft || !a->out) {
     set_err("%s: q, k, v, page_table, seq_len, num_draft and out are required", who);
     return SV_ERR_INVALID;
@@ -341,6 +358,22 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
             "(a token's at most 2^24)", who);
     return SV_ERR_INVALID;
   }
+  if (codes != SV_CODES_NONE) {
+    for (int64_t x : {a->k_page_stride, a->k_head_stride, a->k_token_stride, a->v_page_stride, a->v_head_stride, a->v_token_stride})
+      if (x % 16) {
+        set_err("%s: strides of codes need to be multiples of 16", who);
+        return SV_ERR_INVALID;
+      }
+    if (!o->k_scale || !o->v_scale || !aligned16(o->k_scale) || !aligned16(o->v_scale)) {
+      set_err("%s: k_scale and v_scale (16-byte aligned) are required", who);
+      return SV_ERR_INVALID;
+    }
+    for (int64_t x : {o->k_scale_page_stride, o->k_scale_head_stride, o->v_scale_page_stride, o->v_scale_head_stride})
+      if (x < 0 || x % 4 || x > (int64_t)1 << 40) {
+        set_err("%s: strides of scales need to be multiples of 4", who);
+        return SV_ERR_INVALID;
+      }
+  }
   if (a->page_table_stride < a->max_pages || a->page_table_stride > INT32_MAX) {
     set_err("%s: page_table_stride %lld < max_pages %d", who, (long long)a->page_table_stride, a->max_pages);
     return SV_ERR_INVALID;
@@ -350,7 +383,7 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
     set_err("%s: scale %g (times log2 e) is not finite in 32 bits", who, a->scale);
     return SV_ERR_INVALID;
   }
-  const int64_t need = spec_verify_attention_workspace(a);
+  const int64_t need = spec_verify_attention_options_workspace(a, o);
   if (!a->workspace || !aligned16(a->workspace) || a->workspace_bytes < need) {
     set_err("%s: a 16-byte aligned workspace of %lld bytes is required, got %lld", who, (long long)need,
             (long long)a->workspace_bytes);
@@ -392,7 +425,17 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
   p.status = a->status;
   p.parts = static_cast<float*>(a->workspace);
   p.desc = static_cast<char*>(a->workspace) + s.blocks * s.part_bytes;
-  hipError_t e = sv::launch_attention(p, s.row_tiles, s.blocks, (hipStream_t)hip_stream);
+  if (codes != SV_CODES_NONE) {
+    p.ks = o->k_scale;
+    p.ks_page = o->k_scale_page_stride;
+    p.ks_head = o->k_scale_head_stride;
+    p.vs = o->v_scale;
+    p.vs_page = o->v_scale_page_stride;
+    p.vs_head = o->v_scale_head_stride;
+  }
+  hipError_t e = (codes == SV_CODES_E4M3   ? sv::launch_attention_e4m3
+                  : codes == SV_CODES_INT8 ? sv::launch_attention_int8
+                                           : sv::launch_attention)(p, s.row_tiles, s.blocks, (hipStream_t)hip_stream);
   if (e != hipSuccess) return hip_fail(who, e);
   return SV_OK;
 }

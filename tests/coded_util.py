@@ -68,3 +68,20 @@ def rope_ref(x, positions, inv_freq, weight=None, eps=1e-6, interleaved=False):
     out[..., b] = y[..., b] * t.cos() + y[..., a] * t.sin()
     size[..., a] = size[..., b] = y[..., a].abs() + y[..., b].abs()
     return out, size
+
+
+def make_coded_pages(L, P, KV, D, dtype, quant, seed, extra=3):
+    """serving_util.make_pages as codes: the pools on the GPU, and what they
+    stand for as float64 pools for serving_util.attention_ref.  What no token
+    fills holds codes that are no numbers and scales that are not finite."""
+    from . import serving_util as su
+    k, v, table, seq_len = su.make_pages(L, P, KV, D, dtype, seed, extra=extra)
+    out, ref = [], []
+    for t in (k, v):
+        codes, scale, values = quantise_ref(t.cpu(), quant)
+        empty = scale.isnan()
+        codes[empty] = 0x7F
+        scale[empty] = torch.tensor([torch.nan, torch.inf, -torch.inf, 0.0]).repeat(int(empty.sum()) // 4 + 1)[:int(empty.sum())]
+        out += [codes.cuda().view(torch.float8_e4m3fn if quant == E4M3 else torch.int8), scale.cuda()]
+        ref.append(values)
+    return out, ref, table, seq_len
