@@ -689,7 +689,7 @@ int spec_verify_cache_read(const spec_verify_cache* cache, const spec_verify_cod
 /* sizeof(spec_verify_codes) as compiled into the library. */
 int64_t spec_verify_codes_size(void);
 
-/* ---- attention over a cache held in 8 bits --------------------------------------
+/* ---- attention over a cache held in 8 bits, and over shared prefixes --------------
  * spec_verify_paged_attention with more than its own arguments say: options
  * (NULL, or all zero: the call as it is).
  *   codes     SV_CODES_E4M3 or SV_CODES_INT8: k and v of args are codes, their
@@ -700,6 +700,21 @@ int64_t spec_verify_codes_size(void);
  * take the value's scale on before they are split in two bfloat16 (also for
  * SV_F16: held to 2^-16 of themselves).  A scale or code that is not a number
  * makes the rows that see it NaN, and no others.
+ *   num_groups   0, or the number of groups of neighbouring sequences whose first
+ *             tokens are the same (forks of one sequence, for instance)
+ *   groups    [num_groups + 1] int32: group g is the sequences groups[g] ..
+ *             groups[g + 1] - 1, together 0 .. batch - 1 (a group may be empty)
+ *   prefix_len   [num_groups] int32: how many tokens its sequences share (0:
+ *             none); the new tokens are behind them
+ * The keys of a prefix are read once for all rows of its group, from the pages
+ * of the group's first sequence.  The result is that of the call without groups
+ * up to float32 roundings.  Pages that a prefix fills have to be the same pages in
+ * every page table of the group (a partly filled last one may be a copy): other
+ * ones set SV_ST_BAD_PAGE.  A prefix that a sequence does not have in front of
+ * its new tokens sets SV_ST_BAD_LENGTH for it; one that the group's first
+ * sequence does not have refuses the group.  Groups that do not add up set
+ * SV_ST_BAD_LAYOUT for every sequence.  Refused sequences' rows are NaN.  With
+ * groups window is 0, and five kernels are enqueued instead of two.
  * workspace: spec_verify_attention_options_workspace() bytes. */
 typedef struct spec_verify_attention_options {
   int32_t codes;
@@ -709,6 +724,9 @@ typedef struct spec_verify_attention_options {
   const float* v_scale;
   int64_t v_scale_page_stride;
   int64_t v_scale_head_stride;
+  int32_t num_groups;
+  const int32_t* groups;
+  const int32_t* prefix_len;
 } spec_verify_attention_options;
 int spec_verify_paged_attention_options(const spec_verify_attention_args* args, const spec_verify_attention_options* options,
                                         void* hip_stream);

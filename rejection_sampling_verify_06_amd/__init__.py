@@ -521,7 +521,7 @@ def _code_options(k, v, k_scale, v_scale, dev, torch):
 
 def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs=None, scale: Optional[float] = None,
                     window: int = 0, want_lse: bool = False, want_status: bool = True, stream=None, start=None,
-                    k_scale=None, v_scale=None) -> dict:
+                    k_scale=None, v_scale=None, groups=None, prefix_len=None) -> dict:
     """Attention of a round's new tokens over a paged key-value cache
     (spec_verify_paged_attention_options).
 
@@ -537,7 +537,15 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     ``PagedCache.reserve``): a sequence whose reserve was refused has no new
     tokens, and gets NaN and a status.  Pages of 8-bit codes (float8_e4m3fn or
     int8) go with ``k_scale`` / ``v_scale`` (float32 [num_pages, kv_heads,
-    page_size], tokens side by side).  Returns ``out`` like ``q``
+    page_size], tokens side by side).
+
+    Neighbouring sequences that share their first tokens (forks) are read once
+    for all of them with ``groups`` (int32 [groups + 1]: the first sequence of
+    each, and batch) and ``prefix_len`` (int32 [groups]: tokens shared, in front
+    of the new ones; 0: none).  The result is the same up to float32 roundings.  Pages
+    that a prefix fills are the same pages in every table of its group.
+
+    Returns ``out`` like ``q``
     (contiguous), ``lse`` (float32 [total_rows, heads]) and ``status`` (int32
     [batch]); what was not asked for is None."""
     import torch
@@ -555,6 +563,13 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
         more = None
     else:
         more = _code_options(k_pages, v_pages, k_scale, v_scale, dev, torch)
+    if groups is not None or prefix_len is not None:
+        if groups is None or prefix_len is None:
+            raise ValueError("groups and prefix_len go together")
+        _need(prefix_len, "prefix_len", (torch.int32,), torch, None, dev)
+        _need(groups, "groups", (torch.int32,), torch, prefix_len.numel() + 1, dev)
+        more = _lib.SpecVerifyAttentionOptions() if more is None else more
+        more.num_groups, more.groups, more.prefix_len = prefix_len.numel(), groups.data_ptr(), prefix_len.data_ptr()
     if not q.is_cuda or k_pages.device != dev or v_pages.device != dev:
         raise ValueError(f"q, k_pages and v_pages must be on one GPU, got {dev}, {k_pages.device} and {v_pages.device}")
     qs, ks, vs = q.stride(), k_pages.stride(), v_pages.stride()
@@ -581,7 +596,8 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     nbytes = lib.spec_verify_attention_options_workspace(a, more)
     if nbytes < 0:
         _check(int(nbytes))
-    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start, k_scale, v_scale):
+    with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start, k_scale, v_scale, groups,
+                    prefix_len):
         out = {
             "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
             "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,

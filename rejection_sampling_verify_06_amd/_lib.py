@@ -224,6 +224,9 @@ class SpecVerifyAttentionOptions(ctypes.Structure):
         ("v_scale", ctypes.c_void_p),
         ("v_scale_page_stride", ctypes.c_int64),
         ("v_scale_head_stride", ctypes.c_int64),
+        ("num_groups", ctypes.c_int32),
+        ("groups", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p),
     ]
 
 

@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_NAME = "libspec_verify.so"
 SOURCES = ["csrc/sv_kernels.hip", "csrc/sv_ngram.hip", "csrc/sv_stats.hip", "csrc/sv_filter.hip", "csrc/sv_noalloc.hip",
-           "csrc/sv_logprobs.hip", "csrc/sv_attention.hip", "csrc/sv_attention_e4m3.hip", "csrc/sv_attention_int8.hip", "csrc/sv_cache.hip", "csrc/sv_rope.hip", "csrc/sv_api.cpp", "csrc/sv_serving_api.cpp"]
+           "csrc/sv_logprobs.hip", "csrc/sv_attention.hip", "csrc/sv_attention_e4m3.hip", "csrc/sv_attention_int8.hip",
+           "csrc/sv_attention_shared.hip", "csrc/sv_attention_shared_e4m3.hip", "csrc/sv_attention_shared_int8.hip", "csrc/sv_cache.hip", "csrc/sv_rope.hip", "csrc/sv_api.cpp", "csrc/sv_serving_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -318,7 +318,7 @@ __device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, 
 }
 
 // S: one pass over everything a sequence has, or the stages of a shared prefix
-enum { kWholeSeq = 0, kPrefix = 1, kOwn = 2 };
+constexpr int kWholeSeq = kAttnWhole, kPrefix = kAttnPrefix, kOwn = kAttnOwn;
 
 // Stages of a shared prefix: rows and units of the groups or sequences come
 // from the plan (k_attention_plan), as prefix sums into shared memory.
@@ -341,7 +341,7 @@ __device__ __forceinline__ Extent plan_extent(const AttnParams& P, int S, int b)
     x.len = P.plan.group_len[b];
     x.first = 0;
   } else {
-    x.slot = P.plan.slot[b];
+    x.slot = P.plan.flags[b] ? -1 : P.plan.slot[b];
     x.len = P.plan.len[b];
     x.first = P.plan.first[b];
   }
@@ -855,6 +855,12 @@ hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
     case 256 * 8 + 1: return launch_one<BF, 256, 1, C, S>(p, W, st);
   }
   return hipErrorInvalidValue;
+}
+
+template <int C>
+hipError_t launch_shared(const AttnParams& p, int stage, int mt, int W, hipStream_t st) {
+  if (stage == kPrefix) return p.bf16 ? launch_type<true, C, kPrefix>(p, mt, W, st) : launch_type<false, C, kPrefix>(p, mt, W, st);
+  return p.bf16 ? launch_type<true, C, kOwn>(p, mt, W, st) : launch_type<false, C, kOwn>(p, mt, W, st);
 }
 
 }  // namespace

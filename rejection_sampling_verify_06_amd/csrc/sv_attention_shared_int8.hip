@@ -1,0 +1,13 @@
+// The stages of attention with shared prefixes over a paged cache of int8 codes,
+// for gfx950 (their kernel is in sv_attention_kernel.h, the plan in
+// sv_attention_shared.hip).
+
+#include "sv_attention_kernel.h"
+
+namespace sv {
+
+hipError_t launch_attention_shared_int8(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st) {
+  return launch_shared<codes::kInt8>(p, stage, row_tiles, blocks, st);
+}
+
+}  // namespace sv

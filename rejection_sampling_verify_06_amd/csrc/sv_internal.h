@@ -286,6 +286,12 @@ hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipS
 hipError_t launch_attention_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_int8(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_join(const AttnParams& p, int stage, int tm, int W, hipStream_t st);
+// a call with shared prefixes: the plan, then its two stages
+enum { kAttnWhole = 0, kAttnPrefix = 1, kAttnOwn = 2 };
+hipError_t launch_attention_plan(const AttnParams& p, int own_rows, int group_rows, hipStream_t st);
+hipError_t launch_attention_shared(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_shared_e4m3(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_shared_int8(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
 
 // the paged cache's own operations (sv_cache.hip)
 constexpr int kCacheMaxSlots = 4096;

@@ -50,7 +50,58 @@ struct AttnShape {
 
 bool is_pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
-bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, const spec_verify_attention_options* o, AttnShape* s) {
+// The layout of `rows` rows of `batch` sequences (or groups) each with up to all the keys that a page table holds.
+bool attention_shape(const char* who, const spec_verify_attention_args* a, int32_t codes, int32_t rows, int32_t batch, AttnShape* s) {
+  // A (sequence, key head)'s rows should fit one block's row tiles: every
+  // further block of tiles reads the keys again, at the same rate.  Tiles that
+  // a short sequence leaves empty cost registers and code, not products.  Only
+  // the sum of the rows is known here, so room is made for half again the
+  // average, or for all that one sequence can have.  32 sequences of 4096, 8
+  // key heads of 128: 4 rows with room for 16, 32, 48 95, 96, 97 us; 24 rows
+  // with 32, 48 97, 99 (ragged, 8 to 24 rows and 1024 to 8192 tokens: 127 and
+  // 134); 36 rows with 32, 48 114, 101.  One token of one sequence, 16 and 48 7
+  // and 10 us.  More than 48 rows of 128 do not fit the registers (64 rows: 2
+  // tiles twice 113 us, 3 tiles twice 182, 4 spilled 187), nor more than 16 of
+  // 256 (16 to 40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
+  // of 4096 with 8 heads of 64: 8 rows with room for 16, 32, 64 94, 96, 96 us,
+  // 64 rows with 64, 32 104, 153.
+  const int64_t group = a->heads / a->kv_heads;
+  const int64_t avg = ((int64_t)rows * group + batch - 1) / batch;
+  const int64_t room = std::min(avg + avg / 2, (int64_t)(rows - batch + 1) * group);
+  if (a->head_dim == 256 || room <= 16) s->row_tiles = 1;
+  else if (room <= 32 || (a->head_dim == 128 && avg > 48)) s->row_tiles = 2;
+  else s->row_tiles = a->head_dim == 128 ? 3 : 4;
+  const int64_t tm = 16 * s->row_tiles;
+  const int64_t keys = (int64_t)a->max_pages * a->page_size;
+  const int64_t units = ((int64_t)rows * group / tm + batch) * a->kv_heads *
+                        ((keys + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
+  if (units > INT32_MAX) {
+    set_err("%s: %lld units of work: batch, heads and max_pages are too large together", who, (long long)units);
+    return false;
+  }
+  // One block per CU keeps enough reads in flight for heads of 128 and 256 and
+  // leaves the fewest parts to join (32 sequences of 4096 with 24 rows of 128:
+  // 97 + 4 us, with two 101 + 9; ragged 126 + 6 and 128 + 8, with four 132 +
+  // 10); heads of 64, and tiles that read the keys again, want two (64
+  // sequences of 4096 with 8 heads of 64: 96 and 94 us; 64 rows of 128: 156 and
+  // 113).  One row tile of 64 leaves room for four, which hide each other's
+  // changes from tile to tile (256 ragged sequences of 125 to 1000 tokens, 16
+  // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
+  int per_cu = 1;
+  if (a->head_dim == 64) per_cu = s->row_tiles == 1 ? 4 : 2;
+  else if (a->head_dim == 128 && (avg > 48 || codes != SV_CODES_NONE)) per_cu = 2;
+  s->blocks = (int)std::min<int64_t>(units, 256 * per_cu);
+  s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
+  return true;
+}
+
+// The layout of a call: its sequences', and its shared prefixes'.
+struct AttnLayout {
+  AttnShape own, prefix;
+  int32_t groups;
+};
+
+bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, const spec_verify_attention_options* o, AttnLayout* s) {
   if (!a) {
     set_err("%s: args is NULL", who);
     return false;
@@ -90,51 +141,23 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, co
             (long long)a->num_pages, a->slots, a->max_pages);
     return false;
   }
-  if (a->batch == 0) {
-    *s = AttnShape{1, 1, 0};
-    return true;
-  }
-  // A (sequence, key head)'s rows should fit one block's row tiles: every
-  // further block of tiles reads the keys again, at the same rate.  Tiles that
-  // a short sequence leaves empty cost registers and code, not products.  Only
-  // the sum of the rows is known here, so room is made for half again the
-  // average, or for all that one sequence can have.  32 sequences of 4096, 8
-  // key heads of 128: 4 rows with room for 16, 32, 48 95, 96, 97 us; 24 rows
-  // with 32, 48 97, 99 (ragged, 8 to 24 rows and 1024 to 8192 tokens: 127 and
-  // 134); 36 rows with 32, 48 114, 101.  One token of one sequence, 16 and 48 7
-  // and 10 us.  More than 48 rows of 128 do not fit the registers (64 rows: 2
-  // tiles twice 113 us, 3 tiles twice 182, 4 spilled 187), nor more than 16 of
-  // 256 (16 to 40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
-  // of 4096 with 8 heads of 64: 8 rows with room for 16, 32, 64 94, 96, 96 us,
-  // 64 rows with 64, 32 104, 153.
-  const int64_t group = a->heads / a->kv_heads;
-  const int64_t avg = (a->total_rows * group + a->batch - 1) / a->batch;
-  const int64_t room = std::min(avg + avg / 2, (int64_t)(a->total_rows - a->batch + 1) * group);
-  if (a->head_dim == 256 || room <= 16) s->row_tiles = 1;
-  else if (room <= 32 || (a->head_dim == 128 && avg > 48)) s->row_tiles = 2;
-  else s->row_tiles = a->head_dim == 128 ? 3 : 4;
-  const int64_t tm = 16 * s->row_tiles;
-  const int64_t keys = (int64_t)a->max_pages * a->page_size;
-  const int64_t units = (a->total_rows * group / tm + a->batch) * a->kv_heads *
-                        ((keys + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
-  if (units > INT32_MAX) {
-    set_err("%s: %lld units of work: batch, heads and max_pages are too large together", who, (long long)units);
+  const int32_t groups = o ? o->num_groups : 0;
+  if (groups < 0 || groups > a->batch) {
+    set_err("%s: num_groups %d outside 0..batch", who, groups);
     return false;
   }
-  // One block per CU keeps enough reads in flight for heads of 128 and 256 and
-  // leaves the fewest parts to join (32 sequences of 4096 with 24 rows of 128:
-  // 97 + 4 us, with two 101 + 9; ragged 126 + 6 and 128 + 8, with four 132 +
-  // 10); heads of 64, and tiles that read the keys again, want two (64
-  // sequences of 4096 with 8 heads of 64: 96 and 94 us; 64 rows of 128: 156 and
-  // 113).  One row tile of 64 leaves room for four, which hide each other's
-  // changes from tile to tile (256 ragged sequences of 125 to 1000 tokens, 16
-  // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
-  int per_cu = 1;
-  if (a->head_dim == 64) per_cu = s->row_tiles == 1 ? 4 : 2;
-  else if (a->head_dim == 128 && (avg > 48 || codes != SV_CODES_NONE)) per_cu = 2;
-  s->blocks = (int)std::min<int64_t>(units, 256 * per_cu);
-  s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
-  return true;
+  if (groups > 0 && a->window > 0) {
+    set_err("%s: a window (%d) hides the prefix that groups share; call without groups", who, a->window);
+    return false;
+  }
+  s->groups = groups;
+  s->prefix = AttnShape{1, 0, 0};
+  if (a->batch == 0) {
+    s->own = AttnShape{1, 1, 0};
+    return true;
+  }
+  if (groups > 0 && !attention_shape(who, a, codes, a->total_rows, groups, &s->prefix)) return false;
+  return attention_shape(who, a, codes, a->total_rows, a->batch, &s->own);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -144,6 +167,38 @@ bool strides_ok(int64_t a, int64_t b, int64_t c) {
   for (int64_t x : {a, b, c})
     if (x < 0 || x % 8 || x > (int64_t)1 << 40) return false;
   return true;
+}
+
+// Where a call's parts, records and (with groups) its plan and state lie in its
+// workspace; returns the bytes.  The stages run one after the other and share
+// the parts and records.
+int64_t attention_workspace(const spec_verify_attention_args* a, const AttnLayout& l, char* base, sv::AttnParams* p) {
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    char* x = base + at;
+    at += bytes;
+    return x;
+  };
+  auto ints = [&](int64_t n) { return reinterpret_cast<int32_t*>(take((int64_t)sv::align_up((size_t)n * 4, 16))); };
+  p->parts = reinterpret_cast<float*>(take(std::max(l.own.blocks * l.own.part_bytes, l.prefix.blocks * l.prefix.part_bytes)));
+  p->desc = take((int64_t)std::max(l.own.blocks, l.prefix.blocks) * sv::kAttnPartBytes);
+  if (l.groups == 0) return at;
+  const int64_t B = a->batch, G = l.groups, rows = (int64_t)a->total_rows * a->heads;
+  sv::AttnPlan& n = p->plan;
+  n.bad = ints(1);
+  n.rows = ints(B + 1);
+  n.units = ints(B + 1);
+  n.slot = ints(B);
+  n.len = ints(B);
+  n.first = ints(B);
+  n.flags = ints(B);
+  n.group_rows = ints(G + 1);
+  n.group_units = ints(G + 1);
+  n.group_slot = ints(G);
+  n.group_len = ints(G);
+  p->state_m = reinterpret_cast<float*>(ints(rows));
+  p->state_o = reinterpret_cast<float*>(take(rows * a->head_dim * 4));
+  return at;
 }
 
 // workspace of a cache: the list's length, the ids, the list
@@ -325,9 +380,10 @@ int64_t spec_verify_attention_args_size(void) { return (int64_t)sizeof(spec_veri
 int64_t spec_verify_attention_options_size(void) { return (int64_t)sizeof(spec_verify_attention_options); }
 
 int64_t spec_verify_attention_options_workspace(const spec_verify_attention_args* a, const spec_verify_attention_options* o) {
-  AttnShape s;
-  if (!attention_sizes_ok("spec_verify_attention_workspace", a, o, &s)) return SV_ERR_INVALID;
-  return s.blocks * s.part_bytes + (int64_t)s.blocks * sv::kAttnPartBytes;
+  AttnLayout l;
+  if (!attention_sizes_ok("spec_verify_attention_workspace", a, o, &l)) return SV_ERR_INVALID;
+  sv::AttnParams p{};
+  return attention_workspace(a, l, nullptr, &p);
 }
 
 int64_t spec_verify_attention_workspace(const spec_verify_attention_args* a) {
@@ -341,8 +397,8 @@ int spec_verify_paged_attention(const spec_verify_attention_args* a, void* hip_s
 int spec_verify_paged_attention_options(const spec_verify_attention_args* a, const spec_verify_attention_options* o,
                                         void* hip_stream) {
   const char* who = "spec_verify_paged_attention";
-  AttnShape s;
-  if (!attention_sizes_ok(who, a, o, &s)) return SV_ERR_INVALID;
+  AttnLayout l;
+  if (!attention_sizes_ok(who, a, o, &l)) return SV_ERR_INVALID;
   if (a->batch == 0) return SV_OK;
   const int32_t codes = o ? o->codes : SV_CODES_NONE;
   if (!a->q || !a->k || !a->v || !a->page_table || !a->seq_len || !a->num_draft || !a->out) {
@@ -356,6 +412,10 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
       a->v_token_stride > 1 << 24) {
     set_err("%s: q, k, v and out need 16-byte alignment, and strides that are multiples of 8 elements "
             "(a token's at most 2^24)", who);
+    return SV_ERR_INVALID;
+  }
+  if (l.groups > 0 && (!o->groups || !o->prefix_len)) {
+    set_err("%s: groups and prefix_len are required for num_groups %d", who, l.groups);
     return SV_ERR_INVALID;
   }
   if (codes != SV_CODES_NONE) {
@@ -423,8 +483,7 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
   p.out = a->out;
   p.lse = a->lse;
   p.status = a->status;
-  p.parts = static_cast<float*>(a->workspace);
-  p.desc = static_cast<char*>(a->workspace) + s.blocks * s.part_bytes;
+  attention_workspace(a, l, static_cast<char*>(a->workspace), &p);
   if (codes != SV_CODES_NONE) {
     p.ks = o->k_scale;
     p.ks_page = o->k_scale_page_stride;
@@ -433,9 +492,23 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
     p.vs_page = o->v_scale_page_stride;
     p.vs_head = o->v_scale_head_stride;
   }
-  hipError_t e = (codes == SV_CODES_E4M3   ? sv::launch_attention_e4m3
-                  : codes == SV_CODES_INT8 ? sv::launch_attention_int8
-                                           : sv::launch_attention)(p, s.row_tiles, s.blocks, (hipStream_t)hip_stream);
+  const hipStream_t st = (hipStream_t)hip_stream;
+  hipError_t e;
+  if (l.groups == 0) {
+    e = (codes == SV_CODES_E4M3   ? sv::launch_attention_e4m3
+         : codes == SV_CODES_INT8 ? sv::launch_attention_int8
+                                  : sv::launch_attention)(p, l.own.row_tiles, l.own.blocks, st);
+  } else {
+    p.G = l.groups;
+    p.groups = o->groups;
+    p.prefix_len = o->prefix_len;
+    auto stage = codes == SV_CODES_E4M3   ? sv::launch_attention_shared_e4m3
+                 : codes == SV_CODES_INT8 ? sv::launch_attention_shared_int8
+                                          : sv::launch_attention_shared;
+    e = sv::launch_attention_plan(p, 16 * l.own.row_tiles, 16 * l.prefix.row_tiles, st);
+    if (e == hipSuccess) e = stage(p, sv::kAttnPrefix, l.prefix.row_tiles, l.prefix.blocks, st);
+    if (e == hipSuccess) e = stage(p, sv::kAttnOwn, l.own.row_tiles, l.own.blocks, st);
+  }
   if (e != hipSuccess) return hip_fail(who, e);
   return SV_OK;
 }

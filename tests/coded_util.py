@@ -85,3 +85,60 @@ def make_coded_pages(L, P, KV, D, dtype, quant, seed, extra=3):
         out += [codes.cuda().view(torch.float8_e4m3fn if quant == E4M3 else torch.int8), scale.cuda()]
         ref.append(values)
     return out, ref, table, seq_len
+
+
+def make_shared(groups, P, KV, D, dtype, quant, seed, extra=3):
+    """Sequences that were forked off their group's prefix: groups is a list of
+    (prefix length, [own tokens of each member]).  Whole pages of a prefix are
+    shared, a partly filled last one is copied for every member but the first.
+    Returns pools (k, k_scale, v, v_scale; scales None without quant), float64
+    pools, page_table, seq_len, groups and prefix_len."""
+    g = torch.Generator().manual_seed(seed)
+    tables, copies, fill, n = [], [], [], 0
+    for prefix, own in groups:
+        whole = list(range(n, n + prefix // P))
+        n += len(whole)
+        for m, o in enumerate(own):
+            L = prefix + o
+            mine = list(range(n, n + -(-L // P) - len(whole)))
+            n += len(mine)
+            if prefix % P and m:
+                copies.append((lead, mine[0], prefix % P))
+            elif prefix % P:
+                lead = mine[0]
+            tables.append(whole + mine)
+            fill.append((tables[-1][-1] if L % P else None, L % P))
+    total = n + extra
+    ids = torch.randperm(total, generator=g)
+    pools = []
+    for _ in range(2):
+        x = torch.randn(total, KV, P, D, generator=g).to(dtype)
+        for src, dst, c in copies:
+            x[dst, :, :c] = x[src, :, :c]
+        for page, c in fill:
+            if page is not None:
+                x[page, :, c:] = torch.nan
+        x[n:] = torch.nan
+        out = torch.empty_like(x)
+        out[ids] = x
+        pools.append(out)
+    width = max(len(t) for t in tables)
+    table = torch.full((len(tables), max(width, 1)), -1, dtype=torch.int32)
+    for b, t in enumerate(tables):
+        table[b, :len(t)] = ids[torch.tensor(t, dtype=torch.int64)].to(torch.int32)
+    dev, ref = [], []
+    for x in pools:
+        if quant is None:
+            dev += [x.cuda(), None]
+            ref.append(x.double())
+        else:
+            codes, scale, values = quantise_ref(x, quant)
+            codes[scale.isnan()] = 0x7F
+            dev += [codes.cuda().view(torch.float8_e4m3fn if quant == E4M3 else torch.int8), scale.cuda()]
+            ref.append(values)
+    first = np.cumsum([0] + [len(own) for _, own in groups])
+    L = [p + o for p, own in groups for o in own]
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32).cuda()
+    return dev, ref, table.cuda(), i32(L), i32(first.tolist()), i32([p for p, _ in groups])

@@ -105,3 +105,45 @@ def test_python_checks_before_the_library():
         sv.qk_norm_rope(x[0], x, torch.zeros(2, dtype=torch.int32), f)
     with pytest.raises(ValueError):
         sv.PagedCache(1, 8, 16, 2, 64, 2, 4, quant="e5m2")
+
+
+def _attn(_lib, **kw):
+    a = _lib.SpecVerifyAttentionArgs(batch=2, total_rows=3, heads=4, kv_heads=2, head_dim=64, dtype=_lib.SV_BF16, page_size=16, window=0, num_pages=32,
+                                     slots=2, max_pages=8, page_table_stride=8, q=4096, q_row_stride=256, q_head_stride=64, k=4096, k_page_stride=2048,
+                                     k_head_stride=1024, k_token_stride=64, v=4096, v_page_stride=2048, v_head_stride=1024, v_token_stride=64,
+                                     page_table=4096, seq_len=4096, num_draft=4096, scale=0.125, out=4096, workspace=4096, workspace_bytes=0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _options(_lib, **kw):
+    o = _lib.SpecVerifyAttentionOptions(codes=_lib.SV_CODES_INT8, k_scale=4096, k_scale_page_stride=32, k_scale_head_stride=16, v_scale=4096,
+                                        v_scale_page_stride=32, v_scale_head_stride=16, num_groups=1, groups=4096, prefix_len=4096)
+    for k, v in kw.items():
+        setattr(o, k, v)
+    return o
+
+
+def test_attention_options_reject_bad_arguments():
+    """All but the workspace is in order, which is asked for last."""
+    _lib, lib = _lib_loaded()
+
+    def call(o, **kw):
+        a = _attn(_lib, **kw)
+        assert lib.spec_verify_paged_attention_options(_ref(a), _ref(o), None) == _lib.SV_ERR_INVALID
+        return lib.spec_verify_last_error().decode()
+
+    assert "workspace" in call(_options(_lib)) and "workspace" in call(_options(_lib, codes=0, k_scale=None)) and "workspace" in call(None)
+    for o, a, what in ((dict(codes=3), {}, "codes"), (dict(codes=-1), {}, "codes"), (dict(k_scale=None), {}, "k_scale"), (dict(v_scale=4104), {}, "v_scale"),
+                       (dict(k_scale_page_stride=30), {}, "scales"), (dict(v_scale_head_stride=-4), {}, "scales"),
+                       ({}, dict(k_token_stride=72), "codes"), ({}, dict(v_page_stride=8), "codes"), (dict(num_groups=-1), {}, "num_groups"),
+                       (dict(num_groups=3), {}, "num_groups"), ({}, dict(window=5), "window"), (dict(groups=None), {}, "groups"),
+                       (dict(prefix_len=None), {}, "prefix_len")):
+        assert what in call(_options(_lib, **o), **a), (o, a)
+    plain = lib.spec_verify_attention_workspace(_ref(_attn(_lib)))
+    assert plain == lib.spec_verify_attention_options_workspace(_ref(_attn(_lib)), None) > 0
+    shared = lib.spec_verify_attention_options_workspace(_ref(_attn(_lib)), _ref(_options(_lib)))
+    assert shared >= 3 * 4 * (64 + 1) * 4 + 2 * 6 * 4                       # the state alone
+    assert lib.spec_verify_attention_options_workspace(_ref(_attn(_lib)), _ref(_options(_lib, num_groups=5))) == _lib.SV_ERR_INVALID
+    assert lib.spec_verify_paged_attention_options(_ref(_attn(_lib, batch=0, total_rows=0)), _ref(_options(_lib, num_groups=0)), None) == _lib.SV_OK
