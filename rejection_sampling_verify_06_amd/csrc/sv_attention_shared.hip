@@ -11,7 +11,7 @@
 //   own      each sequence's tokens behind the prefix, starting from what the
 //            prefix left for its rows; the parts' join
 
-#include "sv_attention_kernel.h"
+#include "sv_prefix.h"
 
 namespace sv {
 
@@ -221,6 +221,7 @@ hipError_t launch_attention_plan(const AttnParams& p, int own_rows, int group_ro
 }
 
 hipError_t launch_attention_shared(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st) {
+  if (stage == kPrefix && row_tiles == kAttnManyRows) return launch_prefix_rows<codes::kNone>(p, blocks, st);
   return launch_shared<codes::kNone>(p, stage, row_tiles, blocks, st);
 }
 

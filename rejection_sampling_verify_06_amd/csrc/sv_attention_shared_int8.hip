@@ -2,11 +2,12 @@
 // for gfx950 (their kernel is in sv_attention_kernel.h, the plan in
 // sv_attention_shared.hip).
 
-#include "sv_attention_kernel.h"
+#include "sv_prefix.h"
 
 namespace sv {
 
 hipError_t launch_attention_shared_int8(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st) {
+  if (stage == kPrefix && row_tiles == kAttnManyRows) return launch_prefix_rows<codes::kInt8>(p, blocks, st);
   return launch_shared<codes::kInt8>(p, stage, row_tiles, blocks, st);
 }
 

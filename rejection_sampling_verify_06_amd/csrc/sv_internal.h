@@ -286,7 +286,10 @@ hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipS
 hipError_t launch_attention_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_int8(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_join(const AttnParams& p, int stage, int tm, int W, hipStream_t st);
-// a call with shared prefixes: the plan, then its two stages
+// a call with shared prefixes: the plan, then its two stages; the first with kAttnManyRows for
+// row_tiles by the kernel for many rows
+constexpr int kAttnManyRows = 0;
+constexpr int kAttnPrefixRows = 128;    // rows of its tiles
 enum { kAttnWhole = 0, kAttnPrefix = 1, kAttnOwn = 2 };
 hipError_t launch_attention_plan(const AttnParams& p, int own_rows, int group_rows, hipStream_t st);
 hipError_t launch_attention_shared(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);

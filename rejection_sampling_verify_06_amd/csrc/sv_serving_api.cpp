@@ -156,7 +156,17 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, co
     s->own = AttnShape{1, 1, 0};
     return true;
   }
-  if (groups > 0 && !attention_shape(who, a, codes, a->total_rows, groups, &s->prefix)) return false;
+  if (groups > 0) {
+    if (!attention_shape(who, a, codes, a->total_rows, groups, &s->prefix)) return false;
+    const int64_t avg = (int64_t)a->total_rows * (a->heads / a->kv_heads) / groups;
+    if (avg > 48) {
+      const int64_t units = ((int64_t)a->total_rows * (a->heads / a->kv_heads) / sv::kAttnPrefixRows + groups) * a->kv_heads *
+                            (((int64_t)a->max_pages * a->page_size + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
+      s->prefix.row_tiles = sv::kAttnManyRows;
+      s->prefix.blocks = (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : a->head_dim == 128 ? 512 : 768);
+      s->prefix.part_bytes = 2 * (int64_t)sv::kAttnPrefixRows * (a->head_dim + 2) * 4;
+    }
+  }
   return attention_shape(who, a, codes, a->total_rows, a->batch, &s->own);
 }
 
@@ -505,7 +515,7 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
     auto stage = codes == SV_CODES_E4M3   ? sv::launch_attention_shared_e4m3
                  : codes == SV_CODES_INT8 ? sv::launch_attention_shared_int8
                                           : sv::launch_attention_shared;
-    e = sv::launch_attention_plan(p, 16 * l.own.row_tiles, 16 * l.prefix.row_tiles, st);
+    e = sv::launch_attention_plan(p, 16 * l.own.row_tiles, l.prefix.row_tiles == sv::kAttnManyRows ? sv::kAttnPrefixRows : 16 * l.prefix.row_tiles, st);
     if (e == hipSuccess) e = stage(p, sv::kAttnPrefix, l.prefix.row_tiles, l.prefix.blocks, st);
     if (e == hipSuccess) e = stage(p, sv::kAttnOwn, l.own.row_tiles, l.own.blocks, st);
   }
