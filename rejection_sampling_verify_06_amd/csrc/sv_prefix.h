@@ -50,14 +50,33 @@ __device__ __forceinline__ float pair_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Where 16-byte piece c of key r lies among the pieces of the staged keys.
+// Piece c of key r lies at c ^ k_turn(r) among the row's 16-byte pieces, and of a value at c ^ v_turn(r).
 template <int D>
-__device__ __forceinline__ int k_piece(int r, int c) {
-  return r * (D / 8) + (c ^ (D == 64 ? (r >> 1) & 7 : r & 15));
+__device__ __forceinline__ int k_turn(int r) {
+  return D == 64 ? (r >> 1) & 7 : r & 15;
 }
 template <int D>
-__device__ __forceinline__ int v_piece(int r, int c) {
-  return r * (D / 8) + (c ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2));
+__device__ __forceinline__ int v_turn(int r) {
+  return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+}
+
+// 16 bytes a lane from memory to the wave's 1 KB of shared memory at `to`.  Not
+// the builtin: next to it the compiler waits for all such loads before it reads
+// any shared memory, also the half that they do not write.  loads_done() comes
+// before the barrier behind which they are read.
+__device__ __forceinline__ void load_lds(const char* base, uint32_t offset, const u32x4* to) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u32x4*)to;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)at)), "v"(offset), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// two floats as the sum of two pairs of 16-bit numbers
+template <bool BF>
+__device__ __forceinline__ void split16(float a, float b, uint32_t* hi, uint32_t* lo) {
+  uint32_t x = pack16<BF>(a, b);
+  asm("" : "+v"(x));                             // or the compiler rounds a once more for its own half
+  *hi = x;
+  *lo = pack16<BF>(a - lo16<BF>(x), b - hi16<BF>(x));
 }
 
 }  // namespace
@@ -71,7 +90,7 @@ template <int D>
 constexpr int kPfKeys = D == 256 ? 32 : 64;      // keys staged at a time
 
 template <bool BF, int D, int C>
-__global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : D == 128 ? 2 : 3) k_prefix(AttnParams P) {
+__global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnParams P) {
   constexpr bool PB = BF || C != codes::kNone;   // the second product's type
   constexpr int ES = C != codes::kNone ? 1 : 2;
   constexpr int KT = kPfKeys<D>;
@@ -89,10 +108,34 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : D == 128 ? 2 : 3) k
   __shared__ float kscale[2][KT], vscale[2][KT];
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = uni(t / kWave);
   const int h = lane >> 5, col = lane & 31;
+  // Where a lane reads: piece 2 i + h of key col, at 32 i ^ this; and of four
+  // values the 16 numbers around its own, 4 (lane & 3) .. + 3 of 16 ((lane >> 4)
+  // & 1) .. + 15 of key 4 h + ((lane >> 2) & 3), at 64 j ^ this for number 32 j on.
+  const int vkey = 4 * h + ((lane >> 2) & 3), vd = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const char* kbase = (const char*)&ksh[0][0] + col * (2 * D);
+  char* vbase = (char*)&vsh[0][0] + vkey * (2 * D);
+  const int koff = 16 * (h ^ k_turn<D>(col)), voff = (16 * ((vd >> 3) ^ v_turn<D>(vkey))) | (2 * (vd & 7));
+  // A wave brings (part of) 16 keys, which lie in one page: what a lane's pieces
+  // add to the place of the first, and where they begin among the staged ones.
+  constexpr int GW = kPfWaves / (KT / 16);       // waves that share 16 keys
+  const int grp = wv / GW, piece0 = grp * (16 * CPR) + (wv % GW) * (NI * kWave);
+  uint32_t klane[NI], vlane[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int key = (piece0 + i * kWave + lane) / CPR, c = lane % CPR;
+    klane[i] = ES * (uint32_t)(key & 15) * (uint32_t)P.k_tok + 16 * (C == codes::kNone ? c ^ k_turn<D>(key) : c);
+    vlane[i] = ES * (uint32_t)(key & 15) * (uint32_t)P.v_tok + 16 * (C == codes::kNone ? c ^ v_turn<D>(key) : c);
+  }
+  // scalar instructions are a quarter of the loop's: 32-bit strides (the host has seen to it), and one place for K and V alike
+  const uint32_t k_page = (uint32_t)(ES * P.k_page), k_tok = (uint32_t)(ES * P.k_tok);
+  const uint32_t v_page = (uint32_t)(ES * P.v_page), v_tok = (uint32_t)(ES * P.v_tok);
+  const bool alike = k_page == v_page && k_tok == v_tok;
   load_plan(P, kPrefix, rows, units);
   Part* desc = reinterpret_cast<Part*>(P.desc);
   const uint32_t U = (uint32_t)uni((int)units[P.G]), W = min((uint32_t)gridDim.x, U);
-  const uint32_t w = blockIdx.x;
+  // Neighbouring ranges on one die: blocks go to the eight dies in turn
+  const uint32_t per_die = gridDim.x / 8;
+  const uint32_t w = U >= gridDim.x && gridDim.x % 8 == 0 ? blockIdx.x % 8 * per_die + blockIdx.x / 8 : blockIdx.x;
   if (w >= W) {
     if (t == 0) desc[w].first_unit = -1;
     return;
@@ -113,7 +156,8 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : D == 128 ? 2 : 3) k
     const uint32_t rel = u - (uint32_t)uni((int)units[gi]);
     const int seg = (int)(rel / (uint32_t)nblk), b0 = (int)(rel - (uint32_t)seg * nblk);
     const int b1 = (int)min((uint32_t)nblk, b0 + (u_end - u));
-    const int mb = seg / P.kv_heads, head = seg - mb * P.kv_heads;
+    const int tiles = (n * P.group + TM - 1) / TM;
+    const int head = seg / tiles, mb = seg - head * tiles;
     if (first_part && t == 0) {
       Part d;
       d.first_unit = b0 > 0 ? (int)(u - b0) : -1;
@@ -148,91 +192,124 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : D == 128 ? 2 : 3) k
       for (int i = 0; i < 16; ++i) o[j][i] = 0.f;
     float mx = -INFINITY, ls = 0.f;
     bool bad = slot < 0;
-    typedef const __attribute__((address_space(4))) int32_t* Names;
-    const Names table = (Names)(uintptr_t)(P.table + (int64_t)max(slot, 0) * P.table_stride);
+    const int32_t* table = P.table + (int64_t)max(slot, 0) * P.table_stride;
     const int pmask = (1 << P.page_log2) - 1;
-    const int c0 = t % CPR;
-    u32x4 kr[NI], vr[NI];
-    float scr = 0.f;                             // a scale: thread k brings that of key k, KT + k of value k
-    int id[NI];
-    // piece i of this thread is one of 16 keys of one page: those from 16 group(i) on
-    auto group = [&](int i) { return (i * kPfThreads + wv * kWave) / (16 * CPR); };
+    const char* khead = (const char*)P.k + ES * (int64_t)head * P.k_head;
+    const char* vhead = (const char*)P.v + ES * (int64_t)head * P.v_head;
+    u32x4 kr[NI], vr[NI];                        // codes on their way
+    float scr = 0.f;                             // and a scale: of key lane & 15 of the wave's, values' from lane 16 on
+    int id = 0;
+    // by a vector load: with a scalar one under way each wait for shared memory is one for everything
     auto names = [&](int pos) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) id[i] = table[min(pos + 16 * group(i), len - 1) >> P.page_log2];
+      int i = min(pos + 16 * grp, len - 1) >> P.page_log2;
+      asm("" : "+v"(i));
+      id = table[i];
     };
-    auto load = [&](int pos) {
+    // 16-bit keys go straight to shared memory, 1 KB a wave at a time: the lane
+    // whose place is piece c of a row brings the piece that belongs there
+    auto load = [&](int buf, int pos) {
+      const int name = uni(id);
+      const bool out = (unsigned)name >= (unsigned)P.num_pages;
+      bad |= out;
+      const uint32_t page = out ? 0u : (uint32_t)name, tok = (uint32_t)((pos + 16 * grp) & pmask);
+      const char* kp = khead + ((uint64_t)page * k_page + tok * k_tok);
+      const char* vp = alike ? vhead + (kp - khead) : vhead + ((uint64_t)page * v_page + tok * v_tok);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const bool out = (unsigned)id[i] >= (unsigned)P.num_pages;
-        bad |= out;
-        const int64_t page = out ? 0 : id[i];
-        const int tok = ((pos + 16 * group(i)) & pmask) + (((i * kPfThreads + t) / CPR) & 15);
-        kr[i] = *(const u32x4*)((const char*)P.k + ES * (page * P.k_page + (int64_t)head * P.k_head + (int64_t)tok * P.k_tok) + 16 * c0);
-        vr[i] = *(const u32x4*)((const char*)P.v + ES * (page * P.v_page + (int64_t)head * P.v_head + (int64_t)tok * P.v_tok) + 16 * c0);
-      }
-      if constexpr (C != codes::kNone) {
-        if (t < 2 * KT) {
-          const int key = t % KT, kp = min(pos + key, len - 1);
-          int pg = table[kp >> P.page_log2];
-          pg = (unsigned)pg >= (unsigned)P.num_pages ? 0 : pg;
-          scr = t < KT ? P.ks[(int64_t)pg * P.ks_page + (int64_t)head * P.ks_head + (kp & pmask)]
-                       : P.vs[(int64_t)pg * P.vs_page + (int64_t)head * P.vs_head + (kp & pmask)];
-        }
-      }
-    };
-    // into shared memory; what is behind the prefix becomes 0 (0 * NaN is NaN)
-    auto stage = [&](int buf, int pos) {
-      const bool tail = pos + KT > len;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int key = (i * kPfThreads + t) / CPR;
-        if (tail && pos + key >= len) {
-          kr[i] = u32x4{0u, 0u, 0u, 0u};
-          vr[i] = u32x4{0u, 0u, 0u, 0u};
-        }
         if constexpr (C == codes::kNone) {
-          ksh[buf][k_piece<D>(key, c0)] = kr[i];
-          vsh[buf][v_piece<D>(key, c0)] = vr[i];
+          load_lds(kp, klane[i], &ksh[buf][piece0 + i * kWave]);
+          load_lds(vp, vlane[i], &vsh[buf][piece0 + i * kWave]);
         } else {
-          ksh[buf][k_piece<D>(key, 2 * c0)] = widen8<BF, C>(kr[i][0], kr[i][1]);
-          ksh[buf][k_piece<D>(key, 2 * c0 + 1)] = widen8<BF, C>(kr[i][2], kr[i][3]);
-          vsh[buf][v_piece<D>(key, 2 * c0)] = widen8<true, C>(vr[i][0], vr[i][1]);
-          vsh[buf][v_piece<D>(key, 2 * c0 + 1)] = widen8<true, C>(vr[i][2], vr[i][3]);
+          kr[i] = *(const u32x4*)(kp + klane[i]);
+          vr[i] = *(const u32x4*)(vp + vlane[i]);
         }
       }
       if constexpr (C != codes::kNone) {
-        if (t < 2 * KT) {
-          const int key = t % KT;
+        if (wv % GW == 0) {
+          const float* kq = P.ks + ((int64_t)page * P.ks_page + (int64_t)head * P.ks_head + tok);
+          const float* vq = P.vs + ((int64_t)page * P.vs_page + (int64_t)head * P.vs_head + tok);
+          scr = (lane < 16 ? kq : vq)[lane & 15];
+        }
+      }
+    };
+    // Codes into shared memory.  Values behind the prefix become 0 (0 * NaN is
+    // NaN; their scores are replaced).
+    auto stage = [&](int buf, int pos) {
+      if constexpr (C == codes::kNone) {
+        if (pos + KT > len) {
+          loads_done();
+          __syncthreads();                       // the values have come
+          for (int i = (len - pos) * (D / 8) + t; i < KT * (D / 8); i += kPfThreads) vsh[buf][i] = u32x4{0u, 0u, 0u, 0u};
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int key = (piece0 + i * kWave + lane) / CPR, c0 = lane % CPR;
+          if (pos + key >= len) vr[i] = u32x4{0u, 0u, 0u, 0u};
+          u32x4* kd = &ksh[buf][key * (D / 8)];
+          u32x4* vd = &vsh[buf][key * (D / 8)];
+          kd[(2 * c0) ^ k_turn<D>(key)] = widen8<BF, C>(kr[i][0], kr[i][1]);
+          kd[(2 * c0 + 1) ^ k_turn<D>(key)] = widen8<BF, C>(kr[i][2], kr[i][3]);
+          vd[(2 * c0) ^ v_turn<D>(key)] = widen8<true, C>(vr[i][0], vr[i][1]);
+          vd[(2 * c0 + 1) ^ v_turn<D>(key)] = widen8<true, C>(vr[i][2], vr[i][3]);
+        }
+        if (wv % GW == 0) {
+          const int key = 16 * grp + (lane & 15);
           const float s = pos + key < len ? scr : 0.f;
-          if (t < KT) kscale[buf][key] = s * sl;
-          else vscale[buf][key] = s;
+          if (lane < 16) kscale[buf][key] = s * sl;
+          else if (lane < 32) vscale[buf][key] = s;
         }
       }
     };
     const int pos0 = b0 * kUnitKeys, pos_end = min(len, b1 * kUnitKeys);
     names(pos0);
-    load(pos0);
+    load(0, pos0);                               // the last tile's keys have been read
     if (pos0 + KT < pos_end) names(pos0 + KT);
-    __syncthreads();                             // the last tile's keys have been read
     stage(0, pos0);
+    loads_done();
     __syncthreads();
     int buf = 0;
     for (int pos = pos0; pos < pos_end; pos += KT, buf ^= 1) {
       const bool more = pos + KT < pos_end;
+      // The compiler would wait for each read right in front of its product: the
+      // order is fixed here, with kAhead reads under way, the first of them while
+      // the next keys are sent for.
+      const char* kb = kbase + buf * (KT * D * 2);
+      char* vb = vbase + buf * (KT * D * 2);
+      constexpr int N = NT * NS, kAhead = C == codes::kNone ? 8 : 5;
+      u32x4 k[kAhead];
+      auto read = [&](int i) { k[i % kAhead] = *(const u32x4*)(kb + (i % NT) * (64 * D) + (koff ^ (32 * (i / NT)))); };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) read(i);
+      __builtin_amdgcn_sched_barrier(0);
       if (more) {
-        load(pos + KT);
+        load(buf ^ 1, pos + KT);
         if (pos + 2 * KT < pos_end) names(pos + 2 * KT);
       }
       if (busy) {
         f32x16 s[NT];
+        {
 #pragma unroll
-        for (int a = 0; a < NT; ++a) {
+          for (int a = 0; a < NT; ++a)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[a][i] = 0.f;
+            for (int i = 0; i < 16; ++i) s[a][i] = 0.f;
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < NS; ++i) s[a] = mfma32<BF>(ksh[buf][k_piece<D>(32 * a + col, 2 * i + h)], q[i], s[a]);
+          for (int i = 0; i < N; ++i) {
+            s[i % NT] = mfma32<BF>(k[i % kAhead], q[i / NT], s[i % NT]);
+            if (i + kAhead < N) read(i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
+        u32x4 v[2][NJ];                          // the values of 16 keys, and of the next
+        auto read_v = [&](int c, int k) {        // half k & 1 of tile k >> 1's operand, keys 16 c ..
+          const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (TrPtr)(vb + (16 * c + 8 * (k & 1)) * (2 * D) + (voff ^ (64 * (k >> 1))))));
+          v[c & 1][k >> 1][2 * (k & 1)] = y[0];
+          v[c & 1][k >> 1][2 * (k & 1) + 1] = y[1];
+        };
+#pragma unroll
+        for (int k = 0; k < 2 * NJ; ++k) read_v(0, k);
         if constexpr (C != codes::kNone) {
 #pragma unroll
           for (int a = 0; a < NT; ++a)
@@ -265,52 +342,50 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : D == 128 ? 2 : 3) k
           for (int j = 0; j < NJ; ++j) o[j] *= f;
         }
         const float ref = mx == -INFINITY ? 0.f : reference<PB>(mx);
-#pragma unroll
-        for (int a = 0; a < NT; ++a) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {          // 16 keys: the slots of one product
-            float p[8], eight;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float x = s[a][8 * b + e];
-              p[e] = at_exp2(C == codes::kNone ? fmaf(x, sl, -ref) : x - ref);
-              eight = e ? eight + p[e] : p[e];
+        // 16 keys at a time, the slots of one product.  A wave's products and the next
+        // 16 keys' weights are interleaved by hand, since each takes about as long as
+        // the other: 2 NJ products of 32 cycles, 8 weights of about 40.
+        u32x4 ph[2], pl[2];
+        float p[8], eight = 0.f;
+        f32x4 vf[2];
+        auto weight = [&](int c, int e) {
+          if constexpr (C != codes::kNone)
+            if (e == 0) {
+              vf[0] = *(const f32x4*)&vscale[buf][16 * c + 4 * h];
+              vf[1] = *(const f32x4*)&vscale[buf][16 * c + 8 + 4 * h];
             }
-            ls += eight;
-            if constexpr (C != codes::kNone) {
+          const float x = s[c >> 1][8 * (c & 1) + e];
+          p[e] = at_exp2(C == codes::kNone ? fmaf(x, sl, -ref) : x - ref);
+          eight = e ? eight + p[e] : p[e];
+          if (e == 7) ls += eight;               // summed up first, as in k_attention
+          if constexpr (C != codes::kNone) p[e] *= vf[e >> 2][e & 3];
+          if (e & 1) {
+            uint32_t hi, lo;
+            split16<PB>(p[e - 1], p[e], &hi, &lo);
+            ph[c & 1][e >> 1] = hi;
+            pl[c & 1][e >> 1] = lo;
+          }
+        };
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const f32x4 f = *(const f32x4*)&vscale[buf][32 * a + 16 * b + 8 * i + 4 * h];
+        for (int e = 0; e < 8; ++e) weight(0, e);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[4 * i + k] *= f[k];
-              }
+        for (int c = 0; c < 2 * NT; ++c) {
+#pragma unroll
+          for (int k = 0; k < 2 * NJ; ++k) {
+            const int j = k % NJ;
+            o[j] = mfma32<PB>(v[c & 1][j], k < NJ ? ph[c & 1] : pl[c & 1], o[j]);
+            if (c + 1 < 2 * NT) {
+              read_v(c + 1, k);
+#pragma unroll
+              for (int e = k * 8 / (2 * NJ); e < (k + 1) * 8 / (2 * NJ); ++e) weight(c + 1, e);
             }
-            u32x4 ph, pl;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ph[i] = pack16<PB>(p[2 * i], p[2 * i + 1]);
-              pl[i] = pack16<PB>(p[2 * i] - lo16<PB>(ph[i]), p[2 * i + 1] - hi16<PB>(ph[i]));
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              u32x4 v;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                // of four keys the 16 numbers around this lane's: 4 (lane & 3) .. + 3 of key (lane >> 2) & 3
-                const int key = 32 * a + 16 * b + 8 * i + 4 * h + ((lane >> 2) & 3);
-                const int d = 32 * j + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((TrPtr)((char*)&vsh[buf][v_piece<D>(key, d >> 3)] + 2 * (d & 7)));
-                const u32x2 y = __builtin_bit_cast(u32x2, x);
-                v[2 * i] = y[0];
-                v[2 * i + 1] = y[1];
-              }
-              o[j] = mfma32<PB>(v, ph, o[j]);
-              o[j] = mfma32<PB>(v, pl, o[j]);
-            }
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
       if (more) stage(buf ^ 1, pos + KT);
+      loads_done();
       __syncthreads();
     }
     // a lane's row: numbers 32 j + 8 i + 4 h .. + 3

@@ -163,7 +163,7 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, co
       const int64_t units = ((int64_t)a->total_rows * (a->heads / a->kv_heads) / sv::kAttnPrefixRows + groups) * a->kv_heads *
                             (((int64_t)a->max_pages * a->page_size + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
       s->prefix.row_tiles = sv::kAttnManyRows;
-      s->prefix.blocks = (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : a->head_dim == 128 ? 512 : 768);
+      s->prefix.blocks = (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : 512);
       s->prefix.part_bytes = 2 * (int64_t)sv::kAttnPrefixRows * (a->head_dim + 2) * 4;
     }
   }
@@ -515,6 +515,11 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
     auto stage = codes == SV_CODES_E4M3   ? sv::launch_attention_shared_e4m3
                  : codes == SV_CODES_INT8 ? sv::launch_attention_shared_int8
                                           : sv::launch_attention_shared;
+    // the kernel for many rows takes strides in bytes in 32 bits; the other one's parts are smaller
+    const int64_t es = codes == SV_CODES_NONE ? 2 : 1;
+    const int64_t most = std::max(std::max(a->k_page_stride, a->v_page_stride), a->page_size * std::max(a->k_token_stride, a->v_token_stride));
+    if (l.prefix.row_tiles == sv::kAttnManyRows && most * es > UINT32_MAX)
+      attention_shape(who, a, codes, a->total_rows, l.groups, &l.prefix);
     e = sv::launch_attention_plan(p, 16 * l.own.row_tiles, l.prefix.row_tiles == sv::kAttnManyRows ? sv::kAttnPrefixRows : 16 * l.prefix.row_tiles, st);
     if (e == hipSuccess) e = stage(p, sv::kAttnPrefix, l.prefix.row_tiles, l.prefix.blocks, st);
     if (e == hipSuccess) e = stage(p, sv::kAttnOwn, l.own.row_tiles, l.own.blocks, st);
