@@ -714,7 +714,7 @@ int64_t spec_verify_codes_size(void);
  * its new tokens sets SV_ST_BAD_LENGTH for it; one that the group's first
  * sequence does not have refuses the group.  Groups that do not add up set
  * SV_ST_BAD_LAYOUT for every sequence.  Refused sequences' rows are NaN.  With
- * groups window is 0, and five kernels are enqueued instead of two.
+ * groups window is 0, and up to four kernels are enqueued instead of two.
  * workspace: spec_verify_attention_options_workspace() bytes. */
 typedef struct spec_verify_attention_options {
   int32_t codes;

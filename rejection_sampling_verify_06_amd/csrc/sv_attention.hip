@@ -1,8 +1,6 @@
 // Attention of a round's new tokens over a paged key-value cache, for gfx950:
-// the 16-bit cache, and the parts' join of every kind of call (the kernel and
+// the 16-bit cache, and the parts' join of every kind of cache (the kernel and
 // its reasons are in sv_attention_kernel.h).
-
-#include <type_traits>
 
 #include "sv_attention_kernel.h"
 
@@ -14,11 +12,11 @@ namespace sv {
 // record, then maxima, sums and the first parts' O at once, 8 parts of a
 // lane's 16 bytes in flight.  Further blocks check the sequences' pages for
 // `status`.
-template <bool BF, int D, int S>
+template <bool BF, int D>
 __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int TM, int W0) {
   __shared__ float wt[kAtWaves][kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
-  if (S == kWholeSeq && (int)blockIdx.x >= W0) {
+  if ((int)blockIdx.x >= W0) {
     if (blockIdx.y) return;
     // status of sequence b; block W0 checks the layout for all
     const int b = (int)blockIdx.x - W0;
@@ -75,7 +73,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
   if (row >= nrow) return;                       // whole waves; no block barrier below
   const int parts = (int)(range_of((uint32_t)d.end_unit - 1, d.W, d.U) - w) + 2;
   // part 0: slot 1 of block w - 1; part i: slot 0 of block w - 1 + i
-  auto part = [&](int i) { return (const float*)part_at(P, (int)w - 1 + i, i == 0 ? 1 : 0, TM, D); };
+  auto part = [&](int i) { return (const float*)part_at(P.parts, (int)w - 1 + i, i == 0 ? 1 : 0, TM, D); };
   constexpr int Q = D / 4;                       // lanes that cover a row with 4 floats each
   constexpr int GR = kWave / Q;                  // parts side by side: 4, 2 or 1
   const int pg = lane / Q, dq = (lane - pg * Q) * 4;
@@ -122,11 +120,6 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
     for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor(acc[c], off);
   const int R = d.mb * TM + row, ri = R / P.group, h = d.head * P.group + R - ri * P.group;
   const int64_t at = (int64_t)(d.row0 + ri) * P.heads + h;
-  if constexpr (S == kPrefix) {
-    if (pg == 0) *(f32x4*)(P.state_o + at * D + dq) = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : acc / L;
-    if (lane == 0) P.state_m[at] = L == 0.f ? -INFINITY : M + log2f(L);
-    return;
-  }
   if (pg == 0) {
     uint16_t* op = (uint16_t*)P.out + at * D + dq;
     u32x2 z;
@@ -137,32 +130,23 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_join(AttnParams P, int
   if (P.lse && lane == 0) P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-hipError_t launch_attention_join(const AttnParams& p, int stage, int tm, int W, hipStream_t st) {
-  const dim3 grid((unsigned)(W + (stage == kWholeSeq && p.status ? p.B : 0)), (unsigned)(tm / kAtWaves)), block(kAtThreads);
-  auto launch = [&](auto bf, auto dim) {
-    constexpr bool BF = decltype(bf)::value;
-    constexpr int D = decltype(dim)::value;
-    switch (stage) {
-      case kWholeSeq: hipLaunchKernelGGL((k_attention_join<BF, D, kWholeSeq>), grid, block, 0, st, p, tm, W); break;
-      case kPrefix: hipLaunchKernelGGL((k_attention_join<BF, D, kPrefix>), grid, block, 0, st, p, tm, W); break;
-      case kOwn: hipLaunchKernelGGL((k_attention_join<BF, D, kOwn>), grid, block, 0, st, p, tm, W); break;
-    }
-  };
-  auto by_dim = [&](auto bf) {
-    switch (p.head_dim) {
-      case 64: launch(bf, std::integral_constant<int, 64>{}); break;
-      case 128: launch(bf, std::integral_constant<int, 128>{}); break;
-      case 256: launch(bf, std::integral_constant<int, 256>{}); break;
-    }
-  };
-  if (p.bf16) by_dim(std::true_type{});
-  else by_dim(std::false_type{});
+hipError_t launch_attention_join(const AttnParams& p, int tm, int W, hipStream_t st) {
+  const dim3 grid((unsigned)(W + (p.status ? p.B : 0)), (unsigned)(tm / kAtWaves)), block(kAtThreads);
+  switch (p.head_dim * 2 + (p.bf16 ? 1 : 0)) {
+    case 64 * 2: hipLaunchKernelGGL((k_attention_join<false, 64>), grid, block, 0, st, p, tm, W); break;
+    case 64 * 2 + 1: hipLaunchKernelGGL((k_attention_join<true, 64>), grid, block, 0, st, p, tm, W); break;
+    case 128 * 2: hipLaunchKernelGGL((k_attention_join<false, 128>), grid, block, 0, st, p, tm, W); break;
+    case 128 * 2 + 1: hipLaunchKernelGGL((k_attention_join<true, 128>), grid, block, 0, st, p, tm, W); break;
+    case 256 * 2: hipLaunchKernelGGL((k_attention_join<false, 256>), grid, block, 0, st, p, tm, W); break;
+    case 256 * 2 + 1: hipLaunchKernelGGL((k_attention_join<true, 256>), grid, block, 0, st, p, tm, W); break;
+    default: return hipErrorInvalidValue;
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st) {
-  return p.bf16 ? launch_type<true, codes::kNone, kWholeSeq>(p, row_tiles, blocks, st)
-                : launch_type<false, codes::kNone, kWholeSeq>(p, row_tiles, blocks, st);
+  return p.bf16 ? launch_type<true, codes::kNone, false>(p, row_tiles, blocks, st)
+                : launch_type<false, codes::kNone, false>(p, row_tiles, blocks, st);
 }
 
 }  // namespace sv

@@ -6,8 +6,8 @@
 namespace sv {
 
 hipError_t launch_attention_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st) {
-  return p.bf16 ? launch_type<true, codes::kE4m3, kWholeSeq>(p, row_tiles, blocks, st)
-                : launch_type<false, codes::kE4m3, kWholeSeq>(p, row_tiles, blocks, st);
+  return p.bf16 ? launch_type<true, codes::kE4m3, false>(p, row_tiles, blocks, st)
+                : launch_type<false, codes::kE4m3, false>(p, row_tiles, blocks, st);
 }
 
 }  // namespace sv

@@ -54,10 +54,10 @@
 // numbers exactly, also where the queries are float16 (whose range a weight
 // times a scale would leave).
 //
-// With a shared prefix (S) the kernel runs twice.  Stage 1 takes a group's
-// sequences as one, whose rows are those of all members and whose keys are the
-// prefix, and leaves (O / l, m + log2 l) for each row; stage 2 takes each
-// sequence's keys from the prefix on and starts from them.
+// With shared prefixes (S) the kernel's entries are groups, whose rows are those
+// of all members and whose keys are the prefix, and sequences, whose keys begin
+// behind it.  What a tile of either comes to goes to the workspace, and
+// k_attention_merge (sv_attention_shared.hip) adds up what belongs to a row.
 
 #pragma once
 
@@ -313,47 +313,19 @@ __device__ __forceinline__ uint32_t range_of(uint32_t u, uint32_t W, uint32_t U)
 }
 
 // a part in the workspace: TM rows of O, then what their weights were taken against, then TM sums
-__device__ __forceinline__ float* part_at(const AttnParams& P, int w, int slot, int TM, int D) {
-  return P.parts + ((int64_t)w * 2 + slot) * TM * (D + 2);
+__device__ __forceinline__ float* part_at(float* parts, int w, int slot, int TM, int D) {
+  return parts + ((int64_t)w * 2 + slot) * TM * (D + 2);
 }
 
-// S: one pass over everything a sequence has, or the stages of a shared prefix
-constexpr int kWholeSeq = kAttnWhole, kPrefix = kAttnPrefix, kOwn = kAttnOwn;
-
-// Stages of a shared prefix: rows and units of the groups or sequences come
-// from the plan (k_attention_plan), as prefix sums into shared memory.
-__device__ __forceinline__ bool load_plan(const AttnParams& P, int S, uint32_t* rows, uint32_t* units) {
-  const int n = S == kPrefix ? P.G : P.B;
-  const int32_t* r = S == kPrefix ? P.plan.group_rows : P.plan.rows;
-  const int32_t* u = S == kPrefix ? P.plan.group_units : P.plan.units;
-  for (int i = threadIdx.x; i <= n; i += kAtThreads) {
-    rows[i] = (uint32_t)r[i];
-    units[i] = (uint32_t)u[i];
-  }
-  const bool ok = *P.plan.bad == 0;
-  __syncthreads();
-  return ok;
-}
-__device__ __forceinline__ Extent plan_extent(const AttnParams& P, int S, int b) {
-  Extent x;
-  if (S == kPrefix) {
-    x.slot = P.plan.group_slot[b];
-    x.len = P.plan.group_len[b];
-    x.first = 0;
-  } else {
-    x.slot = P.plan.flags[b] ? -1 : P.plan.slot[b];
-    x.len = P.plan.len[b];
-    x.first = P.plan.first[b];
-  }
-  x.blk0 = x.first / kUnitKeys;
-  x.nblk = (x.len + kUnitKeys - 1) / kUnitKeys - x.blk0;
-  if (S == kOwn) x.nblk = max(1, x.nblk);
-  return x;
+// Shared prefixes: row X of a key head (its rows in packed order) in what whole tiles leave.
+__device__ __forceinline__ int64_t state_row(const AttnParams& P, int row0, int head, int R) {
+  return ((int64_t)head * P.total_rows + row0) * P.group + R;
 }
 
 }  // namespace
 
-template <bool BF, int D, int MT, int C, int S>
+// S: with shared prefixes, whose plan is in the workspace
+template <bool BF, int D, int MT, int C, bool S>
 __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 ? 3 : 4) : D * MT <= 256 && D < 256 ? 2 : 1) k_attention(AttnParams P) {
   constexpr bool PB = BF || C != codes::kNone;   // the second product's type
   constexpr int ES = C != codes::kNone ? 1 : 2;  // bytes of a cached number
@@ -363,22 +335,27 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
   constexpr int VW = NJ * ES / 4;                // dwords of those
   constexpr int NL = D * ES / 64;                // 16-byte loads of a lane's part of a key
   extern __shared__ uint32_t dyn[];
-  const int nseq = S == kPrefix ? P.G : P.B;
-  uint32_t* rows = dyn;
-  uint32_t* units = dyn + nseq + 1;
+  const int nseq = S ? P.entries : P.B;
+  uint32_t* rows = dyn;                          // not with S
+  uint32_t* units = S ? dyn : dyn + P.B + 1;
   constexpr int RS = 256 / D;                    // of a lane's 4 rows of each O^T tile, those that are joined at a time
   __shared__ u32x4 qs[MT][NS][kWave];        // the tile's queries as the first product's right operands
   __shared__ float ml[kAtWaves][2][TM];
   __shared__ float ob[kAtWaves][16][64 + 4];     // 64 of the D values of 16 rows, rows 4 banks apart
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = uni(t / kWave);
   const int g = lane >> 4, col = lane & 15;
-  const bool ok = S == kWholeSeq ? plan(P, TM, rows, units) : load_plan(P, S, rows, units);
+  bool ok = true;
+  if constexpr (S) {
+    for (int i = t; i <= nseq; i += kAtThreads) units[i] = (uint32_t)P.plan.units[i];   // none where the layout is bad
+    __syncthreads();
+  } else {
+    ok = plan(P, TM, rows, units);
+  }
   Part* desc = reinterpret_cast<Part*>(P.desc);
   const uint32_t U = (uint32_t)uni((int)units[nseq]), W = min((uint32_t)gridDim.x, U);
   const uint32_t w = blockIdx.x;
   if (!ok) {                                     // the rows do not add up: every output is cleared
     if (t == 0) desc[w].first_unit = -1;
-    if constexpr (S == kPrefix) return;
     const int64_t total = (int64_t)P.total_rows * P.heads * D;
     for (int64_t i = (int64_t)w * kAtThreads + t; i < total; i += (int64_t)gridDim.x * kAtThreads)
       ((uint16_t*)P.out)[i] = BF ? 0x7FC0 : 0x7E00;
@@ -388,26 +365,46 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
     return;
   }
   if (w >= W) {
-    if (t == 0) desc[w].first_unit = -1;
+    if (!S && t == 0) desc[w].first_unit = -1;
     return;
   }
   uint32_t u = range_start(w, W, U);
   const uint32_t u_end = range_start(w + 1, W, U);
   // the sequence that holds unit u
   int b = 0;
-  for (int step = 4096; step > 0; step >>= 1)
+  for (int step = S ? 8192 : 4096; step > 0; step >>= 1)
     if (b + step < nseq && (uint32_t)uni((int)units[b + step]) <= u) b += step;
   bool first_part = true;
   while (u < u_end) {
     while ((uint32_t)uni((int)units[b + 1]) <= u) ++b;
-    const int row0 = uni((int)rows[b]), n = uni((int)rows[b + 1]) - row0;
-    Extent x = S == kWholeSeq ? seq_extent(P, b, n) : plan_extent(P, S, b);
-    x = Extent{uni(x.slot), uni(x.len), uni(x.first), uni(x.blk0), uni(x.nblk)};
+    int row0, n, tile0 = 0;
+    bool group = false;                          // S: a group and its prefix
+    Extent x;
+    if constexpr (S) {
+      const AttnRecord rec = P.plan.entry[b];
+      group = b < P.group_entries;
+      const int flags = group ? 0 : P.plan.flags[b - P.group_entries];
+      row0 = uni(rec.row0);
+      n = uni(rec.n);
+      tile0 = uni(rec.tile0);
+      x.slot = uni(flags ? -1 : rec.slot);
+      x.len = uni(rec.len);
+      x.first = uni(rec.first);
+      x.blk0 = x.first / kUnitKeys;
+      x.nblk = max(1, (x.len + kUnitKeys - 1) / kUnitKeys - x.blk0);
+    } else {
+      row0 = uni((int)rows[b]);
+      n = uni((int)rows[b + 1]) - row0;
+      x = seq_extent(P, b, n);
+      x = Extent{uni(x.slot), uni(x.len), uni(x.first), uni(x.blk0), uni(x.nblk)};
+    }
     const uint32_t rel = u - (uint32_t)uni((int)units[b]);
     const int seg = (int)(rel / (uint32_t)x.nblk), b0 = (int)(rel - (uint32_t)seg * x.nblk);
     const int b1 = (int)min((uint32_t)x.nblk, b0 + (u_end - u));
     const int mb = seg / P.kv_heads, head = seg - mb * P.kv_heads;
-    if (first_part && t == 0) {
+    if constexpr (S) {
+      if (b0 == 0 && t == 0) P.plan.tile[tile0 + seg] = make_int2((int)w, (int)(range_of(u + (uint32_t)x.nblk - 1, W, U) - w) + 1);
+    } else if (first_part && t == 0) {
       Part d;
       d.first_unit = b0 > 0 ? (int)(u - b0) : -1;
       d.end_unit = (int)(u - b0) + x.nblk;
@@ -425,8 +422,8 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
     int min_last = 0x7FFFFFFF, max_from = 0;
     {
       const int i0 = mb * TM / P.group, i1 = (mb * TM + nrow - 1) / P.group;
-      min_last = S == kPrefix ? x.len - 1 : x.len - n + i0;
-      max_from = S != kWholeSeq ? x.first : P.window > 0 ? max(0, x.len - n + i1 + 1 - P.window) : 0;
+      min_last = S && group ? x.len - 1 : x.len - n + i0;
+      max_from = S ? x.first : P.window > 0 ? max(0, x.len - n + i1 + 1 - P.window) : 0;
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -434,14 +431,20 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
       const bool in = r < nrow;
       const int rr = mb * TM + (in ? r : 0);
       const int i = rr / P.group, h = head * P.group + rr - i * P.group;
-      last[m] = !in ? -1 : S == kPrefix ? x.len - 1 : x.len - n + i;
-      from[m] = S != kWholeSeq ? x.first : P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
-      // 16 bytes of a key are 8 numbers of one slice, or codes of two: 64 s' + 16 g .. + 15
-      const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head + (ES == 2 ? 8 : 16) * g;
+      last[m] = !in ? -1 : S && group ? x.len - 1 : x.len - n + i;
+      from[m] = S ? x.first : P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
+    }
+    // The queries: each wave brings some of the operands, all at once.  16 bytes of
+    // a key are 8 numbers of one slice, or codes of two: 64 s' + 16 g .. + 15.
+    constexpr int NQ = (MT * NS + kAtWaves - 1) / kAtWaves;
+    u32x4 qr[NQ];
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
-        if ((m * NS + s) % kAtWaves == wv)
-          qs[m][s][lane] = *(const u32x4*)(qp + (ES == 2 ? 32 * s : 64 * (s >> 1) + 8 * (s & 1)));
+    for (int k = 0; k < NQ; ++k) {
+      const int at = min(k * kAtWaves + wv, MT * NS - 1), s = at % NS, r = at / NS * 16 + col;
+      const int rr = mb * TM + (r < nrow ? r : 0);
+      const int i = rr / P.group, h = head * P.group + rr - i * P.group;
+      qr[k] = *(const u32x4*)((const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head +
+                              (ES == 2 ? 32 * s + 8 * g : 64 * (s >> 1) + 8 * (s & 1) + 16 * g));
     }
     f32x4 o[MT][NJ];
     float mx[MT], ls[MT];
@@ -451,33 +454,6 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
       ls[m] = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) o[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    if constexpr (S == kOwn) {
-      // what the prefix left: a row's value with the weight that 2^lse has
-      if (b0 == 0 && x.first > 0 && wv == 0) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int r = m * 16 + col;
-          if (r >= nrow) continue;
-          const int R = mb * TM + r, ri = R / P.group;
-          const int64_t at = (int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group;
-          const float lse = P.state_m[at];
-          if (lse == -INFINITY) continue;
-          const bool num = lse == lse;           // NaN: into the sum, not the maximum
-          mx[m] = num ? lse : -INFINITY;
-          const float w = num ? at_exp2(lse - reference<PB>(lse)) : lse;
-          ls[m] = g == 0 ? w : 0.f;              // the four lanes of a row are summed up in the end
-          const float* so = P.state_o + at * D + NJ * 4 * g;
-#pragma unroll
-          for (int rr = 0; rr < 4; ++rr)
-#pragma unroll
-            for (int j = 0; j < NJ; j += 4) {
-              const f32x4 v = *(const f32x4*)(so + NJ * rr + j);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[m][j + k][rr] = v[k] * w;
-            }
-        }
-      }
     }
     bool bad = x.slot < 0;
     // read with scalar loads, whose counter is not the one the keys and values in flight are waited for with
@@ -561,6 +537,8 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
       load_k();
       load_v();
     }
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) (&qs[0][0][lane])[min(k * kAtWaves + wv, MT * NS - 1) * kWave] = qr[k];
     __syncthreads();                             // the queries are in place
     for (; pos < pos_end; pos += kUnitKeys) {
       const bool more = pos + kUnitKeys < pos_end;
@@ -766,7 +744,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
     }
     __syncthreads();
     const bool whole = b0 == 0 && b1 == x.nblk;
-    float* part = part_at(P, (int)w, b0 > 0 ? 0 : 1, TM, D);
+    float* part = part_at(P.parts, (int)w, b0 > 0 ? 0 : 1, TM, D);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (m * 16 >= nrow) break;
@@ -782,11 +760,11 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
         if (!whole) {
           part[TM * D + r] = M;
           part[TM * D + TM + r] = L;
-        } else if (S == kPrefix || P.lse) {
+        } else if (S) {
+          P.state_m[(group ? 0 : (int64_t)P.total_rows * P.heads) + state_row(P, row0, head, mb * TM + r)] = L == 0.f ? -INFINITY : M + log2f(L);
+        } else if (P.lse) {
           const int R = mb * TM + r, ri = R / P.group;
-          const int64_t at = (int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group;
-          if constexpr (S == kPrefix) P.state_m[at] = L == 0.f ? -INFINITY : M + log2f(L);
-          else P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+          P.lse[(int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
         }
       }
 #pragma unroll
@@ -814,11 +792,15 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
           if (row < nrow) {
             const int gr = c / NJ;               // g RS + rr
             const int d = NJ * (4 * (gr / RS) + r0 + gr % RS) + c % NJ;
-            if (whole) {
+            if constexpr (S) {
+              // by fours of the head dimension, then rows: k_attention_merge takes neighbouring rows side by side
+              const int64_t total = (int64_t)P.total_rows * P.heads;
+              float* to = whole ? P.state_o + ((group ? 0 : total * (D / 4)) + state_row(P, row0, head, mb * TM + row)) * 4 : part + row * 4;
+              *(f32x4*)(to + (int64_t)(d / 4) * 4 * (whole ? total : TM)) = v;
+            } else if (whole) {
               const int R = mb * TM + row, ri = R / P.group;
               const int64_t at = (int64_t)(row0 + ri) * P.heads + head * P.group + R - ri * P.group;
-              if constexpr (S == kPrefix) *(f32x4*)(P.state_o + at * D + d) = v;
-              else *(u32x2*)((uint16_t*)P.out + at * D + d) = u32x2{pack16<BF>(v[0], v[1]), pack16<BF>(v[2], v[3])};
+              *(u32x2*)((uint16_t*)P.out + at * D + d) = u32x2{pack16<BF>(v[0], v[1]), pack16<BF>(v[2], v[3])};
             } else {
               *(f32x4*)(part + row * D + d) = v;
             }
@@ -834,16 +816,16 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
 
 namespace {
 
-template <bool BF, int D, int MT, int C, int S>
+template <bool BF, int D, int MT, int C, bool S>
 hipError_t launch_one(const AttnParams& p, int W, hipStream_t st) {
-  const size_t lds = (size_t)((S == kPrefix ? p.G : p.B) + 1) * 8;
+  const size_t lds = S ? (size_t)(p.entries + 1) * 4 : (size_t)(p.B + 1) * 8;
   hipLaunchKernelGGL((k_attention<BF, D, MT, C, S>), dim3((unsigned)W), dim3(kAtThreads), lds, st, p);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_attention_join(p, S, 16 * MT, W, st);
+  if (S || e != hipSuccess) return e;
+  return launch_attention_join(p, 16 * MT, W, st);
 }
 
-template <bool BF, int C, int S>
+template <bool BF, int C, bool S>
 hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
   switch (p.head_dim * 8 + mt) {
     case 64 * 8 + 1: return launch_one<BF, 64, 1, C, S>(p, W, st);
@@ -855,12 +837,6 @@ hipError_t launch_type(const AttnParams& p, int mt, int W, hipStream_t st) {
     case 256 * 8 + 1: return launch_one<BF, 256, 1, C, S>(p, W, st);
   }
   return hipErrorInvalidValue;
-}
-
-template <int C>
-hipError_t launch_shared(const AttnParams& p, int stage, int mt, int W, hipStream_t st) {
-  if (stage == kPrefix) return p.bf16 ? launch_type<true, C, kPrefix>(p, mt, W, st) : launch_type<false, C, kPrefix>(p, mt, W, st);
-  return p.bf16 ? launch_type<true, C, kOwn>(p, mt, W, st) : launch_type<false, C, kOwn>(p, mt, W, st);
 }
 
 }  // namespace

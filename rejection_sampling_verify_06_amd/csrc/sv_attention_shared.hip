@@ -4,12 +4,13 @@
 //
 // Softmax over a row's keys splits into parts (m, l, O) that join exactly, so
 // a prefix that a group of sequences shares is read once for the rows of all
-// of them instead of once for each.  A call is five launches:
-//   plan     rows and units of both stages, every refusal
-//   prefix   the groups' rows over the prefixes: k_attention's stage 1, or
-//            k_prefix (sv_prefix.h) where a group has many rows; the parts' join
-//   own      each sequence's tokens behind the prefix, starting from what the
-//            prefix left for its rows; the parts' join
+// of them instead of once for each.  A call is three or four launches:
+//   plan     rows and units of groups and sequences, every refusal
+//   prefix   the groups' rows over the prefixes, where they are many (k_prefix,
+//            sv_prefix.h)
+//   tiles    each sequence's tokens behind its prefix, and groups of few rows over
+//            theirs (k_attention)
+//   merge    of all that belongs to a row
 
 #include "sv_prefix.h"
 
@@ -73,10 +74,10 @@ __device__ __forceinline__ Seq seq_check(const AttnParams& P, int b, int prefix,
 // Block 0 makes the plan; block 1 + b looks at the pages of sequence b: those
 // of the prefix have to be its leader's (the first sequence of its group), but
 // for a partly filled last one, which may be a copy.
-__global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P, int own_rows, int group_rows) {
+__global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P) {
   extern __shared__ uint32_t dyn[];
-  __shared__ uint32_t tr[kAtWaves], tu[kAtWaves];
-  __shared__ int shared_g, shared_st;
+  __shared__ uint32_t tw[kAtWaves];
+  __shared__ int shared_g, shared_st, shared_row;
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
   const bool bad = layout_bad(P);
   if (blockIdx.x > 0) {
@@ -85,10 +86,16 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P, int
       if (t == 0 && P.status) P.status[b] = SV_ST_BAD_LAYOUT;
       return;
     }
-    if (t == 0) shared_st = 0;
+    if (t == 0) shared_st = shared_row = 0;
+    __syncthreads();
+    int before = 0;                              // rows of the sequences in front
+    for (int i = t; i < b; i += kAtThreads) before += P.num_draft[i] + 1;
+    if (before) atomicAdd(&shared_row, before);
     for (int g = t; g < P.G; g += kAtThreads)
       if (P.groups[g] <= b && b < P.groups[g + 1]) shared_g = g;
     __syncthreads();
+    const int row0 = shared_row, n = P.num_draft[b] + 1;
+    for (int i = t; i < n; i += kAtThreads) P.plan.row_seq[row0 + i] = b;
     const int prefix = P.prefix_len[shared_g], lead = P.groups[shared_g];
     const Seq l = seq_check(P, lead, prefix, true), s = seq_check(P, b, prefix, false);
     int st = s.status | l.status;
@@ -116,43 +123,87 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P, int
     return;
   }
   if (t == 0) *P.plan.bad = bad ? 1 : 0;
-  if (bad) {                                     // no stage has any work; the last one clears the outputs
-    if (t == 0) P.plan.units[P.B] = P.plan.group_units[P.G] = 0;
+  if (bad) {                                     // no tile has any work; the merge clears the outputs
+    if (t == 0) P.plan.units[P.entries] = P.plan.group_units[P.G] = 0;
     return;
   }
   uint32_t* rows = dyn;                          // [B + 1]
-  uint32_t* first = dyn + P.B + 1;               // [G + 1]
-  for (int g = t; g <= P.G; g += kAtThreads) first[g] = (uint32_t)P.groups[g];
+  uint32_t* first = dyn + P.B + 1;               // [G + 1] first sequences
+  uint32_t* mine = first + P.G + 1;              // [B] units of a sequence, or of a group
   // exclusive prefix over the block of a thread's value, and the block's total
-  auto scan = [&](uint32_t v, uint32_t* total, uint32_t* waves) {
+  auto scan = [&](uint32_t v, uint32_t* total) {
     const uint32_t in = wave_incl_scan_u32(v);
     __syncthreads();
-    if (lane == kWave - 1) waves[wv] = in;
+    if (lane == kWave - 1) tw[wv] = in;
     __syncthreads();
     uint32_t before = in - v;
     *total = 0;
     for (int i = 0; i < kAtWaves; ++i) {
-      if (i < wv) before += waves[i];
-      *total += waves[i];
+      if (i < wv) before += tw[i];
+      *total += tw[i];
     }
     return before;
   };
-  uint32_t total;
+  for (int g = t; g <= P.G; g += kAtThreads) first[g] = (uint32_t)P.groups[g];
+  const int per = (P.B + kAtThreads - 1) / kAtThreads, b0 = min(t * per, P.B), b1 = min(b0 + per, P.B);
+  const int gper = (P.G + kAtThreads - 1) / kAtThreads, g0 = min(t * gper, P.G), g1 = min(g0 + gper, P.G);
+  uint32_t total, tiles, units;
   {
-    const int per = (P.B + kAtThreads - 1) / kAtThreads;
-    const int b0 = min(t * per, P.B), b1 = min(b0 + per, P.B);
     uint32_t r = 0;
     for (int b = b0; b < b1; ++b) r += (uint32_t)P.num_draft[b] + 1u;
-    uint32_t at = scan(r, &total, tr);
+    uint32_t at = scan(r, &total);
     for (int b = b0; b < b1; ++b) {
       rows[b] = at;
-      P.plan.rows[b] = (int)at;
       at += (uint32_t)P.num_draft[b] + 1u;
     }
-    if (t == 0) P.plan.rows[P.B] = rows[P.B] = total;
+    if (t == 0) rows[P.B] = total;
     __syncthreads();
-    auto own = [&](int b, bool write) -> uint32_t {
-      int lo = 0, hi = P.G - 1;                  // the last group that begins at or before b and is not empty
+  }
+  auto ceil_div = [](uint32_t a, uint32_t b) { return (a + b - 1) / b; };
+  {
+    // the groups: their tiles, and units where the kernel for many rows takes them
+    auto count = [&](int g) { return ceil_div((rows[first[g + 1]] - rows[first[g]]) * (uint32_t)P.group, (uint32_t)P.prefix_rows) * (uint32_t)P.kv_heads; };
+    uint32_t c = 0, u = 0;
+    for (int g = g0; g < g1; ++g) c += count(g);
+    uint32_t at = scan(c, &tiles);
+    for (int g = g0; g < g1; ++g) {
+      AttnRecord rec{};
+      rec.row0 = (int)rows[first[g]];
+      rec.n = (int)rows[first[g + 1]] - rec.row0;
+      rec.slot = -1;
+      if (rec.n > 0) {
+        const Seq l = seq_check(P, (int)first[g], P.prefix_len[g], true);
+        if (!l.status) {
+          rec.len = P.prefix_len[g];
+          rec.slot = l.slot;
+        }
+      }
+      rec.tile0 = (int)at;
+      P.plan.group[g] = rec;
+      const uint32_t n = count(g);
+      at += n;
+      u += mine[g] = n * (uint32_t)((rec.len + kUnitKeys - 1) / kUnitKeys);
+    }
+    uint32_t ua = scan(u, &units);
+    int32_t* to = P.group_entries ? P.plan.units : P.plan.group_units;
+    for (int g = g0; g < g1; ++g) {
+      to[g] = (int)ua;
+      ua += mine[g];
+    }
+    if (t == 0) {
+      P.plan.group_units[P.G] = P.group_entries ? 0 : (int)units;
+      if (!P.group_entries) units = 0;
+    }
+    if (!P.group_entries) units = 0;
+    __syncthreads();                             // `mine` is used again
+  }
+  {
+    uint32_t c = 0, u = 0;
+    auto count = [&](int b) { return ceil_div((rows[b + 1] - rows[b]) * (uint32_t)P.group, (uint32_t)P.own_rows) * (uint32_t)P.kv_heads; };
+    for (int b = b0; b < b1; ++b) c += count(b);
+    uint32_t at = tiles + scan(c, &total);
+    for (int b = b0; b < b1; ++b) {
+      int lo = 0, hi = P.G - 1;                  // the last group that begins at or before b: not empty
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (first[mid] <= (uint32_t)b) lo = mid;
@@ -161,68 +212,142 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P, int
       const int prefix = P.prefix_len[lo];
       Seq s = seq_check(P, b, prefix, false);
       s.status |= seq_check(P, (int)first[lo], prefix, true).status;
-      const int len = s.status ? 0 : s.len, f = s.status ? 0 : prefix;
-      if (write) {
-        P.plan.slot[b] = s.status ? -1 : s.slot;
-        P.plan.len[b] = len;
-        P.plan.first[b] = f;
-      }
-      const uint32_t n = rows[b + 1] - rows[b];
-      const int blocks = max(1, (len + kUnitKeys - 1) / kUnitKeys - f / kUnitKeys);
-      return (n * P.group + own_rows - 1) / own_rows * P.kv_heads * (uint32_t)blocks;
-    };
-    uint32_t u = 0;
-    for (int b = b0; b < b1; ++b) u += own(b, true);
-    uint32_t ua = scan(u, &total, tu);
+      AttnRecord rec{};
+      rec.slot = s.status ? -1 : s.slot;
+      rec.len = s.status ? 0 : s.len;
+      rec.first = s.status ? 0 : prefix;
+      rec.row0 = (int)rows[b];
+      rec.n = (int)(rows[b + 1] - rows[b]);
+      rec.tile0 = (int)at;
+      rec.group_row = (int)(rows[b] - rows[first[lo]]);
+      rec.group_tile0 = P.plan.group[lo].tile0;
+      P.plan.seq[b] = rec;
+      const uint32_t n = count(b);
+      at += n;
+      u += mine[b] = n * (uint32_t)max(1, (rec.len + kUnitKeys - 1) / kUnitKeys - rec.first / kUnitKeys);
+    }
+    uint32_t ua = units + scan(u, &total);
     for (int b = b0; b < b1; ++b) {
-      P.plan.units[b] = (int)ua;
-      ua += own(b, false);
+      P.plan.units[P.group_entries + b] = (int)ua;
+      ua += mine[b];
     }
-    if (t == 0) P.plan.units[P.B] = (int)total;
-  }
-  {
-    const int per = (P.G + kAtThreads - 1) / kAtThreads;
-    const int g0 = min(t * per, P.G), g1 = min(g0 + per, P.G);
-    auto units = [&](int g, bool write) -> uint32_t {
-      const uint32_t n = rows[first[g + 1]] - rows[first[g]];
-      int len = 0, slot = -1;
-      if (n > 0) {
-        const Seq l = seq_check(P, (int)first[g], P.prefix_len[g], true);
-        if (!l.status) {
-          len = P.prefix_len[g];
-          slot = l.slot;
-        }
-      }
-      if (write) {
-        P.plan.group_rows[g] = (int)rows[first[g]];
-        P.plan.group_slot[g] = slot;
-        P.plan.group_len[g] = len;
-      }
-      return (n * P.group + group_rows - 1) / group_rows * P.kv_heads * (uint32_t)((len + kUnitKeys - 1) / kUnitKeys);
-    };
-    uint32_t u = 0;
-    for (int g = g0; g < g1; ++g) u += units(g, true);
-    uint32_t ua = scan(u, &total, tu);
-    for (int g = g0; g < g1; ++g) {
-      P.plan.group_units[g] = (int)ua;
-      ua += units(g, false);
-    }
-    if (t == 0) {
-      P.plan.group_units[P.G] = (int)total;
-      P.plan.group_rows[P.G] = (int)rows[P.B];
-    }
+    if (t == 0) P.plan.units[P.entries] = (int)(units + total);
   }
 }
 
-hipError_t launch_attention_plan(const AttnParams& p, int own_rows, int group_rows, hipStream_t st) {
-  const size_t lds = ((size_t)p.B + p.G + 2) * 4;
-  hipLaunchKernelGGL(k_attention_plan, dim3((unsigned)p.B + 1), dim3(kAtThreads), lds, st, p, own_rows, group_rows);
+// Adds up, for 16 rows of a key head in packed order, what the tiles of their
+// groups and sequences came to: states of tiles that one block had whole, parts
+// of others.  A lane has a row and D / 64 fours of the head dimension, the waves
+// a quarter of it each; kBatch tiles' worth of loads are under way at a time.
+template <bool BF, int D>
+__global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
+  constexpr int GN = D / 64;                     // a lane's fours
+  constexpr int kBatch = D == 256 ? 4 : 8;
+  const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave, g = lane >> 4;
+  const int head = (int)blockIdx.y, four0 = wv * (D / 16) + g * GN;
+  const int rows = P.total_rows * P.group;       // of a key head
+  const int X = (int)blockIdx.x * 16 + (lane & 15);
+  const bool in = X < rows;
+  const int row = (in ? X : 0) / P.group, hh = (in ? X : 0) - row * P.group;
+  const int64_t at = (int64_t)row * P.heads + head * P.group + hh;
+  const bool bad = *P.plan.bad != 0;
+  f32x4 acc[GN];
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int j = 0; j < GN; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (bad) {
+    L = __builtin_nanf("");
+  } else {
+    const int b = P.plan.row_seq[row];
+    const AttnRecord rec = P.plan.seq[b];
+    const int flags = P.plan.flags[b];
+    const int R = (row - rec.row0) * P.group + hh, mb = R / P.own_rows;
+    const int pR = R + rec.group_row * P.group, pmb = pR / P.prefix_rows;
+    const int2 mine = P.plan.tile[rec.tile0 + mb * P.kv_heads + head];
+    const int2 theirs = rec.first > 0 ? P.plan.tile[rec.group_tile0 + pmb * P.kv_heads + head] : make_int2(0, 0);
+    const int parts = flags ? 0 : mine.y + theirs.y;
+    if (flags) L = __builtin_nanf("");
+    const int64_t total = (int64_t)P.total_rows * P.heads, sr = state_row(P, row, head, hh);
+    const int most = wave_max_i(parts);
+    for (int k0 = 0; k0 < most; k0 += kBatch) {
+      float m[kBatch], l[kBatch];
+      f32x4 v[kBatch][GN];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (k0 + i >= parts) continue;
+        const bool own = k0 + i < mine.y;
+        const int k = own ? k0 + i : k0 + i - mine.y;
+        const int2 tile = own ? mine : theirs;
+        const int tm = own ? P.own_rows : P.prefix_rows, r = own ? R - mb * P.own_rows : pR - pmb * P.prefix_rows;
+        const float *pm, *po;
+        int64_t four;
+        if (tile.y == 1) {
+          pm = P.state_m + (own ? total : 0) + sr;
+          po = P.state_o + ((own ? total * (D / 4) : 0) + sr) * 4;
+          four = 4 * total;
+          l[i] = 1.f;
+        } else {
+          const float* part = part_at(own ? P.parts : P.prefix_parts, tile.x + k, k == 0 ? 1 : 0, tm, D);
+          pm = part + tm * D + r;
+          po = part + r * 4;
+          four = 4 * tm;
+          l[i] = pm[tm];
+        }
+        m[i] = *pm;
+#pragma unroll
+        for (int j = 0; j < GN; ++j) v[i][j] = *(const f32x4*)(po + (four0 + j) * four);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // a tile in which the row saw nothing has m = -inf or l = 0
+        if (k0 + i >= parts || m[i] == -INFINITY || l[i] == 0.f) continue;
+        const float nm = fmaxf(M, m[i]);
+        const float f0 = M == nm ? 1.f : at_exp2(M - nm), f1 = m[i] == nm ? 1.f : at_exp2(m[i] - nm);
+        M = nm;
+        L = L * f0 + l[i] * f1;
+#pragma unroll
+        for (int j = 0; j < GN; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[j][c] = fmaf(v[i][j][c], f1, acc[j][c] * f0);
+      }
+    }
+  }
+  if (!in) return;
+  const float inv = L == 0.f ? 0.f : 1.f / L;    // NaN stays
+#pragma unroll
+  for (int j = 0; j < GN; ++j) {
+    float x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = L != L ? L : acc[j][c] * inv;
+    *(u32x2*)((uint16_t*)P.out + at * D + (four0 + j) * 4) = u32x2{pack16<BF>(x[0], x[1]), pack16<BF>(x[2], x[3])};
+  }
+  if (P.lse && wv == 0 && g == 0) P.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+hipError_t launch_attention_plan(const AttnParams& p, hipStream_t st) {
+  const size_t lds = (2 * (size_t)p.B + p.G + 2) * 4;
+  hipLaunchKernelGGL(k_attention_plan, dim3((unsigned)p.B + 1), dim3(kAtThreads), lds, st, p);
   return hipGetLastError();
 }
 
-hipError_t launch_attention_shared(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st) {
-  if (stage == kPrefix && row_tiles == kAttnManyRows) return launch_prefix_rows<codes::kNone>(p, blocks, st);
-  return launch_shared<codes::kNone>(p, stage, row_tiles, blocks, st);
+hipError_t launch_attention_merge(const AttnParams& p, hipStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)p.total_rows * p.group + 15) / 16), (unsigned)p.kv_heads), block(kAtThreads);
+  switch (p.head_dim * 2 + (p.bf16 ? 1 : 0)) {
+    case 64 * 2: hipLaunchKernelGGL((k_attention_merge<false, 64>), grid, block, 0, st, p); break;
+    case 64 * 2 + 1: hipLaunchKernelGGL((k_attention_merge<true, 64>), grid, block, 0, st, p); break;
+    case 128 * 2: hipLaunchKernelGGL((k_attention_merge<false, 128>), grid, block, 0, st, p); break;
+    case 128 * 2 + 1: hipLaunchKernelGGL((k_attention_merge<true, 128>), grid, block, 0, st, p); break;
+    case 256 * 2: hipLaunchKernelGGL((k_attention_merge<false, 256>), grid, block, 0, st, p); break;
+    case 256 * 2 + 1: hipLaunchKernelGGL((k_attention_merge<true, 256>), grid, block, 0, st, p); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
 }
+
+hipError_t launch_attention_shared(const AttnParams& p, int row_tiles, int blocks, hipStream_t st) {
+  return p.bf16 ? launch_type<true, codes::kNone, true>(p, row_tiles, blocks, st) : launch_type<false, codes::kNone, true>(p, row_tiles, blocks, st);
+}
+
+hipError_t launch_attention_prefix(const AttnParams& p, hipStream_t st) { return launch_prefix_rows<codes::kNone>(p, st); }
 
 }  // namespace sv

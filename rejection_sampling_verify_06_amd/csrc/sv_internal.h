@@ -224,20 +224,27 @@ hipError_t launch_logprobs(const LogprobParams& p, hipStream_t st);
 constexpr int kAttnUnitKeys = 128;      // keys of a unit of work
 constexpr int kAttnPartBytes = 32;      // a block's record for the join
 
-// What a call with a shared prefix works out once, in its workspace: packed
-// rows and units of work as prefix sums, and each sequence's and group's keys.
+// What a call with shared prefixes works out once, in its workspace.  Its units
+// of work belong to entries: the groups (unless the kernel for many rows takes
+// them), then the sequences.
+struct AttnRecord {                 // of a group or a sequence
+  int32_t slot;                     // row of page_table; -1: refused
+  int32_t len;                      // tokens
+  int32_t first;                    // the first of them (a sequence's prefix's length)
+  int32_t row0, n;                  // packed rows
+  int32_t tile0;                    // its first tile
+  int32_t group_row, group_tile0;   // of a sequence: its first row in its group, and the group's first tile
+};
 struct AttnPlan {
   int32_t* bad;                     // [1] rows or groups do not add up
-  int32_t* rows;                    // [B + 1]
-  int32_t* units;                   // [B + 1]
-  int32_t* slot;                    // [B] -1: refused
-  int32_t* len;                     // [B]
-  int32_t* first;                   // [B] the prefix's length
+  int32_t* units;                   // [entries + 1] prefix sums
+  int32_t* group_units;             // [G + 1] prefix sums for the kernel for many rows
+  AttnRecord* group;                // [G]
+  AttnRecord* seq;                  // [B], behind the groups
+  AttnRecord* entry;                // [entries]: group or seq
   int32_t* flags;                   // [B] status, pages looked at
-  int32_t* group_rows;              // [G + 1]
-  int32_t* group_units;             // [G + 1]
-  int32_t* group_slot;              // [G]
-  int32_t* group_len;               // [G]
+  int32_t* row_seq;                 // [total_rows] the row's sequence
+  int2* tile;                       // a tile's first block and how many, written by that block; [row tile][key head] of an entry
 };
 
 struct AttnParams {
@@ -277,24 +284,31 @@ struct AttnParams {
   int32_t G;                        // groups
   const int32_t* groups;            // [G + 1] first sequence of each
   const int32_t* prefix_len;        // [G]
+  int32_t entries, group_entries;   // entries of units, and how many of them are groups
+  int32_t own_rows, prefix_rows;    // rows of a tile of a sequence, and of a group
+  int32_t prefix_blocks;            // blocks of the kernel for many rows
   AttnPlan plan;
-  float* state_o;                   // [total_rows][heads][head_dim]: what the prefix gives a row
-  float* state_m;                   // [total_rows][heads]: log2 of its sum of weights
+  float* prefix_parts;              // the parts of groups' tiles
+  // What whole tiles come to, groups' rows and then sequences' (parts are laid out alike):
+  float* state_o;                   // [2][head_dim / 4][kv_heads][total_rows][group][4]
+  float* state_m;                   // [2][kv_heads][total_rows][group]: log2 of the sum of weights (of state_o's the sum is 1)
 };
 
 hipError_t launch_attention(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
 hipError_t launch_attention_int8(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
-hipError_t launch_attention_join(const AttnParams& p, int stage, int tm, int W, hipStream_t st);
-// a call with shared prefixes: the plan, then its two stages; the first with kAttnManyRows for
-// row_tiles by the kernel for many rows
-constexpr int kAttnManyRows = 0;
-constexpr int kAttnPrefixRows = 128;    // rows of its tiles
-enum { kAttnWhole = 0, kAttnPrefix = 1, kAttnOwn = 2 };
-hipError_t launch_attention_plan(const AttnParams& p, int own_rows, int group_rows, hipStream_t st);
-hipError_t launch_attention_shared(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
-hipError_t launch_attention_shared_e4m3(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
-hipError_t launch_attention_shared_int8(const AttnParams& p, int stage, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_join(const AttnParams& p, int tm, int W, hipStream_t st);
+// A call with shared prefixes: the plan, the groups' tiles (where the kernel for many rows takes them), the
+// other entries' tiles, the merge.
+constexpr int kAttnPrefixRows = 128;    // rows of a tile of the kernel for many rows
+hipError_t launch_attention_plan(const AttnParams& p, hipStream_t st);
+hipError_t launch_attention_prefix(const AttnParams& p, hipStream_t st);
+hipError_t launch_attention_prefix_e4m3(const AttnParams& p, hipStream_t st);
+hipError_t launch_attention_prefix_int8(const AttnParams& p, hipStream_t st);
+hipError_t launch_attention_shared(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_shared_e4m3(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_shared_int8(const AttnParams& p, int row_tiles, int blocks, hipStream_t st);
+hipError_t launch_attention_merge(const AttnParams& p, hipStream_t st);
 
 // the paged cache's own operations (sv_cache.hip)
 constexpr int kCacheMaxSlots = 4096;

@@ -17,8 +17,8 @@
 // keys (V, transposed), fall on different banks.  The next 64 keys are in
 // flight to registers while these are worked on.
 //
-// Weights are split in two 16-bit halves and units dealt out in equal
-// ranges, for the same reasons as in k_attention, whose join adds the parts up.
+// Weights are split in two 16-bit halves and units dealt out in equal ranges,
+// for the same reasons as in k_attention; k_attention_merge adds the parts up.
 
 #pragma once
 
@@ -60,15 +60,10 @@ __device__ __forceinline__ int v_turn(int r) {
   return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
 }
 
-// 16 bytes a lane from memory to the wave's 1 KB of shared memory at `to`.  Not
-// the builtin: next to it the compiler waits for all such loads before it reads
-// any shared memory, also the half that they do not write.  loads_done() comes
-// before the barrier behind which they are read.
-__device__ __forceinline__ void load_lds(const char* base, uint32_t offset, const u32x4* to) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const u32x4*)to;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni((int)at)), "v"(offset), "s"(base) : "memory", "m0");
+// 16 bytes a lane from memory to the wave's 1 KB of shared memory at `to`; there behind the next barrier
+__device__ __forceinline__ void load_lds(const char* base, uint32_t offset, u32x4* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + offset), (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
-__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // two floats as the sum of two pairs of 16-bit numbers
 template <bool BF>
@@ -102,8 +97,7 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
   constexpr int NI = KT * CPR / kPfThreads;      // pieces of K (and of V) that a thread brings
   static_assert(KT * CPR % kPfThreads == 0 && kUnitKeys % KT == 0, "pieces");
   extern __shared__ uint32_t dyn[];
-  uint32_t* rows = dyn;
-  uint32_t* units = dyn + P.G + 1;
+  uint32_t* units = dyn;
   __shared__ u32x4 ksh[2][KT * D / 8], vsh[2][KT * D / 8];
   __shared__ float kscale[2][KT], vscale[2][KT];
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = uni(t / kWave);
@@ -130,51 +124,35 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
   const uint32_t k_page = (uint32_t)(ES * P.k_page), k_tok = (uint32_t)(ES * P.k_tok);
   const uint32_t v_page = (uint32_t)(ES * P.v_page), v_tok = (uint32_t)(ES * P.v_tok);
   const bool alike = k_page == v_page && k_tok == v_tok;
-  load_plan(P, kPrefix, rows, units);
-  Part* desc = reinterpret_cast<Part*>(P.desc);
+  for (int i = t; i <= P.G; i += kPfThreads) units[i] = (uint32_t)P.plan.group_units[i];   // none where the layout is bad
+  __syncthreads();
   const uint32_t U = (uint32_t)uni((int)units[P.G]), W = min((uint32_t)gridDim.x, U);
   // Neighbouring ranges on one die: blocks go to the eight dies in turn
   const uint32_t per_die = gridDim.x / 8;
   const uint32_t w = U >= gridDim.x && gridDim.x % 8 == 0 ? blockIdx.x % 8 * per_die + blockIdx.x / 8 : blockIdx.x;
-  if (w >= W) {
-    if (t == 0) desc[w].first_unit = -1;
-    return;
-  }
+  if (w >= W) return;
   uint32_t u = range_start(w, W, U);
   const uint32_t u_end = range_start(w + 1, W, U);
   int gi = 0;
   for (int step = 4096; step > 0; step >>= 1)
     if (gi + step < P.G && (uint32_t)uni((int)units[gi + step]) <= u) gi += step;
-  bool first_part = true;
   const float sl = fabsf(P.scale_log2);
   const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;       // the sign of the scale goes to the queries
   while (u < u_end) {
     while ((uint32_t)uni((int)units[gi + 1]) <= u) ++gi;
-    const int row0 = uni((int)rows[gi]), n = uni((int)rows[gi + 1]) - row0;
-    const int slot = uni(P.plan.group_slot[gi]), len = uni(P.plan.group_len[gi]);
+    const AttnRecord rec = P.plan.group[gi];
+    const int row0 = uni(rec.row0), n = uni(rec.n), slot = uni(rec.slot), len = uni(rec.len), tile0 = uni(rec.tile0);
     const int nblk = (len + kUnitKeys - 1) / kUnitKeys;
     const uint32_t rel = u - (uint32_t)uni((int)units[gi]);
     const int seg = (int)(rel / (uint32_t)nblk), b0 = (int)(rel - (uint32_t)seg * nblk);
     const int b1 = (int)min((uint32_t)nblk, b0 + (u_end - u));
     const int tiles = (n * P.group + TM - 1) / TM;
     const int head = seg / tiles, mb = seg - head * tiles;
-    if (first_part && t == 0) {
-      Part d;
-      d.first_unit = b0 > 0 ? (int)(u - b0) : -1;
-      d.end_unit = (int)(u - b0) + nblk;
-      d.row0 = row0;
-      d.n = n;
-      d.head = head;
-      d.mb = mb;
-      d.U = U;
-      d.W = W;
-      desc[w] = d;
-    }
+    if (b0 == 0 && t == 0) P.plan.tile[tile0 + mb * P.kv_heads + head] = make_int2((int)w, (int)(range_of(u + (uint32_t)nblk - 1, W, U) - w) + 1);
     const int nrow = min(TM, n * P.group - mb * TM);
     const bool busy = wv * 32 < nrow;            // this wave has rows
     const int r = wv * 32 + col;
     const int rr = mb * TM + (r < nrow ? r : 0), ri = rr / P.group;
-    const int64_t at = (int64_t)(row0 + ri) * P.heads + head * P.group + rr - ri * P.group;   // the row's place in the outputs
     u32x4 q[NS];
     {
       const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + ri) * P.q_row + (int64_t)(head * P.group + rr - ri * P.group) * P.q_head + 8 * h;
@@ -237,7 +215,6 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
     auto stage = [&](int buf, int pos) {
       if constexpr (C == codes::kNone) {
         if (pos + KT > len) {
-          loads_done();
           __syncthreads();                       // the values have come
           for (int i = (len - pos) * (D / 8) + t; i < KT * (D / 8); i += kPfThreads) vsh[buf][i] = u32x4{0u, 0u, 0u, 0u};
         }
@@ -266,7 +243,6 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
     load(0, pos0);                               // the last tile's keys have been read
     if (pos0 + KT < pos_end) names(pos0 + KT);
     stage(0, pos0);
-    loads_done();
     __syncthreads();
     int buf = 0;
     for (int pos = pos0; pos < pos_end; pos += KT, buf ^= 1) {
@@ -385,7 +361,6 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
         }
       }
       if (more) stage(buf ^ 1, pos + KT);
-      loads_done();
       __syncthreads();
     }
     // a lane's row: numbers 32 j + 8 i + 4 h .. + 3
@@ -394,8 +369,10 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
     if (__syncthreads_or(bad)) L = __builtin_nanf("");
     if (r < nrow) {
       const bool whole = b0 == 0 && b1 == nblk;
-      float* part = part_at(P, (int)w, b0 > 0 ? 0 : 1, TM, D);
-      float* to = whole ? P.state_o + at * D : part + r * D;
+      float* part = part_at(P.prefix_parts, (int)w, b0 > 0 ? 0 : 1, TM, D);
+      const int64_t at = state_row(P, row0, head, mb * TM + r);
+      float* to = whole ? P.state_o + at * 4 : part + r * 4;
+      const int64_t four = 4 * (whole ? (int64_t)P.total_rows * P.heads : TM);
       const float f = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -404,7 +381,7 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
           f32x4 v;
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = o[j][4 * i + k] * f;
-          *(f32x4*)(to + 32 * j + 8 * i + 4 * h) = v;
+          *(f32x4*)(to + (8 * j + 2 * i + h) * four) = v;
         }
       if (h == 0) {
         if (whole) {
@@ -415,7 +392,6 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
         }
       }
     }
-    first_part = false;
     u += (uint32_t)(b1 - b0);
   }
 }
@@ -423,18 +399,17 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
 namespace {
 
 template <bool BF, int D, int C>
-hipError_t launch_prefix_one(const AttnParams& p, int W, hipStream_t st) {
-  hipLaunchKernelGGL((k_prefix<BF, D, C>), dim3((unsigned)W), dim3(kPfThreads), (size_t)(p.G + 1) * 8, st, p);
-  hipError_t e = hipGetLastError();
-  return e == hipSuccess ? launch_attention_join(p, kPrefix, kPfRows, W, st) : e;
+hipError_t launch_prefix_one(const AttnParams& p, hipStream_t st) {
+  hipLaunchKernelGGL((k_prefix<BF, D, C>), dim3((unsigned)p.prefix_blocks), dim3(kPfThreads), (size_t)(p.G + 1) * 4, st, p);
+  return hipGetLastError();
 }
 
 template <int C>
-hipError_t launch_prefix_rows(const AttnParams& p, int W, hipStream_t st) {
+hipError_t launch_prefix_rows(const AttnParams& p, hipStream_t st) {
   switch (p.head_dim) {
-    case 64: return p.bf16 ? launch_prefix_one<true, 64, C>(p, W, st) : launch_prefix_one<false, 64, C>(p, W, st);
-    case 128: return p.bf16 ? launch_prefix_one<true, 128, C>(p, W, st) : launch_prefix_one<false, 128, C>(p, W, st);
-    case 256: return p.bf16 ? launch_prefix_one<true, 256, C>(p, W, st) : launch_prefix_one<false, 256, C>(p, W, st);
+    case 64: return p.bf16 ? launch_prefix_one<true, 64, C>(p, st) : launch_prefix_one<false, 64, C>(p, st);
+    case 128: return p.bf16 ? launch_prefix_one<true, 128, C>(p, st) : launch_prefix_one<false, 128, C>(p, st);
+    case 256: return p.bf16 ? launch_prefix_one<true, 256, C>(p, st) : launch_prefix_one<false, 256, C>(p, st);
   }
   return hipErrorInvalidValue;
 }

@@ -95,11 +95,40 @@ bool attention_shape(const char* who, const spec_verify_attention_args* a, int32
   return true;
 }
 
-// The layout of a call: its sequences', and its shared prefixes'.
+// The layout of a call.  With shared prefixes `tiles` is that of the sequences'
+// own parts where the kernel for many rows takes the groups' (of prefix_blocks
+// blocks), otherwise of groups and sequences together.
 struct AttnLayout {
-  AttnShape own, prefix;
+  AttnShape tiles;
   int32_t groups;
+  bool many;
+  int prefix_blocks;
+  AttnShape together;   // should `many` not do after all
 };
+
+bool shared_shape(const char* who, const spec_verify_attention_args* a, int32_t codes, AttnLayout* s) {
+  AttnShape own, prefix;
+  if (!attention_shape(who, a, codes, a->total_rows, a->batch, &own) ||
+      !attention_shape(who, a, codes, a->total_rows, s->groups, &prefix))
+    return false;
+  const int64_t group = a->heads / a->kv_heads;
+  const int64_t blocks = ((int64_t)a->max_pages * a->page_size + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys;
+  if (((int64_t)a->total_rows * group / 16 + a->batch + s->groups) * a->kv_heads * blocks > INT32_MAX) {
+    set_err("%s: batch, heads and max_pages are too large together", who);
+    return false;
+  }
+  // a tile's start is most of a short part's time: two blocks a CU overlap
+  own.blocks = std::max(own.blocks, a->head_dim == 256 ? 256 : 512);
+  s->together = own;
+  s->together.row_tiles = std::max(own.row_tiles, prefix.row_tiles);
+  s->together.part_bytes = std::max(own.part_bytes, prefix.part_bytes);
+  const int64_t avg = ((int64_t)a->total_rows * group + s->groups - 1) / s->groups;
+  s->many = avg > 48;
+  s->tiles = s->many ? own : s->together;
+  const int64_t units = ((int64_t)a->total_rows * group / sv::kAttnPrefixRows + s->groups) * a->kv_heads * blocks;
+  s->prefix_blocks = s->many ? (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : 512) : 0;
+  return true;
+}
 
 bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, const spec_verify_attention_options* o, AttnLayout* s) {
   if (!a) {
@@ -150,24 +179,13 @@ bool attention_sizes_ok(const char* who, const spec_verify_attention_args* a, co
     set_err("%s: a window (%d) hides the prefix that groups share; call without groups", who, a->window);
     return false;
   }
+  *s = AttnLayout{};
   s->groups = groups;
-  s->prefix = AttnShape{1, 0, 0};
   if (a->batch == 0) {
-    s->own = AttnShape{1, 1, 0};
+    s->tiles = AttnShape{1, 1, 0};
     return true;
   }
-  if (groups > 0) {
-    if (!attention_shape(who, a, codes, a->total_rows, groups, &s->prefix)) return false;
-    const int64_t avg = (int64_t)a->total_rows * (a->heads / a->kv_heads) / groups;
-    if (avg > 48) {
-      const int64_t units = ((int64_t)a->total_rows * (a->heads / a->kv_heads) / sv::kAttnPrefixRows + groups) * a->kv_heads *
-                            (((int64_t)a->max_pages * a->page_size + sv::kAttnUnitKeys - 1) / sv::kAttnUnitKeys);
-      s->prefix.row_tiles = sv::kAttnManyRows;
-      s->prefix.blocks = (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : 512);
-      s->prefix.part_bytes = 2 * (int64_t)sv::kAttnPrefixRows * (a->head_dim + 2) * 4;
-    }
-  }
-  return attention_shape(who, a, codes, a->total_rows, a->batch, &s->own);
+  return groups > 0 ? shared_shape(who, a, codes, s) : attention_shape(who, a, codes, a->total_rows, a->batch, &s->tiles);
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -179,35 +197,36 @@ bool strides_ok(int64_t a, int64_t b, int64_t c) {
   return true;
 }
 
-// Where a call's parts, records and (with groups) its plan and state lie in its
-// workspace; returns the bytes.  The stages run one after the other and share
-// the parts and records.
+// Where a call's parts, records and (with groups) its plan and states lie in its
+// workspace; returns the bytes.
 int64_t attention_workspace(const spec_verify_attention_args* a, const AttnLayout& l, char* base, sv::AttnParams* p) {
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     char* x = base + at;
-    at += bytes;
+    at += (int64_t)sv::align_up((size_t)bytes, 16);
     return x;
   };
-  auto ints = [&](int64_t n) { return reinterpret_cast<int32_t*>(take((int64_t)sv::align_up((size_t)n * 4, 16))); };
-  p->parts = reinterpret_cast<float*>(take(std::max(l.own.blocks * l.own.part_bytes, l.prefix.blocks * l.prefix.part_bytes)));
-  p->desc = take((int64_t)std::max(l.own.blocks, l.prefix.blocks) * sv::kAttnPartBytes);
-  if (l.groups == 0) return at;
+  if (l.groups == 0) {
+    p->parts = reinterpret_cast<float*>(take(l.tiles.blocks * l.tiles.part_bytes));
+    p->desc = take((int64_t)l.tiles.blocks * sv::kAttnPartBytes);
+    return at;
+  }
+  p->parts = reinterpret_cast<float*>(take(l.together.blocks * l.together.part_bytes));
   const int64_t B = a->batch, G = l.groups, rows = (int64_t)a->total_rows * a->heads;
+  p->prefix_parts = l.many ? reinterpret_cast<float*>(take(2 * (int64_t)l.prefix_blocks * sv::kAttnPrefixRows * (a->head_dim + 2) * 4)) : p->parts;
+  auto ints = [&](int64_t n) { return reinterpret_cast<int32_t*>(take(n * 4)); };
   sv::AttnPlan& n = p->plan;
   n.bad = ints(1);
-  n.rows = ints(B + 1);
-  n.units = ints(B + 1);
-  n.slot = ints(B);
-  n.len = ints(B);
-  n.first = ints(B);
-  n.flags = ints(B);
-  n.group_rows = ints(G + 1);
+  n.units = ints(G + B + 1);
   n.group_units = ints(G + 1);
-  n.group_slot = ints(G);
-  n.group_len = ints(G);
-  p->state_m = reinterpret_cast<float*>(ints(rows));
-  p->state_o = reinterpret_cast<float*>(take(rows * a->head_dim * 4));
+  n.group = reinterpret_cast<sv::AttnRecord*>(take((G + B) * (int64_t)sizeof(sv::AttnRecord)));
+  n.seq = n.group + G;
+  n.flags = ints(B);
+  n.row_seq = ints(a->total_rows);
+  // tiles have 16 rows at least; the last of a group's, or of a sequence's, may be cut
+  n.tile = reinterpret_cast<int2*>(take((2 * (rows / a->kv_heads / 16) + G + B) * a->kv_heads * (int64_t)sizeof(int2)));
+  p->state_m = reinterpret_cast<float*>(take(2 * rows * 4));
+  p->state_o = reinterpret_cast<float*>(take(2 * rows * a->head_dim * 4));
   return at;
 }
 
@@ -507,22 +526,35 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
   if (l.groups == 0) {
     e = (codes == SV_CODES_E4M3   ? sv::launch_attention_e4m3
          : codes == SV_CODES_INT8 ? sv::launch_attention_int8
-                                  : sv::launch_attention)(p, l.own.row_tiles, l.own.blocks, st);
+                                  : sv::launch_attention)(p, l.tiles.row_tiles, l.tiles.blocks, st);
   } else {
     p.G = l.groups;
     p.groups = o->groups;
     p.prefix_len = o->prefix_len;
-    auto stage = codes == SV_CODES_E4M3   ? sv::launch_attention_shared_e4m3
-                 : codes == SV_CODES_INT8 ? sv::launch_attention_shared_int8
-                                          : sv::launch_attention_shared;
-    // the kernel for many rows takes strides in bytes in 32 bits; the other one's parts are smaller
+    // the kernel for many rows takes strides in bytes in 32 bits
     const int64_t es = codes == SV_CODES_NONE ? 2 : 1;
     const int64_t most = std::max(std::max(a->k_page_stride, a->v_page_stride), a->page_size * std::max(a->k_token_stride, a->v_token_stride));
-    if (l.prefix.row_tiles == sv::kAttnManyRows && most * es > UINT32_MAX)
-      attention_shape(who, a, codes, a->total_rows, l.groups, &l.prefix);
-    e = sv::launch_attention_plan(p, 16 * l.own.row_tiles, l.prefix.row_tiles == sv::kAttnManyRows ? sv::kAttnPrefixRows : 16 * l.prefix.row_tiles, st);
-    if (e == hipSuccess) e = stage(p, sv::kAttnPrefix, l.prefix.row_tiles, l.prefix.blocks, st);
-    if (e == hipSuccess) e = stage(p, sv::kAttnOwn, l.own.row_tiles, l.own.blocks, st);
+    if (l.many && most * es > UINT32_MAX) {
+      l.many = false;
+      l.tiles = l.together;
+      p.prefix_parts = p.parts;
+    }
+    p.own_rows = 16 * l.tiles.row_tiles;
+    p.prefix_rows = l.many ? sv::kAttnPrefixRows : p.own_rows;
+    p.prefix_blocks = l.prefix_blocks;
+    p.group_entries = l.many ? 0 : l.groups;
+    p.entries = p.group_entries + a->batch;
+    p.plan.entry = l.many ? p.plan.seq : p.plan.group;
+    e = sv::launch_attention_plan(p, st);
+    if (e == hipSuccess && l.many)
+      e = (codes == SV_CODES_E4M3   ? sv::launch_attention_prefix_e4m3
+           : codes == SV_CODES_INT8 ? sv::launch_attention_prefix_int8
+                                    : sv::launch_attention_prefix)(p, st);
+    if (e == hipSuccess)
+      e = (codes == SV_CODES_E4M3   ? sv::launch_attention_shared_e4m3
+           : codes == SV_CODES_INT8 ? sv::launch_attention_shared_int8
+                                    : sv::launch_attention_shared)(p, l.tiles.row_tiles, l.tiles.blocks, st);
+    if (e == hipSuccess) e = sv::launch_attention_merge(p, st);
   }
   if (e != hipSuccess) return hip_fail(who, e);
   return SV_OK;
