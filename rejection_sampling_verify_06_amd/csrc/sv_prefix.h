@@ -87,6 +87,10 @@ constexpr int kPfKeys = D == 256 ? 32 : 64;      // keys staged at a time
 template <bool BF, int D, int C>
 __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnParams P) {
   constexpr bool PB = BF || C != codes::kNone;   // the second product's type
+  // Weights need not stay below 1: two bfloat16 hold 2^8 as well as 1, float16
+  // (weights against the maximum less 14) ends at 2^16.  Without it 32 rows find a
+  // new maximum in some two of three steps.
+  constexpr float kSlack = PB ? 8.f : 1.f;
   constexpr int ES = C != codes::kNone ? 1 : 2;
   constexpr int KT = kPfKeys<D>;
   constexpr int TM = kPfRows;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
 #pragma unroll
           for (int i = 0; i < 16; ++i) top = fmaxf(top, s[a][i]);
         if constexpr (C == codes::kNone) top *= sl;
-        if (__ballot(top > mx)) {                // a new maximum in some row: rescale
+        if (__ballot(top > mx + kSlack)) {       // far above what some row's weights are taken against: rescale
           const float nm = fmaxf(mx, pair_max(top));
           const float f = mx == nm ? 1.f : at_exp2(reference<PB>(mx) - reference<PB>(nm));
           mx = nm;
