@@ -326,7 +326,7 @@ __device__ __forceinline__ int64_t state_row(const AttnParams& P, int row0, int 
 
 // S: with shared prefixes, whose plan is in the workspace
 template <bool BF, int D, int MT, int C, bool S>
-__global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 ? 3 : 4) : D * MT <= 256 && D < 256 ? 2 : 1) k_attention(AttnParams P) {
+__global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNone || (D * MT <= 256 && D < 256) ? 2 : 1) k_attention(AttnParams P) {
   constexpr bool PB = BF || C != codes::kNone;   // the second product's type
   constexpr int ES = C != codes::kNone ? 1 : 2;  // bytes of a cached number
   constexpr int TM = 16 * MT;                    // rows of a tile
@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
   constexpr int VW = NJ * ES / 4;                // dwords of those
   constexpr int NL = D * ES / 64;                // 16-byte loads of a lane's part of a key
+  constexpr bool kTight = C != codes::kNone && D * MT > 256;   // registers are short
   extern __shared__ uint32_t dyn[];
   const int nseq = S ? P.entries : P.B;
   uint32_t* rows = dyn;                          // not with S
@@ -508,7 +509,8 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
     auto load_v = [&]() {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const char* p = vb[e >> 2] + (uint32_t)ES * ((uint32_t)(4 * g + (e & 3)) * (uint32_t)P.v_tok + (uint32_t)NJ * col);
+        const char* p = !kTight ? vb[e >> 2] + (uint32_t)ES * ((uint32_t)(4 * g + (e & 3)) * (uint32_t)P.v_tok + (uint32_t)NJ * col)
+                                          : vb[e >> 2] + (e & 3) * (int64_t)P.v_tok + (4u * g * (uint32_t)P.v_tok + (uint32_t)NJ * col);
         if constexpr (VW == 1) {
           vr[e][0] = *(const uint32_t*)p;
         } else if constexpr (VW == 2) {
@@ -557,6 +559,11 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
             }
           }
       } else {
+        // Else the codes are unpacked where they were loaded, which waits for them there.
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < NL; ++s) asm volatile("" : "+v"(kr[h][s]));
 #pragma unroll
         for (int m = 0; m < MT; ++m) sc[m][0] = sc[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -565,11 +572,11 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
           for (int s = 0; s < NS; ++s) {
             const u32x4 a = widen8<BF, C>(kr[h][s >> 1][2 * (s & 1)], kr[h][s >> 1][2 * (s & 1) + 1]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              if (m == 0 || m * 16 < nrow) sc[m][h] = mfma<BF>(a, qs[m][s][lane], sc[m][h]);
+            for (int m = 0; m < MT; ++m) sc[m][h] = mfma<BF>(a, qs[m][s][lane], sc[m][h]);
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) kf[h][r] = ksc[h][r] * P.scale_log2;
+          if (kTight) __builtin_amdgcn_sched_barrier(0);
         }
       }
       if (more) {
@@ -596,7 +603,10 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
       u32x4 ph[MT], pl[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        if (m > 0 && m * 16 >= nrow) continue;
+        if (m > 0 && m * 16 >= nrow) {
+          if constexpr (C != codes::kNone) ph[m] = pl[m] = u32x4{0u, 0u, 0u, 0u};
+          continue;
+        }
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] = sc[m][e >> 2][e & 3] * (C == codes::kNone ? P.scale_log2 : kf[e >> 2][e & 3]);
@@ -638,6 +648,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
           ph[m][i] = pack16<PB>(p[2 * i], p[2 * i + 1]);
           pl[m][i] = pack16<PB>(p[2 * i] - lo16<PB>(ph[m][i]), p[2 * i + 1] - hi16<PB>(ph[m][i]));
         }
+        if (kTight) __builtin_amdgcn_sched_barrier(0);
       }
       // The schedule that the compiler takes without this holds up to 16
       // registers more: two float16 tiles of 128 spilled two (134 us, 133 with it).
@@ -719,11 +730,10 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? (C == codes::kInt8 
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              if (m == 0 || m * 16 < nrow) {
-                o[m][4 * c + i] = mfma<true>(a[i], ph[m], o[m][4 * c + i]);
-                o[m][4 * c + i] = mfma<true>(a[i], pl[m], o[m][4 * c + i]);
-              }
+            for (int m = 0; m < MT; ++m) {
+              o[m][4 * c + i] = mfma<true>(a[i], ph[m], o[m][4 * c + i]);
+              o[m][4 * c + i] = mfma<true>(a[i], pl[m], o[m][4 * c + i]);
+            }
         }
       }
       if (more) load_v();

@@ -89,7 +89,7 @@ bool attention_shape(const char* who, const spec_verify_attention_args* a, int32
   // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
   int per_cu = 1;
   if (a->head_dim == 64) per_cu = s->row_tiles == 1 ? 4 : 2;
-  else if (a->head_dim == 128 && (avg > 48 || codes != SV_CODES_NONE)) per_cu = 2;
+  else if (codes != SV_CODES_NONE || (a->head_dim == 128 && avg > 48)) per_cu = 2;
   s->blocks = (int)std::min<int64_t>(units, 256 * per_cu);
   s->part_bytes = 2 * tm * (a->head_dim + 2) * 4;
   return true;
