@@ -712,7 +712,6 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                if (m > 0 && m * 16 >= nrow) continue;
                 f32x4 d = mfma<true>(a[i], ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
                 d = mfma<true>(a[i], pl[m], d);
 #pragma unroll
