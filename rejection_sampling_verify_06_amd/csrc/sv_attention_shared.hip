@@ -18,31 +18,41 @@ namespace sv {
 
 namespace {
 
-// Rows or groups that do not add up, found by every block for itself.
-__device__ __forceinline__ bool layout_bad(const AttnParams& P) {
+// Rows or groups that do not add up, found by every block for itself; and, on
+// the way, the rows in front of sequence b and its group.
+struct Layout {
+  bool bad;
+  int row0, group;
+};
+__device__ __forceinline__ Layout layout(const AttnParams& P, int b) {
   __shared__ unsigned long long sum;
-  __shared__ int bad;
+  __shared__ int bad, row0, group;
   const int t = threadIdx.x;
   if (t == 0) {
     sum = 0;
-    bad = 0;
+    bad = row0 = group = 0;
   }
   __syncthreads();
   unsigned long long r = 0;
-  bool b = false;
+  uint32_t before = 0;
+  bool f = false;
   for (int i = t; i < P.B; i += kAtThreads) {
     const int K = P.num_draft[i];
-    b |= K < 0 || K >= P.total_rows;
-    r += (unsigned)max(K, 0) + 1u;
+    f |= K < 0 || K >= P.total_rows;
+    const uint32_t n = (uint32_t)max(K, 0) + 1u;
+    r += n;
+    if (i < b) before += n;
   }
   for (int g = t; g < P.G; g += kAtThreads) {
     const int a = P.groups[g], e = P.groups[g + 1];
-    b |= a < 0 || e < a || e > P.B || (g == 0 && a != 0) || (g == P.G - 1 && e != P.B);
+    f |= a < 0 || e < a || e > P.B || (g == 0 && a != 0) || (g == P.G - 1 && e != P.B);
+    if (a <= b && b < e) group = g;              // one thread's, where the groups are in order
   }
-  if (b) bad = 1;
-  atomicAdd(&sum, r);
+  if (f) bad = 1;
+  if (r) atomicAdd(&sum, r);
+  if (before) atomicAdd(&row0, (int)before);
   __syncthreads();
-  return bad || sum != (unsigned long long)P.total_rows;
+  return Layout{bad || sum != (unsigned long long)P.total_rows, row0, group};
 }
 
 // What can be said of sequence b without its pages: its slot and length, 0 or SV_ST_*.
@@ -77,26 +87,20 @@ __device__ __forceinline__ Seq seq_check(const AttnParams& P, int b, int prefix,
 __global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P) {
   extern __shared__ uint32_t dyn[];
   __shared__ uint32_t tw[kAtWaves];
-  __shared__ int shared_g, shared_st, shared_row;
+  __shared__ int shared_st;
   const int t = threadIdx.x, lane = t & (kWave - 1), wv = t / kWave;
-  const bool bad = layout_bad(P);
-  if (blockIdx.x > 0) {
-    const int b = (int)blockIdx.x - 1;
+  const int b = (int)blockIdx.x - 1;
+  if (t == 0) shared_st = 0;
+  const Layout at = layout(P, b);
+  const bool bad = at.bad;
+  if (b >= 0) {
     if (bad) {
       if (t == 0 && P.status) P.status[b] = SV_ST_BAD_LAYOUT;
       return;
     }
-    if (t == 0) shared_st = shared_row = 0;
-    __syncthreads();
-    int before = 0;                              // rows of the sequences in front
-    for (int i = t; i < b; i += kAtThreads) before += P.num_draft[i] + 1;
-    if (before) atomicAdd(&shared_row, before);
-    for (int g = t; g < P.G; g += kAtThreads)
-      if (P.groups[g] <= b && b < P.groups[g + 1]) shared_g = g;
-    __syncthreads();
-    const int row0 = shared_row, n = P.num_draft[b] + 1;
-    for (int i = t; i < n; i += kAtThreads) P.plan.row_seq[row0 + i] = b;
-    const int prefix = P.prefix_len[shared_g], lead = P.groups[shared_g];
+    const int n = P.num_draft[b] + 1;
+    for (int i = t; i < n; i += kAtThreads) P.plan.row_seq[at.row0 + i] = b;
+    const int prefix = P.prefix_len[at.group], lead = P.groups[at.group];
     const Seq l = seq_check(P, lead, prefix, true), s = seq_check(P, b, prefix, false);
     int st = s.status | l.status;
     if (!st) {
@@ -104,9 +108,18 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_plan(AttnParams P) {
       const int32_t* theirs = P.table + (int64_t)l.slot * P.table_stride;
       const int mask = (1 << P.page_log2) - 1, whole = prefix >> P.page_log2;
       int f = 0;
-      for (int i = t; i < whole; i += kAtThreads) {
-        const int id = theirs[i];
-        if (id != mine[i] || (unsigned)id >= (unsigned)P.num_pages) f = SV_ST_BAD_PAGE;
+      // loads of eight pages of both at once: one at a time 2048 pages took 11.5 us
+      for (int i = t; i < whole; i += 8 * kAtThreads) {
+        int a[8], e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int at = min(i + k * kAtThreads, whole - 1);
+          a[k] = theirs[at];
+          e[k] = mine[at];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (a[k] != e[k] || (unsigned)a[k] >= (unsigned)P.num_pages) f = SV_ST_BAD_PAGE;
       }
       if (t == 0 && (prefix & mask) && (unsigned)theirs[whole] >= (unsigned)P.num_pages) f = SV_ST_BAD_PAGE;
       const int end = (s.len + mask) >> P.page_log2;
@@ -251,6 +264,10 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
   const int row = (in ? X : 0) / P.group, hh = (in ? X : 0) - row * P.group;
   const int64_t at = (int64_t)row * P.heads + head * P.group + hh;
   const bool bad = *P.plan.bad != 0;
+  // loaded beside `bad`: where the layout is, it may be anything
+  const int b = min((unsigned)P.plan.row_seq[row], (unsigned)P.B - 1u);
+  const AttnRecord rec = P.plan.seq[b];
+  const int flags = P.plan.flags[b];
   f32x4 acc[GN];
   float M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -258,9 +275,6 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
   if (bad) {
     L = __builtin_nanf("");
   } else {
-    const int b = P.plan.row_seq[row];
-    const AttnRecord rec = P.plan.seq[b];
-    const int flags = P.plan.flags[b];
     const int R = (row - rec.row0) * P.group + hh, mb = R / P.own_rows;
     const int pR = R + rec.group_row * P.group, pmb = pR / P.prefix_rows;
     const int2 mine = P.plan.tile[rec.tile0 + mb * P.kv_heads + head];
@@ -272,39 +286,37 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
     for (int k0 = 0; k0 < most; k0 += kBatch) {
       float m[kBatch], l[kBatch];
       f32x4 v[kBatch][GN];
+      uint32_t wholes = 0;                       // looked at behind all loads: here it would wait for each
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        if (k0 + i >= parts) continue;
-        const bool own = k0 + i < mine.y;
-        const int k = own ? k0 + i : k0 + i - mine.y;
+        if (k0 + i >= most) break;
+        // No branch here depends on the lane: a register written on one side and
+        // loaded on the other is waited for.  Lanes out of parts load again.
+        const int kk = min(k0 + i, max(parts - 1, 0));
+        const bool own = kk < mine.y;
+        const int k = own ? kk : kk - mine.y;
         const int2 tile = own ? mine : theirs;
         const int tm = own ? P.own_rows : P.prefix_rows, r = own ? R - mb * P.own_rows : pR - pmb * P.prefix_rows;
-        const float *pm, *po;
-        int64_t four;
-        if (tile.y == 1) {
-          pm = P.state_m + (own ? total : 0) + sr;
-          po = P.state_o + ((own ? total * (D / 4) : 0) + sr) * 4;
-          four = 4 * total;
-          l[i] = 1.f;
-        } else {
-          const float* part = part_at(own ? P.parts : P.prefix_parts, tile.x + k, k == 0 ? 1 : 0, tm, D);
-          pm = part + tm * D + r;
-          po = part + r * 4;
-          four = 4 * tm;
-          l[i] = pm[tm];
-        }
+        const bool whole = tile.y == 1;
+        const float* part = part_at(own ? P.parts : P.prefix_parts, tile.x + k, k == 0 ? 1 : 0, tm, D);
+        const float* pm = whole ? P.state_m + (own ? total : 0) + sr : part + tm * D + r;
+        const float* po = whole ? P.state_o + ((own ? total * (D / 4) : 0) + sr) * 4 : part + r * 4;
+        const int64_t four = 4 * (whole ? total : (int64_t)tm);
         m[i] = *pm;
+        l[i] = pm[whole ? 0 : tm];
+        wholes |= (uint32_t)whole << i;
 #pragma unroll
         for (int j = 0; j < GN; ++j) v[i][j] = *(const f32x4*)(po + (four0 + j) * four);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         // a tile in which the row saw nothing has m = -inf or l = 0
-        if (k0 + i >= parts || m[i] == -INFINITY || l[i] == 0.f) continue;
+        const float li = (wholes >> i & 1) ? 1.f : l[i];
+        if (k0 + i >= parts || m[i] == -INFINITY || li == 0.f) continue;
         const float nm = fmaxf(M, m[i]);
         const float f0 = M == nm ? 1.f : at_exp2(M - nm), f1 = m[i] == nm ? 1.f : at_exp2(m[i] - nm);
         M = nm;
-        L = L * f0 + l[i] * f1;
+        L = L * f0 + li * f1;
 #pragma unroll
         for (int j = 0; j < GN; ++j)
 #pragma unroll
