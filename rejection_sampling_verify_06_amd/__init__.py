@@ -599,9 +599,9 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
     with _on_stream(dev, stream, q, k_pages, v_pages, page_table, seq_len, num_draft, seqs, start, k_scale, v_scale, groups,
                     prefix_len):
         out = {
-            "out": torch.empty((N, H, D), dtype=q.dtype, device=dev),
+            "out": q.new_empty((N, H, D)),
             "lse": torch.empty((N, H), dtype=torch.float32, device=dev) if want_lse else None,
-            "status": torch.empty(B, dtype=torch.int32, device=dev) if want_status else None,
+            "status": num_draft.new_empty(B) if want_status else None,
         }
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         a.out, a.lse, a.status = out["out"].data_ptr(), _ptr(out["lse"]), _ptr(out["status"])
@@ -613,15 +613,16 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_len, num_draft, *, seqs
 def _rope_rows(t, name, dtype, dev, rows, torch, heads=None):
     """A [rows, heads, head_dim] tensor with unit stride in its last
     dimension: its strides of row and head (0 where the dimension is 1)."""
-    if t.dim() != 3 or t.shape[0] != rows or (heads is not None and tuple(t.shape[1:]) != heads):
-        raise ValueError(f"{name} must be [{rows}, {'heads, head_dim' if heads is None else f'{heads[0]}, {heads[1]}'}], got {tuple(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != rows or (heads is not None and shape[1:] != heads):
+        raise ValueError(f"{name} must be [{rows}, {'heads, head_dim' if heads is None else f'{heads[0]}, {heads[1]}'}], got {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.stride(2) != 1:
+    if stride[2] != 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return t.stride(0) if rows > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    return stride[0] if rows > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
 def _qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, stream, cache=None, layer=0, v=None, slots=None):
@@ -639,18 +640,17 @@ def _qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, interleave
     vs = (0, 0) if v is None else _rope_rows(v, "v", q.dtype, dev, N, torch, (KV, D))
     _need(positions, "positions", (torch.int32,), torch, N, dev)
     _need(inv_freq, "inv_freq", (torch.float64,), torch, None, dev)
-    weights = [w for w in (q_weight, k_weight) if w is not None]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(w, name, (q.dtype, torch.float32), torch, D, dev)
-    if len({w.dtype for w in weights}) > 1:
+    _need(q_weight, "q_weight", (q.dtype, torch.float32), torch, D, dev)
+    _need(k_weight, "k_weight", (q.dtype, torch.float32), torch, D, dev)
+    weight = k_weight if q_weight is None else q_weight
+    if weight is not None and k_weight is not None and weight.dtype != k_weight.dtype:
         raise TypeError(f"q_weight is {q_weight.dtype}, k_weight {k_weight.dtype}")
     _need(slots, "slots", (torch.int64,), torch, N, dev)
     with _on_stream(dev, stream, q, k, v, positions, inv_freq, q_weight, k_weight, slots):
-        out = {"q": torch.empty((N, H, D), dtype=q.dtype, device=dev),
-               "k": torch.empty((N, KV, D), dtype=q.dtype, device=dev) if cache is None else None}
+        out = {"q": q.new_empty((N, H, D)), "k": q.new_empty((N, KV, D)) if cache is None else None}
         a = _lib.SpecVerifyRopeArgs(
             N, H, KV, D, _int32(2 * inv_freq.numel(), "rotary"), int(bool(interleaved)), dt,
-            SV_F32 if weights and weights[0].dtype == torch.float32 else dt, _int32(layer, "layer"), float(eps),
+            SV_F32 if weight is not None and weight.dtype == torch.float32 else dt, _int32(layer, "layer"), float(eps),
             q.data_ptr(), *qs, k.data_ptr(), *ks, _ptr(v), *vs, positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight),
             _ptr(k_weight), out["q"].data_ptr(), _ptr(out["k"]), _ptr(slots))
         _check(lib.spec_verify_qk_norm_rope(ctypes.byref(a), None if cache is None else cache._ref,
@@ -835,7 +835,7 @@ class PagedCache:
             shape = (max(n, 0), *self._heads)
             out = {"k": torch.empty(shape, dtype=self.dtype, device=self.device),
                    "v": torch.empty(shape, dtype=self.dtype, device=self.device),
-                   "status": torch.empty(B, dtype=torch.int32, device=self.device)}
+                   "status": first.new_empty(B)}
             _check(self._lib.spec_verify_cache_read(
                 self._ref, self._codes, SV_BF16 if self.dtype == torch.bfloat16 else SV_F16, _int32(layer, "layer"), B, _ptr(seqs),
                 first.data_ptr(), count.data_ptr(), n, _ptr(out["k"]), _ptr(out["v"]), _ptr(out["status"]), _queue(self.device)))
