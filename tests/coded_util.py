@@ -142,3 +142,28 @@ def make_shared(groups, P, KV, D, dtype, quant, seed, extra=3):
     def i32(x):
         return torch.tensor(x, dtype=torch.int32).cuda()
     return dev, ref, table.cuda(), i32(L), i32(first.tolist()), i32([p for p, _ in groups])
+
+
+def ramp_keys(pools, ref, table, seq_len, P, quant, falling=False, top=3.0):
+    """The first number of every key becomes 0 .. top by its position (or top ..
+    0), in the pools and in what they stand for: scores that grow or fall."""
+    L = int(seq_len.max())
+    table, k = table.cpu().long(), pools[0].cpu()
+    for b, n in enumerate(seq_len.tolist()):
+        pos = torch.arange(n)
+        page, off = table[b, pos // P], pos % P
+        r = ((L - 1 - pos if falling else pos).double() * (top / L))[:, None]
+        if quant is None:
+            v = r.to(k.dtype).expand(n, k.shape[1])
+            k[page, :, off, 0] = v
+            ref[0][page, :, off, 0] = v.double()
+        else:
+            s = pools[1].cpu()[page, :, off].double()
+            if quant == E4M3:
+                c = (r / s).clamp(max=448.0).to(torch.float8_e4m3fn)
+                k.view(torch.uint8)[page, :, off, 0] = c.view(torch.uint8)
+            else:
+                c = (r / s).clamp(max=127.0).round().to(torch.int8)
+                k[page, :, off, 0] = c
+            ref[0][page, :, off, 0] = c.double() * s
+    pools[0].copy_(k)

@@ -144,6 +144,44 @@ def test_what_a_row_does_not_see(sv, quant, dtype, D):
         assert torch.isnan(got[..., 5]).all() if what == "code" else not torch.isfinite(got).any() or what == "inf"
 
 
+@pytest.mark.parametrize("quant,dtype", KINDS)
+@pytest.mark.parametrize("heads", [2, 8])
+def test_many_rows_next_to_few(sv, heads, quant, dtype):
+    """Two and three row tiles, of which some sequences leave the higher ones
+    empty; then a value without a number (or its scale) at the last new token,
+    which only the last rows see."""
+    L, nd, P = [290, 70, 9, 300], [7, 0, 1, 8], 16
+    pools, ref, table, seq_len = cu.make_coded_pages(L, P, 2, 128, dtype, quant, 12)
+    N = sum(n + 1 for n in nd)
+    q = _q(N, heads, 128, dtype, 12)
+    want = su.attention_ref(q, *ref, table, seq_len, _i32(nd))
+    _near(_call(sv, q, pools, table, seq_len, nd), want, dtype)
+    _near(_call(sv, q, pools, table, seq_len, nd, window=40), su.attention_ref(q, *ref, table, seq_len, _i32(nd), window=40), dtype)
+    last = [7, 8, 10, 19]
+    for b, n in enumerate(L):
+        p = table[b, (n - 1) // P].long()
+        if quant == cu.E4M3:
+            pools[2].view(torch.uint8)[p, :, (n - 1) % P, 77] = 0x7F
+        else:
+            pools[3][p, :, (n - 1) % P] = torch.nan
+    o = _call(sv, q, pools, table, seq_len, nd)
+    _near(o, want, dtype, [i for i in range(N) if i not in last])
+    assert torch.isnan(o["out"][last][..., 77]).all()
+
+
+@pytest.mark.parametrize("quant,dtype", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("falling", [False, True])
+def test_scores_that_grow_or_fall(sv, falling, D, quant, dtype):
+    """As the test of that name for shared prefixes, which has the errors."""
+    for nd, L in (([8, 0, 7], [1500, 40, 900]), ([0], [1500])):
+        made = cu.make_coded_pages(L, 32, 1, D, dtype, quant, 32)
+        cu.ramp_keys(*made, 32, quant, falling)
+        q = _q(sum(n + 1 for n in nd), 4, D, dtype, 32)
+        q[:, :, 0] = 200.0
+        _near(_call(sv, q, made[0], made[2], made[3], nd), su.attention_ref(q, *made[1], made[2], made[3], _i32(nd)), dtype)
+
+
 @pytest.mark.parametrize("quant", [cu.E4M3, cu.INT8])
 def test_rows_that_see_nothing(sv, quant):
     o = _run(sv, [0, 3, 40, 0], [0, 5, 2, 3], 8, 2, 128, 16, torch.bfloat16, quant, seed=9)

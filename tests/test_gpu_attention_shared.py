@@ -139,6 +139,26 @@ def test_sharp_softmax_and_scales(sv):
 
 
 @pytest.mark.parametrize("quant,dtype", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("falling", [False, True])
+def test_scores_that_grow_or_fall(sv, falling, D, quant, dtype):
+    """Along 1500 keys the scores grow (or fall) by some 3 * 200 / sqrt(D) = 37 to
+    75, a few units with every tile, so that the rows' maximum moves many times,
+    now by less and now by more than what the weights may grow by; many rows
+    (tiles of 128) and few.  A score's float32 sum is off by some 8 * 600 * 2^-24
+    before the scale of at most 1 / 8, a weight by 2^-14 of itself."""
+    for own, group in (([30, 9, 50] * 7, 4), ([30, 9], 1)):
+        made = cu.make_shared([(1500, own)], 32, 1, D, dtype, quant, 31)
+        cu.ramp_keys(made[0], made[1], made[2], made[3], 32, quant, falling)
+        nd = [i % 4 for i in range(len(own))]
+        q = _q(sum(n + 1 for n in nd), group, D, dtype, 31)
+        q[:, :, 0] = 200.0
+        o = _call(sv, q, made, nd)
+        assert not o["status"].any()
+        _near(o, su.attention_ref(q, *made[1], made[2], made[3], _i32(nd)), dtype)
+
+
+@pytest.mark.parametrize("quant,dtype", KINDS)
 def test_what_is_not_finite(sv, quant, dtype):
     """A key of the prefix, then one of a sequence's own, that is not finite:
     the rows that see it are not, the others stay what they are."""
