@@ -84,7 +84,9 @@ bool attention_shape(const char* who, const spec_verify_attention_args* a, int32
   // 97 + 4 us, with two 101 + 9; ragged 126 + 6 and 128 + 8, with four 132 +
   // 10); heads of 64, and tiles that read the keys again, want two (64
   // sequences of 4096 with 8 heads of 64: 96 and 94 us; 64 rows of 128: 156 and
-  // 113).  One row tile of 64 leaves room for four, which hide each other's
+  // 113), and so do codes, whose unpacking one wave a SIMD does not hide (16
+  // sequences of up to 20000 with heads of 256, one and two: 55 and 52 us, 40
+  // sequences 88 and 82; 33 units a sequence 34.2 and 34.6).  One row tile of 64 leaves room for four, which hide each other's
   // changes from tile to tile (256 ragged sequences of 125 to 1000 tokens, 16
   // heads: 140 + 6 us with two, 126 + 7 with four, 124 + 9 with eight in turn).
   int per_cu = 1;
@@ -123,9 +125,17 @@ bool shared_shape(const char* who, const spec_verify_attention_args* a, int32_t 
   s->together.row_tiles = std::max(own.row_tiles, prefix.row_tiles);
   s->together.part_bytes = std::max(own.part_bytes, prefix.part_bytes);
   const int64_t avg = ((int64_t)a->total_rows * group + s->groups - 1) / s->groups;
-  s->many = avg > 48;
-  s->tiles = s->many ? own : s->together;
   const int64_t units = ((int64_t)a->total_rows * group / sv::kAttnPrefixRows + s->groups) * a->kv_heads * blocks;
+  // The kernel for many rows (tiles of 128) has its own launch and adds its parts
+  // to the merge's; k_attention reads the keys once for each 16 to 48 rows, and
+  // spills nothing of codes.  8 groups behind 8000 tokens, 8 key heads of 128, whole
+  // call, k_attention and this one: 14 rows of a group and key head 55 and 60 us, 24
+  // 94 and 77, 28 84 and 65, 56 106 and 77; heads of 256 28 118 and 93; but heads
+  // of 64 28 47 and 51, 42 46 and 56, 56 60 and 58, e4m3 42 64 and 72, 56 88 and 79,
+  // int8 of 256 42 115 and 138, 84 186 and 155.  One group behind 2000 tokens is
+  // latency alone: 32 rows 26 and 33; behind 30000 62 and 62.
+  s->many = avg > 48 || (codes == SV_CODES_NONE && a->head_dim >= 128 && avg > 16 && units >= 2048);
+  s->tiles = s->many ? own : s->together;
   s->prefix_blocks = s->many ? (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : 512) : 0;
   return true;
 }

@@ -119,6 +119,12 @@ def test_long_prefix(sv, quant):
     _run(sv, [(9000, [9] * 30)], [8] * 30, 8, 2, 64, 16, torch.float16, quant, seed=6)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_few_rows_behind_long_prefixes(sv, dtype):
+    """20 to 24 rows of a key head in the tiles made for many."""
+    _run(sv, [(9000, [5, 9, 3]), (8001, [7, 2])], [1, 2, 0, 3, 0], 64, 16, 128, 16, dtype, seed=8)
+
+
 def test_sharp_softmax_and_scales(sv):
     """Rows whose weight lies all in the prefix, or all in their own part."""
     _run(sv, [(500, [20, 3])], [2, 1], 4, 1, 64, 16, torch.float16, seed=3, std=4.0)
