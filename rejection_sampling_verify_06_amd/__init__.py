@@ -10,8 +10,9 @@ current stream.  PyTorch supplies device memory and streams.
     out["accepted_len"], out["emitted"], out["p_at"], out["q_at"], out["status"]
 
 Around a decode loop's verify call: ``PagedCache`` (the target's keys and
-values, with ``paged_attention`` over them) and ``token_logprobs`` (of what
-was emitted).
+values in 16 or 8 bits, with ``paged_attention`` over them, also of sequences
+that share a prefix), ``qk_norm_rope`` (queries and keys normed and rotated) and
+``token_logprobs`` (of what was emitted).
 
 If the library has not been built, every entry point raises ``LibraryMissing``:
 there is no fallback implementation.

@@ -1,7 +1,6 @@
 // The kernels of attention over a paged key-value cache, for gfx950 (internal;
 // instantiated by sv_attention*.hip).
 //
-//
 // Sequence b brings n = num_draft[b] + 1 query rows (packed like a verify
 // call's target rows; n = 1 is plain decoding) and holds L = seq_len[b]
 // tokens in its pages, the new ones among them.  Row i sees positions
@@ -52,7 +51,16 @@
 // products of the queries with the codes, times the key's scale; the values'
 // scales go into the weights in front of their split, and codes are bfloat16
 // numbers exactly, also where the queries are float16 (whose range a weight
-// times a scale would leave).
+// times a scale would leave).  Half the bytes leave less time to hide the
+// unpacking in, so two waves share a SIMD everywhere, and three row tiles go
+// without branches between their products: 36 rows over int8 226 us with one
+// wave a SIMD, 134 with two; 24 and 36 rows over e4m3 85 and 124 us with branches
+// where codes without a number are looked for, which spilled, 81 and 100 without.
+// Measured: 32 sequences of 1024 to 8192, up to 24 rows, e4m3 76 + 8 us (300 MB,
+// 4.0 TB/s), of which a tile's start and end take some 10; 98925 and 116850
+// tokens with 16 and 36 rows, int8 under float16 134 + 8 us (456 MB, 3.4 TB/s:
+// products, unpacking and softmax of 36 rows take as long as the reads); 16 sequences in a
+// window of 4096, heads of 256, 28 + 6 us; one token of 777, 8 + 4 us.
 //
 // With shared prefixes (S) the kernel's entries are groups, whose rows are those
 // of all members and whose keys are the prefix, and sequences, whose keys begin
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
   constexpr int NJ = D / 16;                     // 16-row tiles of O^T; also a lane's elements of a V row
   constexpr int VW = NJ * ES / 4;                // dwords of those
   constexpr int NL = D * ES / 64;                // 16-byte loads of a lane's part of a key
-  constexpr bool kTight = C != codes::kNone && D * MT > 256;   // registers are short
+  constexpr bool kTight = C != codes::kNone && D * MT > 256;   // registers are short: the order of stages is kept
   extern __shared__ uint32_t dyn[];
   const int nseq = S ? P.entries : P.B;
   uint32_t* rows = dyn;                          // not with S

@@ -11,6 +11,13 @@
 //   tiles    each sequence's tokens behind its prefix, and groups of few rows over
 //            theirs (k_attention)
 //   merge    of all that belongs to a row
+//
+// Measured on one MI355X (rocprofv3, plan + prefix + tiles + merge): 4 branches of
+// 2000 tokens 5 + 9 + 8 us; 64 sequences behind 32768 tokens 10 + 205 + 30 + 12 us
+// (one by one, without groups, 64 times the prefix's bytes: 1.7 ms at 5 TB/s); 8 groups
+// of 8 behind 8000 over e4m3 8 + 50 + 31 + 12 us.  Plan and merge are chains of loads: the
+// merge's 17 parts a row took 14 us with one load after the other, 8.5 with eight parts'
+// under way; 12 us of 64 sequences' merge are its 50 MB of parts.
 
 #include "sv_prefix.h"
 
