@@ -18,8 +18,8 @@
 // heads, so that a lane's 8 angles serve all of them.
 //
 // Measured on one MI355X (rocprofv3): 9101 prompt rows of 32 + 8 + 8 heads of 128
-// into a 16-bit cache 47 us (224 MB, 4.8 TB/s); a round's 138 rows 5 us, a chain of
-// loads, sines and stores.  As int8 codes a layer's 6905 rows are written in 13 us
+// into a 16-bit cache 41 us (224 MB, 5.5 TB/s); a round's 138 rows 5 us, a chain of
+// loads, sines and stores.  As int8 codes a layer's 6905 rows are written in 12.5 us
 // and read back in 13 (43 MB each, 3.3 TB/s; more blocks, or 32-bit divisions, changed
 // nothing); a round's in 3.7 and 5.
 
@@ -382,8 +382,13 @@ hipError_t launch_read_type(const CacheReadParams& p, hipStream_t st) {
 hipError_t launch_rope(RopeParams p, hipStream_t st) {
   const int lph = p.D <= 64 ? 4 : p.D <= 128 ? 8 : p.D <= 256 ? 16 : 32, hpw = kWave / lph;
   const int head_blocks = (p.H + p.KV + p.NV + hpw - 1) / hpw;
-  p.per = 1;
-  p.parts = (head_blocks + p.per - 1) / p.per;
+  // Where there are more waves than the chip holds (8 on each of 1024 SIMDs), a
+  // wave takes up to three blocks of heads, for which a lane's angles are the same;
+  // fewer rows want the waves.  One, two, three, six blocks a wave, 48 heads of 128:
+  // 9101 rows 48.8, 44.0, 43.4, 42.6 us, some 2400 17.8, 16.7, 16.4, 19.0, 300 8.0, 8.9,
+  // 9.6, 12.4, 138 6.6, 7.7, 9.1, 12.0 (48 heads of 256 110.7, 100.8, 100.5, 102.5).
+  p.parts = p.rows * head_blocks >= 8192 ? (head_blocks + 2) / 3 : head_blocks;
+  p.per = (head_blocks + p.parts - 1) / p.parts;
   const int64_t blocks = (p.rows * p.parts + kRoWaves - 1) / kRoWaves;
   return p.bf16 ? launch_rope_type<true>(p, lph, (int)blocks, st) : launch_rope_type<false>(p, lph, (int)blocks, st);
 }

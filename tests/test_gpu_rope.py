@@ -89,6 +89,31 @@ def test_one_norm_only_and_none_of_the_rows(sv):
     assert o["q"].shape == (0, 4, 64)
 
 
+@pytest.mark.parametrize("N,H,KV,D,quant", [(2100, 20, 5, 128, None), (2101, 30, 5, 128, None), (4200, 3, 1, 512, None), (8192, 3, 2, 64, None),
+                                            (2100, 28, 4, 128, cu.E4M3), (2740, 17, 3, 128, cu.INT8)])
+def test_many_rows_are_as_few(sv, N, H, KV, D, quant):
+    """Thousands of rows (a wave takes several blocks of heads) are what a hundred
+    at a time are, bit for bit, as tensors and in a cache."""
+    qkv, pos, f, w = _case(N, H, KV, D, D, torch.bfloat16, 40, True)
+    q, k, v = _parts(qkv.cuda(), H, KV)
+    more = dict(q_weight=w[0].cuda(), k_weight=w[1].cuda())
+    f, at = f.cuda(), pos.cuda()
+    o = sv.qk_norm_rope(q, k, at, f, **more)
+    few = [sv.qk_norm_rope(q[i:i + 100], k[i:i + 100], at[i:i + 100], f, **more) for i in range(0, N, 100)]
+    assert all(torch.equal(o[n], torch.cat([x[n] for x in few])) for n in ("q", "k"))
+    caches = [sv.PagedCache(layers=1, num_pages=520, page_size=16, kv_heads=KV, head_dim=D, max_seqs=1, max_pages=520, device="cuda", quant=quant) for _ in range(2)]
+    for c in caches:
+        for t in (c.k, c.v) + (() if quant is None else (c.k_scale, c.v_scale)):
+            t.view(torch.uint8).zero_()
+    r = [c.reserve(None, _i32([N]), N)["slots"] for c in caches]
+    a = caches[0].write_rotated(0, q, k, v, r[0], at, f, **more)
+    b = [caches[1].write_rotated(0, q[i:i + 100], k[i:i + 100], v[i:i + 100], r[1][i:i + 100], at[i:i + 100], f, **more) for i in range(0, N, 100)]
+    assert torch.equal(a, torch.cat(b)) and torch.equal(a, o["q"])
+    for n in ("k", "v") if quant is None else ("k", "v", "k_scale", "v_scale"):
+        x, y = (getattr(c, n).view(torch.uint8) for c in caches)
+        assert torch.equal(x, y) and x.any()
+
+
 def test_far_positions_and_plain_norms(sv):
     """Angles of a million radians and beyond; a zero vector under a norm."""
     qkv, pos, f, w = _case(64, 2, 1, 128, 128, torch.float16, 4, True)
