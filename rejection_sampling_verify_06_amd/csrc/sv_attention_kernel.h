@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
   constexpr int VW = NJ * ES / 4;                // dwords of those
   constexpr int NL = D * ES / 64;                // 16-byte loads of a lane's part of a key
   constexpr bool kTight = C != codes::kNone && D * MT > 256;   // registers are short: the order of stages is kept
+  constexpr bool kBatchQ = C != codes::kNone || S;
   extern __shared__ uint32_t dyn[];
   const int nseq = S ? P.entries : P.B;
   uint32_t* rows = dyn;                          // not with S
@@ -442,11 +443,17 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
       const int i = rr / P.group, h = head * P.group + rr - i * P.group;
       last[m] = !in ? -1 : S && group ? x.len - 1 : x.len - n + i;
       from[m] = S ? x.first : P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
+      if constexpr (!kBatchQ) {
+        const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head + 8 * g;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if ((m * NS + s) % kAtWaves == wv) qs[m][s][lane] = *(const u32x4*)(qp + 32 * s);
+      }
     }
     // The queries: each wave brings some of the operands, all at once.  16 bytes of
     // a key are 8 numbers of one slice, or codes of two: 64 s' + 16 g .. + 15.
-    constexpr int NQ = (MT * NS + kAtWaves - 1) / kAtWaves;
-    u32x4 qr[NQ];
+    constexpr int NQ = kBatchQ ? (MT * NS + kAtWaves - 1) / kAtWaves : 0;
+    u32x4 qr[kBatchQ ? NQ : 1];
 #pragma unroll
     for (int k = 0; k < NQ; ++k) {
       const int at = min(k * kAtWaves + wv, MT * NS - 1), s = at % NS, r = at / NS * 16 + col;
