@@ -56,9 +56,9 @@
 // without branches between their products: 36 rows over int8 226 us with one
 // wave a SIMD, 134 with two; 24 and 36 rows over e4m3 85 and 124 us with branches
 // where codes without a number are looked for, which spilled, 81 and 100 without.
-// Measured: 32 sequences of 1024 to 8192, up to 24 rows, e4m3 76 + 8 us (300 MB,
+// Measured: 32 sequences of 1024 to 8192, up to 24 rows, e4m3 75 + 8 us (300 MB,
 // 4.0 TB/s), of which a tile's start and end take some 10; 98925 and 116850
-// tokens with 16 and 36 rows, int8 under float16 134 + 8 us (456 MB, 3.4 TB/s:
+// tokens with 16 and 36 rows, int8 under float16 127 + 8 us (456 MB, 3.6 TB/s:
 // products, unpacking and softmax of 36 rows take as long as the reads); 16 sequences in a
 // window of 4096, heads of 256, 28 + 6 us; one token of 777, 8 + 4 us.
 //
@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
   constexpr int VW = NJ * ES / 4;                // dwords of those
   constexpr int NL = D * ES / 64;                // 16-byte loads of a lane's part of a key
   constexpr bool kTight = C != codes::kNone && D * MT > 256;   // registers are short: the order of stages is kept
-  constexpr bool kBatchQ = C != codes::kNone || S;
   extern __shared__ uint32_t dyn[];
   const int nseq = S ? P.entries : P.B;
   uint32_t* rows = dyn;                          // not with S
@@ -443,24 +442,11 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
       const int i = rr / P.group, h = head * P.group + rr - i * P.group;
       last[m] = !in ? -1 : S && group ? x.len - 1 : x.len - n + i;
       from[m] = S ? x.first : P.window > 0 ? max(0, last[m] + 1 - P.window) : 0;
-      if constexpr (!kBatchQ) {
-        const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head + 8 * g;
+      // 16 bytes of a key are 8 numbers of one slice, or codes of two: 64 s' + 16 g .. + 15
+      const uint16_t* qp = (const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head;
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if ((m * NS + s) % kAtWaves == wv) qs[m][s][lane] = *(const u32x4*)(qp + 32 * s);
-      }
-    }
-    // The queries: each wave brings some of the operands, all at once.  16 bytes of
-    // a key are 8 numbers of one slice, or codes of two: 64 s' + 16 g .. + 15.
-    constexpr int NQ = kBatchQ ? (MT * NS + kAtWaves - 1) / kAtWaves : 0;
-    u32x4 qr[kBatchQ ? NQ : 1];
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int at = min(k * kAtWaves + wv, MT * NS - 1), s = at % NS, r = at / NS * 16 + col;
-      const int rr = mb * TM + (r < nrow ? r : 0);
-      const int i = rr / P.group, h = head * P.group + rr - i * P.group;
-      qr[k] = *(const u32x4*)((const uint16_t*)P.q + (int64_t)(row0 + i) * P.q_row + (int64_t)h * P.q_head +
-                              (ES == 2 ? 32 * s + 8 * g : 64 * (s >> 1) + 8 * (s & 1) + 16 * g));
+      for (int s = 0; s < NS; ++s)
+        if ((m * NS + s) % kAtWaves == wv) qs[m][s][lane] = *(const u32x4*)(qp + (ES == 2 ? 32 * s + 8 * g : 64 * (s >> 1) + 8 * (s & 1) + 16 * g));
     }
     f32x4 o[MT][NJ];
     float mx[MT], ls[MT];
@@ -554,8 +540,6 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
       load_k();
       load_v();
     }
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) (&qs[0][0][lane])[min(k * kAtWaves + wv, MT * NS - 1) * kWave] = qr[k];
     __syncthreads();                             // the queries are in place
     for (; pos < pos_end; pos += kUnitKeys) {
       const bool more = pos + kUnitKeys < pos_end;
