@@ -317,9 +317,11 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        // a tile in which the row saw nothing has m = -inf or l = 0
-        const float li = (wholes >> i & 1) ? 1.f : l[i];
-        if (k0 + i >= parts || m[i] == -INFINITY || li == 0.f) continue;
+        // Where the row saw nothing a part has l = 0, a whole tile m = -inf.  (A part
+        // in which all its scores are NaN has m = -inf too: its l is NaN.)
+        const bool whole = wholes >> i & 1;
+        const float li = whole ? 1.f : l[i];
+        if (k0 + i >= parts || (whole ? m[i] == -INFINITY : li == 0.f)) continue;
         const float nm = fmaxf(M, m[i]);
         const float f0 = M == nm ? 1.f : at_exp2(M - nm), f1 = m[i] == nm ? 1.f : at_exp2(m[i] - nm);
         M = nm;
