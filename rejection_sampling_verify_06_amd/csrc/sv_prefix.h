@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kPfThreads, D == 256 ? 1 : 2) k_prefix(AttnPar
   int gi = 0;
   for (int step = 4096; step > 0; step >>= 1)
     if (gi + step < P.G && (uint32_t)uni((int)units[gi + step]) <= u) gi += step;
-  const float sl = fabsf(P.scale_log2);
+  const float sl = fabsf(P.scale_log2);                              // not 0 (the host has seen to it): scores behind the prefix are -inf
   const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;       // the sign of the scale goes to the queries
   while (u < u_end) {
     while ((uint32_t)uni((int)units[gi + 1]) <= u) ++gi;
