@@ -698,8 +698,9 @@ int64_t spec_verify_codes_size(void);
  *             of 4), neighbouring tokens side by side, 16-byte aligned
  * Scores are products of q and the codes, times the key's scale; the weights
  * take the value's scale on before they are split in two bfloat16 (also for
- * SV_F16: held to 2^-16 of themselves).  A scale or code that is not a number
- * makes the rows that see it NaN, and no others.
+ * SV_F16: held to 2^-16 of themselves).  A scale or code that is not a number,
+ * or an infinite scale of a value, makes the rows that see it NaN whatever its
+ * weight, and no others; an infinite scale of a key makes its scores infinite.
  *   num_groups   0, or the number of groups of neighbouring sequences whose first
  *             tokens are the same (forks of one sequence, for instance)
  *   groups    [num_groups + 1] int32: group g is the sequences groups[g] ..

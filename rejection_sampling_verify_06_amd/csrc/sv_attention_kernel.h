@@ -585,7 +585,18 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
       const bool masked = pos + kTileKeys - 1 > min_last || pos < max_from;   // some row does not see some key
       // what the mask hides of V must not be multiplied: 0 * NaN is NaN
       bool strange = false;
+      // ones where a row of tile m sees the key, as the second product's right operand
+      auto seen = [&](int m) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kp = pos + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
+          w[i] = (kp <= last[m] && kp >= from[m] ? kOne<true> : 0u) | (kp < last[m] && kp + 1 >= from[m] ? kOne<true> << 16 : 0u);
+        }
+        return w;
+      };
       if (masked) {
+        float all = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int kp = pos + 16 * (e >> 2) + 4 * g + (e & 3);
@@ -596,8 +607,28 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
             if constexpr (C == codes::kNone) strange |= not_finite<BF>(vr[e][i]) || not_finite<BF>(vr[e][i] >> 16);
             else if constexpr (C == codes::kE4m3) strange |= nan_codes(vr[e][i]) != 0;
           }
+          if constexpr (C != codes::kNone) all = fmaf(vsc[e >> 2][e & 3], 0.f, all);
         }
-        if constexpr (C != codes::kInt8) strange = __ballot(strange) != 0;
+        strange = __ballot(strange) != 0;
+        if (C != codes::kNone && __ballot(all != 0.f)) {
+          // A value's scale that is not finite: a product of ones there with ones where a
+          // row sees the key finds the rows that do, which become NaN; the value becomes 0.
+          u32x4 marks = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int kp = pos + 16 * (e >> 2) + 4 * g + (e & 3);
+            const bool odd = (__float_as_uint(vsc[e >> 2][e & 3]) & 0x7F800000u) == 0x7F800000u;
+            vsc[e >> 2][e & 3] = odd ? 0.f : vsc[e >> 2][e & 3];
+            marks[e >> 1] |= odd && kp < x.len ? kOne<true> << (16 * (e & 1)) : 0u;
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const f32x4 d = mfma<true>(marks, seen(m), f32x4{0.f, 0.f, 0.f, 0.f});
+            const float add = d[0] != 0.f ? __builtin_nanf("") : 0.f;     // the same in all of d
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) o[m][j] += add;
+          }
+        }
       }
       u32x4 ph[MT], pl[MT];
 #pragma unroll
@@ -637,10 +668,7 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
         ls[m] += eight;
         if constexpr (C != codes::kNone) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float w = p[e] * vsc[e >> 2][e & 3];
-            p[e] = masked && s[e] == -INFINITY ? 0.f : w;   // the scale of a key that is not seen may be anything
-          }
+          for (int e = 0; e < 8; ++e) p[e] *= vsc[e >> 2][e & 3];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -695,7 +723,10 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
         }
       } else {
         if (C == codes::kE4m3 && strange) {
-          // as above, with codes that are no numbers
+          // As above, with codes that are no numbers, and all rows that see them, whatever the weight.
+          u32x4 sees[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) sees[m] = seen(m);
 #pragma unroll
           for (int c = 0; c < VW; ++c) {
             uint32_t w[8];
@@ -704,15 +735,14 @@ __global__ void __launch_bounds__(kAtThreads, D * MT <= 64 ? 4 : C != codes::kNo
             for (int e = 0; e < 8; ++e) {
               w[e] = nan_codes(vr[e][c]) >> 7;
               vr[e][c] &= ~(w[e] * 0xFFu);
-              w[e] *= C == codes::kE4m3 ? 0x38u : 1u;      // 1 in such places
+              w[e] *= 0x38u;                     // 1 in such places
             }
             turn_codes<C>(w, a);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                f32x4 d = mfma<true>(a[i], ph[m], f32x4{0.f, 0.f, 0.f, 0.f});
-                d = mfma<true>(a[i], pl[m], d);
+                const f32x4 d = mfma<true>(a[i], sees[m], f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[m][4 * c + i][r] += d[r] != 0.f ? __builtin_nanf("") : 0.f;
               }
