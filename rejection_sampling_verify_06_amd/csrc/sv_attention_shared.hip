@@ -317,11 +317,10 @@ __global__ void __launch_bounds__(kAtThreads) k_attention_merge(AttnParams P) {
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        // Where the row saw nothing a part has l = 0, a whole tile m = -inf.  (A part
-        // in which all its scores are NaN has m = -inf too: its l is NaN.)
-        const bool whole = wholes >> i & 1;
-        const float li = whole ? 1.f : l[i];
-        if (k0 + i >= parts || (whole ? m[i] == -INFINITY : li == 0.f)) continue;
+        if (k0 + i >= parts) continue;
+        // Nothing else is left out: where the row's weights are 0 (m = -inf) its O is 0,
+        // unless it saw a value that is not finite, and where its scores are all NaN l is.
+        const float li = !(wholes >> i & 1) ? l[i] : m[i] == -INFINITY ? 0.f : 1.f;
         const float nm = fmaxf(M, m[i]);
         const float f0 = M == nm ? 1.f : at_exp2(M - nm), f1 = m[i] == nm ? 1.f : at_exp2(m[i] - nm);
         M = nm;

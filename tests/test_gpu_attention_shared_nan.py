@@ -65,3 +65,32 @@ def test_runs_of_keys(sv, shape, D, quant, dtype):  # noqa: F811
             gone = torch.zeros(N, 8, dtype=torch.bool)
             gone[rows] = True
             _check(sv, (pools, *made[1:]), nd, q, ref, dtype, gone)
+
+
+@pytest.mark.parametrize("quant,dtype", [x for x in KINDS if x[0] is not None])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
+def test_values_of_weight_0(sv, shape, D, quant, dtype):  # noqa: F811
+    """128 keys with scores of -inf, for all rows, in front of value scales that are NaN: rows that see them are NaN, their lse is not."""
+    groups, nd = shape
+    made = cu.make_shared(groups, 16, 2, D, dtype, quant, 43)
+    N, first = sum(nd) + len(nd), sum(n + 1 for n in nd[:len(groups[0][1])])
+    q = _q(N, 8, D, dtype, 43)
+    q[:, :, 0] = -8.0
+    b = len(groups[0][1])
+    for seq, start, rows in ((0, 256, slice(0, first)), (b, 384, slice(first, first + nd[b] + 1))):
+        pools, ref = [x.clone() for x in made[0]], [x.clone() for x in made[1]]
+        pages = made[2][seq, start // 16:start // 16 + 8].long()
+        codes = pools[0].view(torch.uint8)
+        codes[pages] = 0
+        codes[pages, :, :, 0] = 0x38 if quant == cu.E4M3 else 1
+        pools[1][pages], pools[3][pages] = torch.inf, torch.nan
+        ref[0][pages.cpu()] = 0.0
+        ref[0][pages.cpu(), :, :, 0] = 1e9                                     # times -8: a weight of 0
+        want = su.attention_ref(q, *ref, made[2], made[3], _i32(nd))
+        for kw in ({}, dict(groups=None, prefix_len=None)):
+            o = _call(sv, q, (pools, *made[1:]), nd, **kw)
+            out, lse = o["out"].cpu(), o["lse"].cpu()
+            assert torch.isnan(out[rows]).all() and not o["status"].any()
+            out[rows] = want[0].to(dtype)[rows]
+            _near({"out": out, "lse": lse}, want, dtype)
