@@ -701,8 +701,8 @@ int64_t spec_verify_codes_size(void);
  * SV_F16: held to 2^-16 of themselves).  A scale or code that is not a number,
  * or an infinite scale of a value, makes the rows that see it NaN whatever its
  * weight, and no others; an infinite scale of a key makes its scores infinite.
- *   num_groups   0, or the number of groups of neighbouring sequences whose first
- *             tokens are the same (forks of one sequence, for instance)
+ *   num_groups   0, or the number (at most batch) of groups of neighbouring sequences
+ *             whose first tokens are the same (forks of one sequence, for instance)
  *   groups    [num_groups + 1] int32: group g is the sequences groups[g] ..
  *             groups[g + 1] - 1, together 0 .. batch - 1 (a group may be empty)
  *   prefix_len   [num_groups] int32: how many tokens its sequences share (0:

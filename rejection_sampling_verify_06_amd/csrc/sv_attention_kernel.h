@@ -56,11 +56,11 @@
 // without branches between their products: 36 rows over int8 226 us with one
 // wave a SIMD, 134 with two; 24 and 36 rows over e4m3 85 and 124 us with branches
 // where codes without a number are looked for, which spilled, 81 and 100 without.
-// Measured: 32 sequences of 1024 to 8192, up to 24 rows, e4m3 75 + 8 us (300 MB,
-// 4.0 TB/s), of which a tile's start and end take some 10; 98925 and 116850
-// tokens with 16 and 36 rows, int8 under float16 127 + 8 us (456 MB, 3.6 TB/s:
+// Measured: 32 sequences of 1024 to 8192, up to 24 rows, e4m3 68 + 7 us (300 MB,
+// 4.4 TB/s), of which a tile's start and end take some 10; 98925 and 116850
+// tokens with 16 and 36 rows, int8 under float16 116 + 8 us (456 MB, 3.9 TB/s:
 // products, unpacking and softmax of 36 rows take as long as the reads); 16 sequences in a
-// window of 4096, heads of 256, 28 + 6 us; one token of 777, 8 + 4 us.
+// window of 4096, heads of 256, 28 + 5 us; one token of 777, 8 + 4 us.
 //
 // With shared prefixes (S) the kernel's entries are groups, whose rows are those
 // of all members and whose keys are the prefix, and sequences, whose keys begin

@@ -13,11 +13,11 @@
 //   merge    of all that belongs to a row
 //
 // Measured on one MI355X (rocprofv3, plan + prefix + tiles + merge): 4 branches of
-// 2000 tokens 5 + 9 + 8 us; 64 sequences behind 32768 tokens 10 + 205 + 30 + 12 us
+// 2000 tokens 5 + 8 + 9 us; 64 sequences behind 32768 tokens 9 + 186 + 25 + 11 us
 // (one by one, without groups, 64 times the prefix's bytes: 1.7 ms at 5 TB/s); 8 groups
-// of 8 behind 8000 over e4m3 8 + 50 + 31 + 12 us.  Plan and merge are chains of loads: the
+// of 8 behind 8000 over e4m3 8 + 46 + 30 + 12 us.  Plan and merge are chains of loads: the
 // merge's 17 parts a row took 14 us with one load after the other, 8.5 with eight parts'
-// under way; 12 us of 64 sequences' merge are its 50 MB of parts.
+// under way; 11 us of 64 sequences' merge are its 50 MB of parts.
 
 #include "sv_prefix.h"
 

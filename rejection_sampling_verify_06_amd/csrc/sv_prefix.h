@@ -24,10 +24,12 @@
 //
 // Bound by the matrix pipes and, beside them, the issue of 308 vector instructions
 // a step.  Measured on one MI355X (rocprofv3): 64 sequences of up to 6 rows behind 32768
-// tokens, 8 key heads of 128, 200 to 214 us: 0.6 PFLOP/s of the formula's products, 0.9
-// with the split's second one (a library product of 8192^3 reaches 1.2); one
-// 16-bit weight instead of two 178, a ring of four tiles of 32 keys 218.  8
-// groups of 8 behind 8000 tokens over e4m3 50 us.
+// tokens, 8 key heads of 128, 186 us after a hundred calls, 212 among the first twenty: 0.7
+// PFLOP/s of the formula's products, 1.05 with the split's second one (a library product
+// of 8192^3 reaches 1.2); among the first twenty one 16-bit weight instead of two took
+// 178, a ring of four tiles of 32 keys 218.  8 groups of 8 behind 8000 tokens over e4m3
+// 46 us.  Over codes heads of 256 have 22 registers too many (44 bytes a lane in
+// scratch), heads of 128 two (12 bytes).
 
 #pragma once
 

@@ -18,7 +18,7 @@
 // heads, so that a lane's 8 angles serve all of them.
 //
 // Measured on one MI355X (rocprofv3): 9101 prompt rows of 32 + 8 + 8 heads of 128
-// into a 16-bit cache 41 us (224 MB, 5.5 TB/s); a round's 138 rows 5 us, a chain of
+// into a 16-bit cache 43 us (224 MB, 5.2 TB/s); a round's 138 rows 5 us, a chain of
 // loads, sines and stores.  As int8 codes a layer's 6905 rows are written in 12.5 us
 // and read back in 13 (43 MB each, 3.3 TB/s; more blocks, or 32-bit divisions, changed
 // nothing); a round's in 3.7 and 5.

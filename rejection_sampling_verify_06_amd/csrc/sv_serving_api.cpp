@@ -62,7 +62,8 @@ bool attention_shape(const char* who, const spec_verify_attention_args* a, int32
   // 134); 36 rows with 32, 48 114, 101.  One token of one sequence, 16 and 48 7
   // and 10 us.  More than 48 rows of 128 do not fit the registers (64 rows: 2
   // tiles twice 113 us, 3 tiles twice 182, 4 spilled 187), nor more than 16 of
-  // 256 (16 to 40 rows in a window of 4096: 39 us, 2 tiles spilled 63); 64 sequences
+  // 256 over 16-bit pages (16 to 40 rows in a window of 4096: 39 us, 2 tiles spilled
+  // 63; over codes, whose one tile has 226 of 256 registers, not tried); 64 sequences
   // of 4096 with 8 heads of 64: 8 rows with room for 16, 32, 64 94, 96, 96 us,
   // 64 rows with 64, 32 104, 153.
   const int64_t group = a->heads / a->kv_heads;
@@ -132,8 +133,13 @@ bool shared_shape(const char* who, const spec_verify_attention_args* a, int32_t 
   // call, k_attention and this one: 14 rows of a group and key head 55 and 60 us, 24
   // 94 and 77, 28 84 and 65, 56 106 and 77; heads of 256 28 118 and 93; but heads
   // of 64 28 47 and 51, 42 46 and 56, 56 60 and 58, e4m3 42 64 and 72, 56 88 and 79,
-  // int8 of 256 42 115 and 138, 84 186 and 155.  One group behind 2000 tokens is
-  // latency alone: 32 rows 26 and 33; behind 30000 62 and 62.
+  // int8 of 256 42 115 and 138, 52 189 and 180, 60 172 and 177, 72 269 and 233, 84 283
+  // and 229 (52 rows on: with longer own parts).  Short prefixes pay for the launch
+  // whatever their rows, which the rule does not look at: 8 groups behind 500 or 2000
+  // tokens, 52 to 256 rows, 58 to 258 us and 62 to 279 (behind 130 69 to 318 and 63
+  // to 248); one group behind 130 to 2000 is latency alone, 52 rows 23 to 26 and 27 to
+  // 31, 256 29 to 38 and 30 to 42; behind 8000 52 rows 41 and 49, 128 53 and 53, 256 82
+  // and 53; behind 30000 32 rows 62 and 62.
   s->many = avg > 48 || (codes == SV_CODES_NONE && a->head_dim >= 128 && avg > 16 && units >= 2048);
   s->tiles = s->many ? own : s->together;
   s->prefix_blocks = s->many ? (int)std::min<int64_t>(units, a->head_dim == 256 ? 256 : 512) : 0;
