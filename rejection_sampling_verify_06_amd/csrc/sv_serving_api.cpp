@@ -547,19 +547,16 @@ int spec_verify_paged_attention_options(const spec_verify_attention_args* a, con
     p.G = l.groups;
     p.groups = o->groups;
     p.prefix_len = o->prefix_len;
-    // the kernel for many rows takes strides in bytes in 32 bits
+    // The kernel for many rows takes strides in bytes in 32 bits; and its scores take
+    // the scale on behind the mask, where a scale of 0 makes 0 * -inf.  (Scores scaled
+    // in front of it cost 0.7 to 1 % of a long prefix's time: its registers are all in use.)
     const int64_t es = codes == SV_CODES_NONE ? 2 : 1;
     const int64_t most = std::max(std::max(a->k_page_stride, a->v_page_stride), a->page_size * std::max(a->k_token_stride, a->v_token_stride));
-    if (l.many && most * es > UINT32_MAX) {
+    if (l.many && (most * es > UINT32_MAX || p.scale_log2 == 0.f)) {
       l.many = false;
       l.tiles = l.together;
       p.prefix_parts = p.parts;
     }
-    // That kernel's scores take the scale on behind the mask, and 0 * -inf is NaN: a
-    // scale of 0 is taken as the smallest float above it, under which scores of up to
-    // 2^128 are below 2^-21 and weights 1 to their last bit or two.  (In the kernel,
-    // whose registers are all in use, this costs 0.7 to 1 % of a long prefix's time.)
-    if (l.many && p.scale_log2 == 0.f) p.scale_log2 = 0x1p-149f;
     p.own_rows = 16 * l.tiles.row_tiles;
     p.prefix_rows = l.many ? sv::kAttnPrefixRows : p.own_rows;
     p.prefix_blocks = l.prefix_blocks;
